@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
 
@@ -27,7 +27,12 @@ __all__ = [
     "tsel_keep_count", "tsel_read_device_status", "tsel_clear_device_status",
     "tsel_importance_redo_pairs", "tsel_select_path_counts", "tsel_importance_one_launch",
     "tsel_status_string", "tsel_last_error", "tsel_probe_ex2",
+    "tsel_rope_frequencies", "tsel_rope_table", "tsel_rope",
+    "TselCache", "tsel_cache_new", "tsel_cache_workspace_size", "tsel_cache_write", "tsel_cache_read",
+    "tsel_prefix_attention_workspace_size", "tsel_prefix_attention",
+    "TSEL_ROPE_ADJACENT", "TSEL_ROPE_INVERSE", "TSEL_ROPE_SECTIONED", "TSEL_ROPE_INTERLEAVED", "TSEL_ROPE_PER_AXIS",
     "TSEL_DEV_SEQLENS", "TSEL_DEV_REQUESTS", "TSEL_DEV_KEEP_IDX", "TSEL_DEV_TIMEOUT", "TSEL_DEV_NAN",
+    "TSEL_DEV_PAGES", "TSEL_DEV_POSITIONS",
     "TSEL_IMP_LSE_PROVIDED", "TSEL_IMP_FP8_E4M3", "TSEL_IMP_SCORE_SUM", "TSEL_IMP_ROWREF_FIXED", "TSEL_IMP_ROWREF_MOVING", "TSEL_IMP_TWO_PASS", "TSEL_IMP_TEST_STALL", "TSEL_IMP_STAGE_PREP", "TSEL_IMP_STAGE_PASS1", "TSEL_IMP_STAGE_PASS2",
 ]
 
@@ -43,6 +48,8 @@ TSEL_DEV_REQUESTS = 0x2
 TSEL_DEV_KEEP_IDX = 0x4
 TSEL_DEV_TIMEOUT = 0x8
 TSEL_DEV_NAN = 0x10
+TSEL_DEV_PAGES = 0x20
+TSEL_DEV_POSITIONS = 0x40
 
 TSEL_KEEP_FROM_DEVICE = -1
 
@@ -57,6 +64,14 @@ TSEL_IMP_STAGE_PREP = 0x100
 TSEL_IMP_STAGE_PASS1 = 0x200
 TSEL_IMP_STAGE_PASS2 = 0x400
 TSEL_SEL_STAGE_TOPK = 0x800
+
+TSEL_ROPE_ADJACENT = 0x1
+TSEL_ROPE_INVERSE = 0x2
+TSEL_ROPE_SECTIONED = 0
+TSEL_ROPE_INTERLEAVED = 1
+TSEL_ROPE_PER_AXIS = 2
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # TSEL_BF16, _FP16, _FP32
 
 _c_int, _c_i64, _c_size, _c_float, _c_uint, _p = (ctypes.c_int, ctypes.c_int64, ctypes.c_size_t,
                                                    ctypes.c_float, ctypes.c_uint, ctypes.c_void_p)
@@ -96,6 +111,21 @@ _SIGNATURES = {
     "tsel_importance_noalloc": (_c_int, [_p, _c_i64, _p, _c_i64, _p, _p, _c_int, _c_int, _c_int,
                                          _c_int, _c_int, _c_int, _c_int, _c_int, _c_float, _p, _p,
                                          _p, _p]),
+    "tsel_rope_frequencies": (_c_int, [ctypes.c_double, _p, _c_int, _c_int, _p, _p]),
+    "tsel_rope_table": (_c_int, [_p, _p, _c_int, _p]),
+    "tsel_cache_workspace_size": (_c_size, []),
+    "tsel_rope": (_c_int, [_p, _c_i64, _p, _c_i64, _p, _c_int, _p, _c_int, _c_int, _c_int, _c_int,
+                           _c_int, _c_int, _c_uint, _p, _c_i64, _p, _c_i64, _p, _c_size, _p]),
+    "tsel_cache_write": (_c_int, [_p, _c_i64, _p, _c_i64, _p, _c_int, _p, _c_int, _p, _c_int,
+                                  _c_int, _c_int, _c_int, _c_uint, _p, _p, _p, _p, _c_int, _c_int,
+                                  _p, _c_size, _p]),
+    "tsel_cache_read": (_c_int, [_p, _p, _p, _p, _c_int, _c_int, _p, _c_int, _c_int, _c_int,
+                                 _c_int, _p, _c_i64, _p, _c_i64, _p, _c_size, _p]),
+    "tsel_prefix_attention_workspace_size": (_c_size, [_c_int] * 8),
+    "tsel_prefix_attention": (_c_int, [_p, _c_i64, _p, _c_int, _c_int, _c_int, _p, _p, _p, _p,
+                                       _c_int, _c_int, _p, _p, _c_int, _p, _c_i64, _p, _c_int,
+                                       _c_int, _c_int, _c_int, _c_int, _c_float, _p, _c_i64, _p,
+                                       _p, _c_size, _p]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -491,6 +521,289 @@ def tsel_gather_compact_counted(hidden: torch.Tensor, pos: Optional[torch.Tensor
         _ptr(out_cu_seqlens), _ptr(workspace), workspace.numel(), _stream(stream, dev))
     _check(st)
     return out_hidden, out_pos, out_img_id, out_cu_seqlens
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions with several axes
+# ---------------------------------------------------------------------------
+
+def _rows(t: torch.Tensor, name: str, device=None, dtype=None, shape=None) -> int:
+    """Checks a [rows, heads, head_dim] tensor; returns its row stride."""
+    if not t.is_cuda or t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be a CUDA bf16, fp16 or fp32 tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be a [rows, heads, head_dim] tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    n, h, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name} must have contiguous [heads, head_dim] rows")
+    return t.stride(0) if n > 1 else 0
+
+
+def _vector(t: torch.Tensor, dtype, name: str, device, numel: Optional[int] = None) -> None:
+    _need(t, dtype, name)
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if numel is not None and t.numel() != numel:
+        raise ValueError(f"{name} must have {numel} entries")
+
+
+def _rope_args(pos, table, total: int, device):
+    """(pos pointer, pos_dim, table pointer, pairs) of a rotation."""
+    if table is None:
+        return None, 0, None, 0
+    if pos is None:
+        raise ValueError("a rope table needs positions")
+    _vector(pos, torch.int32, "pos", device)
+    if pos.dim() != 2 or pos.shape[0] != total:
+        raise ValueError("pos must be an int32 [tokens, axes] tensor")
+    _vector(table, torch.int64, "table", device)
+    return pos.data_ptr(), pos.shape[1], table.data_ptr(), table.numel()
+
+
+def _workspace(workspace: Optional[torch.Tensor], nbytes: int, device) -> torch.Tensor:
+    if workspace is None:
+        return _new_workspace(nbytes, device)
+    if workspace.device != device:
+        raise ValueError(f"workspace must be on {device}")
+    return workspace
+
+
+def tsel_rope_frequencies(base: float, sections: Sequence[int],
+                          layout: int = TSEL_ROPE_SECTIONED) -> Tuple[list, list]:
+    """Frequencies (radians per position step) and axes of the rotated pairs, axis a
+    having sections[a] of them; see tsel_rope_frequencies in include/tsel.h."""
+    n = len(sections)
+    pairs = max(sum(max(int(x), 0) for x in sections), 1)
+    sec = (ctypes.c_int32 * max(n, 1))(*[int(x) for x in sections])
+    freq, axis = (ctypes.c_double * pairs)(), (ctypes.c_int32 * pairs)()
+    _check(load_library().tsel_rope_frequencies(float(base), sec, n, int(layout), freq, axis))
+    total = sum(int(x) for x in sections)
+    return list(freq)[:total], list(axis)[:total]
+
+
+def tsel_rope_table(inv_freq: Sequence[float], axis: Sequence[int], device="cuda") -> torch.Tensor:
+    """The device table (int64 [pairs]) of a rotation, built once from its
+    frequencies and axes (tsel_rope_frequencies, or any others)."""
+    n = len(inv_freq)
+    if len(axis) != n:
+        raise ValueError("inv_freq and axis must have the same length")
+    freq = (ctypes.c_double * max(n, 1))(*[float(x) for x in inv_freq])
+    ax = (ctypes.c_int32 * max(n, 1))(*[int(x) for x in axis])
+    table = torch.empty(n, dtype=torch.int64)
+    _check(load_library().tsel_rope_table(freq, ax, n, _ptr(table) if n else None))
+    return table.to(device)
+
+
+def tsel_rope(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, table: torch.Tensor, *,
+              flags: int = 0, q_out: Optional[torch.Tensor] = None,
+              k_out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+              stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Rotates q [T, H, d] and k [T, Hkv, d] (or None) by positions pos int32 [T, axes];
+    returns (q_out, k_out), which may be q and k themselves. With
+    TSEL_ROPE_INVERSE it turns gradients of the outputs into those of the inputs."""
+    dev = q.device
+    total, H, d = q.shape if q.dim() == 3 else (0, 0, 0)
+    qs = _rows(q, "q")
+    Hkv = ks = 0
+    if k is not None:
+        Hkv = k.shape[1] if k.dim() == 3 else 0
+        ks = _rows(k, "k", dev, q.dtype, (total, Hkv, d))
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    pos_p, pos_dim, table_p, pairs = _rope_args(pos, table, total, dev)
+    qos = 0 if q_out is None else _rows(q_out, "q_out", dev, q.dtype, (total, H, d))
+    kos = 0 if k_out is None else _rows(k_out, "k_out", dev, q.dtype, (total, Hkv, d))
+    if q_out is None:
+        q_out = torch.empty((total, H, d), dtype=q.dtype, device=dev)
+    if k is not None and k_out is None:
+        k_out = torch.empty((total, Hkv, d), dtype=q.dtype, device=dev)
+    workspace = _workspace(workspace, 1024, dev)
+    with torch.cuda.device(dev):
+        st = load_library().tsel_rope(
+            q.data_ptr(), qs, _ptr(k), ks, pos_p, pos_dim, table_p, pairs, total, H, Hkv, d,
+            _DTYPES[q.dtype], int(flags), q_out.data_ptr(), qos, _ptr(k_out), kos,
+            workspace.data_ptr(), workspace.numel(), _stream(stream, dev))
+    _check(st)
+    return q_out, k_out
+
+
+# ---------------------------------------------------------------------------
+# Quantised paged cache
+# ---------------------------------------------------------------------------
+
+class TselCache(NamedTuple):
+    """A paged cache: E4M3 codes uint8 [pages, Hkv, page_size, d] and scale
+    exponents uint8 [pages, Hkv, page_size] of K and V."""
+    k_pages: torch.Tensor
+    v_pages: torch.Tensor
+    k_exps: torch.Tensor
+    v_exps: torch.Tensor
+
+
+def tsel_cache_new(num_pages: int, page_size: int, num_kv_heads: int, head_dim: int,
+                   device="cuda") -> TselCache:
+    """A zeroed cache."""
+    shape = (int(num_pages), int(num_kv_heads), int(page_size))
+    codes = [torch.zeros(shape + (int(head_dim),), dtype=torch.uint8, device=device) for _ in range(2)]
+    return TselCache(*codes, *[torch.zeros(shape, dtype=torch.uint8, device=device) for _ in range(2)])
+
+
+def _cache_args(cache: TselCache, device):
+    """(pointers and sizes of the C calls, Hkv, d) of a cache."""
+    shape = cache.k_pages.shape
+    if len(shape) != 4:
+        raise ValueError("k_pages must be a uint8 [pages, heads, page_size, head_dim] tensor")
+    for name in TselCache._fields:
+        t = getattr(cache, name)
+        _vector(t, torch.uint8, name, device)
+        if tuple(t.shape) != tuple(shape if name.endswith("pages") else shape[:3]):
+            raise ValueError(f"{name} does not match k_pages")
+    return ([t.data_ptr() for t in cache], shape[0], shape[2]), shape[1], shape[3]
+
+
+def tsel_cache_workspace_size() -> int:
+    return int(load_library().tsel_cache_workspace_size())
+
+
+def tsel_cache_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cache: TselCache, *,
+                     pos: Optional[torch.Tensor] = None, table: Optional[torch.Tensor] = None,
+                     flags: int = 0, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Quantises k and v [T, Hkv, d] into the cache's slots (int32 [T], negative:
+    skipped); with a rope table and positions k is rotated on its way."""
+    dev = k.device
+    ks = _rows(k, "k")
+    total, Hkv, d = k.shape
+    vs = _rows(v, "v", dev, k.dtype, (total, Hkv, d))
+    (ptrs, pages, page_size), ch, cd = _cache_args(cache, dev)
+    if (ch, cd) != (Hkv, d):
+        raise ValueError("k and v do not match the cache's heads and head_dim")
+    _vector(slots, torch.int32, "slots", dev, total)
+    pos_p, pos_dim, table_p, pairs = _rope_args(pos, table, total, dev)
+    workspace = _workspace(workspace, 1024, dev)
+    with torch.cuda.device(dev):
+        st = load_library().tsel_cache_write(
+            k.data_ptr(), ks, v.data_ptr(), vs, pos_p, pos_dim, table_p, pairs, slots.data_ptr(),
+            total, Hkv, d, _DTYPES[k.dtype], int(flags), *ptrs, pages, page_size,
+            workspace.data_ptr(), workspace.numel(), _stream(stream, dev))
+    _check(st)
+
+
+def tsel_cache_read(cache: TselCache, slots: torch.Tensor, *, dtype=torch.bfloat16,
+                    k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None,
+                    stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Reads slots (int32 [T], negative: zeros) back as k and v [T, Hkv, d] of dtype."""
+    dev = cache.k_pages.device
+    (ptrs, pages, page_size), Hkv, d = _cache_args(cache, dev)
+    _vector(slots, torch.int32, "slots", dev)
+    if dtype not in _DTYPES:
+        raise TypeError("dtype must be bf16, fp16 or fp32")
+    shape = (slots.numel(), Hkv, d)
+    kos = 0 if k_out is None else _rows(k_out, "k_out", dev, dtype, shape)
+    vos = 0 if v_out is None else _rows(v_out, "v_out", dev, dtype, shape)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=dev)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=dev)
+    workspace = _workspace(workspace, 1024, dev)
+    with torch.cuda.device(dev):
+        st = load_library().tsel_cache_read(
+            *ptrs, pages, page_size, slots.data_ptr(), shape[0], Hkv, d, _DTYPES[dtype],
+            k_out.data_ptr(), kos, v_out.data_ptr(), vos, workspace.data_ptr(), workspace.numel(),
+            _stream(stream, dev))
+    _check(st)
+    return k_out, v_out
+
+
+# ---------------------------------------------------------------------------
+# Attention over a shared prefix
+# ---------------------------------------------------------------------------
+
+def tsel_prefix_attention_workspace_size(num_req: int, total_q: int, max_seqlen_q: int,
+                                         num_heads: int, num_kv_heads: int, head_dim: int,
+                                         max_prefix_len: int, max_suffix_len: int) -> int:
+    return int(load_library().tsel_prefix_attention_workspace_size(
+        int(num_req), int(total_q), int(max_seqlen_q), int(num_heads), int(num_kv_heads),
+        int(head_dim), int(max_prefix_len), int(max_suffix_len)))
+
+
+def tsel_prefix_attention(q: torch.Tensor, cu_seqlens_q: torch.Tensor, max_seqlen_q: int,
+                          cache: TselCache, prefix_pages: Optional[torch.Tensor],
+                          prefix_len: Optional[torch.Tensor], max_prefix_len: int,
+                          page_table: Optional[torch.Tensor], suffix_lens: Optional[torch.Tensor],
+                          max_suffix_len: int, *, softmax_scale: float = 0.0,
+                          out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                          want_lse: bool = True, workspace: Optional[torch.Tensor] = None,
+                          stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Attention of a batch over a prefix that all requests share and each one's own
+    suffix, both in the cache; returns (out [Tq, H, d], lse fp32 [H, Tq] or None).
+
+    q bf16 or fp16 [Tq, H, d]; cu_seqlens_q int32 [R+1]; prefix_pages int32 and
+    prefix_len int32 [1] (None with max_prefix_len 0); page_table int32
+    [R, pages] and suffix_lens int32 [R] (None with max_suffix_len 0). A
+    request's last query rows are its last suffix tokens (causal). Rows past
+    cu_seqlens_q[R] are left as they are in a given out or lse."""
+    dev = q.device
+    qs = _rows(q, "q")
+    if q.dtype == torch.float32:
+        raise TypeError("q must be bf16 or fp16")
+    tq, H, d = q.shape
+    (ptrs, pages, page_size), Hkv, cd = _cache_args(cache, dev)
+    if cd != d:
+        raise ValueError("q does not match the cache's head_dim")
+    _vector(cu_seqlens_q, torch.int32, "cu_seqlens_q", dev)
+    R = cu_seqlens_q.numel() - 1
+    if R < 0:
+        raise ValueError("cu_seqlens_q must have at least one entry")
+    max_p, max_s = int(max_prefix_len), int(max_suffix_len)
+    if max_p > 0:
+        if prefix_pages is None or prefix_len is None:
+            raise ValueError("max_prefix_len > 0 needs prefix_pages and prefix_len")
+        _vector(prefix_pages, torch.int32, "prefix_pages", dev)
+        _vector(prefix_len, torch.int32, "prefix_len", dev, 1)
+        if prefix_pages.numel() * page_size < max_p:
+            raise ValueError("prefix_pages holds fewer than max_prefix_len keys")
+    table_stride = 0
+    if max_s > 0 and R > 0:
+        if page_table is None or suffix_lens is None:
+            raise ValueError("max_suffix_len > 0 needs page_table and suffix_lens")
+        _need(page_table, torch.int32, "page_table")
+        if page_table.device != dev:
+            raise ValueError(f"page_table must be on {dev}")
+        if page_table.dim() != 2 or page_table.shape[0] != R or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+            raise ValueError("page_table must be an int32 [requests, pages] tensor with contiguous rows")
+        if page_table.shape[1] * page_size < max_s:
+            raise ValueError("page_table rows hold fewer than max_suffix_len keys")
+        table_stride = page_table.stride(0) if R > 1 else page_table.shape[1]
+        _vector(suffix_lens, torch.int32, "suffix_lens", dev, R)
+    os_ = 0 if out is None else _rows(out, "out", dev, q.dtype, (tq, H, d))
+    if lse is not None:
+        _vector(lse, torch.float32, "lse", dev, H * tq)
+    if workspace is not None and workspace.device != dev:
+        raise ValueError(f"workspace must be on {dev}")
+    if out is None:
+        out = torch.empty((tq, H, d), dtype=q.dtype, device=dev)
+    if lse is None and want_lse:
+        lse = torch.empty((H, tq), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = _new_workspace(tsel_prefix_attention_workspace_size(R, tq, max_seqlen_q, H, Hkv, d, max_p, max_s), dev)
+    with torch.cuda.device(dev):
+        st = load_library().tsel_prefix_attention(
+            q.data_ptr(), qs, cu_seqlens_q.data_ptr(), R, tq, int(max_seqlen_q), *ptrs, pages, page_size,
+            _ptr(prefix_pages) if max_p > 0 else None, _ptr(prefix_len) if max_p > 0 else None, max_p,
+            _ptr(page_table) if table_stride else None, table_stride, _ptr(suffix_lens) if table_stride else None,
+            max_s, H, Hkv, d, _DTYPES[q.dtype], float(softmax_scale), out.data_ptr(), os_, _ptr(lse),
+            workspace.data_ptr(), workspace.numel(), _stream(stream, dev))
+    _check(st)
+    return out, lse
 
 
 # ---------------------------------------------------------------------------

@@ -1,0 +1,785 @@
+// Attention of a batch of requests over a prefix that all of them share (the
+// kept tokens of the images they ask about) and each one's own suffix, read
+// from the quantised paged cache (kvcache.cu).
+//
+// o_i = sum_j p_ij v_j / sum_j p_ij with p_ij = exp(s q_i . k_j) over the
+// prefix and the suffix keys that row i sees. LiteVLM review, "core formulas"
+// (softmax(Q K^T / sqrt d) V); the pruned sequence in the KV cache: dynamic
+// vision-token compression article, section 3.2.
+//
+// The prefix is read once for all rows, not once per request: the rows of every
+// request and of the query heads that share a KV head form one matrix, cut into
+// 128-row tiles. The keys are cut into chunks so that few rows still fill the
+// device. A unit is (KV head, one or two row tiles, key chunk); a request's
+// suffix is units of the same kind with its own rows. Each unit writes a
+// normalised partial result and its log-sum-exp, and a second launch joins a
+// row's partials in chunk order (deterministic: no atomics).
+//
+// Per 128-key tile of a unit:
+//   - converter warps load the E4M3 codes (16 bytes per lane, one tile ahead in
+//     registers), turn them into fp16 — exact, with the row's power-of-two
+//     scale relative to the tile's largest folded into one multiplication — and
+//     store them to 128-byte-swizzled shared memory: K rows as the K-major B
+//     operand of S = Q K^T, V rows as the MN-major B operand of O = P V.
+//   - one thread per row tile issues both products (tcgen05, kind::f16, fp32
+//     accumulators in TMEM: 128 columns of S and up to 128 of O per row tile).
+//   - four softmax warps per row tile, one row per thread: the running maximum
+//     follows the row when it is exceeded by more than 2^5 (O is then rescaled
+//     in TMEM), P = exp2(S - m + 10) in fp16 overwrites S in TMEM and is the A
+//     operand of the second product.
+// fp16 throughout: q rows are scaled by a power of two so that their largest
+// element is near 2^13 (bf16's eight bits fit, elements below 2^-27 of the
+// largest lose bits), codes have four bits, and P keeps eleven bits down to
+// 2^-24 of the row's maximum. V keeps its codes exactly while a row's scale is
+// within 2^-20 of the largest scale so far in its chunk, K while within 2^-22
+// of its tile's largest; smaller rows are rounded on that grid.
+//
+// Masked keys never reach a result: V rows past the last visible key of a tile
+// are zeros whatever the page holds, S of masked keys is replaced, not added
+// to, and a row stored as NaN (scale byte 255) enters through S (K) or P (V) of
+// the rows that see it only.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "attend.cuh"
+#include "imp_pass.cuh"
+
+namespace tsel {
+
+namespace {
+
+constexpr int kAttMetaRing = 4;
+constexpr float kAttLift = 10.f;      // P = 2^10 at the row's reference
+constexpr float kAttSlack = 5.f;      // the reference may lag the row maximum by 2^5
+constexpr int kAttVSlack = 2;         // a moved V reference leaves room for 2^2 larger scales
+
+struct AttTileMeta {
+  float k_scale;       // 2^(tile's K reference - 7)
+  int v_ref;           // exponent byte of the V reference
+  uint32_t v_nan[4];   // keys whose V row is NaN, a bit each
+};
+
+template <int D, int NT>
+struct AttCfg {
+  static constexpr int DC = D > 64 ? 2 : 1;                 // 64-element chunks of a row
+  static constexpr int TILE_BYTES = DC * kTile * 128;       // one 128-row fp16 operand
+  static constexpr int KS = NT;                             // K and V stages
+  static constexpr int CONV_GROUPS = NT;                    // two groups: one for K, one for V
+  static constexpr int SOFT_WARPS = 4 * NT;
+  static constexpr int MMA_WARP = SOFT_WARPS;               // NT issuing warps
+  static constexpr int CONV_WARP = MMA_WARP + NT;
+  static constexpr int WARPS = CONV_WARP + 4 * CONV_GROUPS;
+  static constexpr int THREADS = 32 * WARPS;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = NT * TILE_BYTES;
+  static constexpr int OFF_V = OFF_K + KS * TILE_BYTES;
+  static constexpr int OFF_FAC = OFF_V + KS * TILE_BYTES;   // uint32 [K, V][tile parity][128]
+  static constexpr int OFF_PAGES = OFF_FAC + 2 * 2 * kTile * 4;
+  static constexpr int OFF_META = OFF_PAGES + kAttMaxPages * 4;
+  static constexpr int NUM_BARS = 4 * KS + 3 * NT;
+  static constexpr int OFF_BAR = OFF_META + kAttMetaRing * int(sizeof(AttTileMeta));
+  static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;
+  static constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;   // + alignment slack
+  static constexpr int UPT = D / 16;                        // 16-code pieces per converter thread and tile
+  static constexpr uint32_t TMEM_COLS = 256 * NT;
+  static_assert(sizeof(AttTileMeta) % 8 == 0 && OFF_META % 8 == 0, "barrier alignment");
+  static_assert(SMEM_BYTES <= (NT == 1 ? 113 * 1024 : 227 * 1024), "shared memory");
+};
+
+// Shared-memory descriptor of an MN-major operand with the 128-byte swizzle:
+// 64 elements contiguous along MN, rows of 128 bytes along K in groups of
+// eight. lbo: bytes to the next 64 elements along MN; sbo: to the next eight
+// rows along K.
+__device__ __forceinline__ uint64_t smem_desc_mn(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  uint64_t d = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// Instruction descriptor of kind::f16: fp16 A and B, fp32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
+  return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | (uint32_t(N >> 3) << 17) |
+         (uint32_t(M >> 4) << 24);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem].
+__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Two fp32 values as fp16 (x in the low half).
+__device__ __forceinline__ uint32_t pack_f16(float x, float y) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+  return r;
+}
+
+// Two E4M3 codes times a power of two, as fp16.
+__device__ __forceinline__ uint32_t unpack_e4m3(uint32_t two, uint32_t factor) {
+  uint32_t r;
+  asm("{\n\t.reg .b32 t;\n\t"
+      "cvt.rn.f16x2.e4m3x2 t, %1;\n\t"
+      "mul.rn.f16x2 %0, t, %2;\n\t}"
+      : "=r"(r)
+      : "h"(uint16_t(two)), "r"(factor));
+  return r;
+}
+
+// 2^(7 + exp - ref) in both fp16 halves (exp <= ref): codes of the largest
+// row reach 448 * 2^7.
+__device__ __forceinline__ uint32_t att_factor(int exp, int ref) {
+  const int n = 7 + exp - ref;
+  const uint32_t f = n >= -14 ? uint32_t(n + 15) << 10 : (n >= -24 ? 1u << (n + 24) : 0u);
+  return f | (f << 16);
+}
+
+// Largest of four exponent bytes that are not 255.
+__device__ __forceinline__ uint32_t max_byte(uint32_t w) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t b = (w >> (8 * i)) & 0xFFu;
+    m = max(m, b == 255u ? 0u : b);
+  }
+  return m;
+}
+
+// What a CTA works on: rows [tok0 + x * tt, ...) of KV head kvh for row tile
+// x, keys [k0, k1) of a page list.
+struct AttUnit {
+  int kvh, slot;
+  int tok0, tok_end;     // first token of row tile 0; one past the last token
+  int k0, k1;            // keys, in the coordinates of the page list
+  int lim0;              // keys the token tok_first sees; one more for each later token (suffix)
+  int tok_first;
+  int causal;
+  const int32_t* pages;
+  bool bad;
+};
+
+__device__ __forceinline__ AttUnit att_unit(const AttParams& p, int nt, int64_t u) {
+  AttUnit w{};
+  if (u < p.units_p) {
+    const int g = int(u % p.ntg);
+    const int64_t ch = u / p.ntg;
+    w.kvh = int(ch % p.Hkv);
+    const int c = int(ch / p.Hkv);
+    w.slot = c;
+    int n = __ldg(p.prefix_len);
+    const int rows = __ldg(p.cu_q + p.R);
+    w.bad = n < 0 || n > p.max_prefix || rows < 0 || rows > p.Tq;
+    if (w.bad) return w;
+    w.tok0 = g * nt * p.tt;
+    w.tok_end = rows;
+    w.k0 = min(c * p.lp, n);
+    w.k1 = min(w.k0 + p.lp, n);
+    w.lim0 = n;
+    w.pages = p.prefix_pages;
+  } else {
+    u -= p.units_p;
+    const int c = int(u % p.sc);
+    u /= p.sc;
+    const int qi = int(u % p.qt);
+    u /= p.qt;
+    w.kvh = int(u % p.Hkv);
+    const int r = int(u / p.Hkv);
+    w.slot = p.nc + c;
+    const int a = __ldg(p.cu_q + r), b = __ldg(p.cu_q + r + 1);
+    const int n = __ldg(p.suffix_lens + r);
+    w.bad = a < 0 || b < a || b > p.Tq || b - a > p.max_q || n < 0 || n > p.max_suffix ||
+            (r == 0 && a != 0);
+    if (w.bad) return w;
+    w.tok_first = a;
+    w.tok0 = a + qi * p.tt;
+    w.tok_end = min(b, w.tok0 + p.tt);
+    w.causal = 1;
+    w.lim0 = n - (b - a) + 1;
+    // keys past the last row's limit are seen by no row of the tile
+    const int seen = min(n, w.lim0 + (w.tok_end - 1 - a));
+    w.k0 = min(c * p.ls, max(seen, 0));
+    w.k1 = min(w.k0 + p.ls, max(seen, 0));
+    w.pages = p.page_table + r * p.table_stride;
+  }
+  return w;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(AttCfg<D, NT>::THREADS, NT == 1 ? 2 : 1)
+    attend_kernel(const AttParams p) {
+  using C = AttCfg<D, NT>;
+  extern __shared__ uint8_t smem_dyn[];
+  uint8_t* smem = smem_dyn + ((1024u - (smem_u32(smem_dyn) & 1023u)) & 1023u);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* k_full = bars;                  // [KS] K tile converted
+  uint64_t* k_free = k_full + C::KS;        // [KS] S products of the tile done
+  uint64_t* v_full = k_free + C::KS;        // [KS]
+  uint64_t* v_free = v_full + C::KS;        // [KS]
+  uint64_t* s_full = v_free + C::KS;        // [NT] S in TMEM
+  uint64_t* p_full = s_full + NT;           // [NT] P in TMEM
+  uint64_t* o_done = p_full + NT;           // [NT] O product of the tile done
+  int32_t* s_pages = reinterpret_cast<int32_t*>(smem + C::OFF_PAGES);
+  AttTileMeta* s_meta = reinterpret_cast<AttTileMeta*>(smem + C::OFF_META);
+  uint32_t* s_fac = reinterpret_cast<uint32_t*>(smem + C::OFF_FAC);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t T = p.timeout_ns;
+  pdl_wait();   // every input may come from an earlier kernel
+  const AttUnit w = att_unit(p, NT, p.unit0 + blockIdx.x);
+  if (w.bad) {
+    pdl_launch_dependents();
+    if (threadIdx.x == 0) set_status(p.status, TSEL_DEV_SEQLENS);
+    return;
+  }
+  // row tiles with a row
+  const int nact = NT == 2 && w.tok0 + p.tt < w.tok_end ? 2 : (w.tok0 < w.tok_end ? 1 : 0);
+  if (nact == 0) {
+    pdl_launch_dependents();
+    return;
+  }
+  const int tiles = int(ceil_div(w.k1 - w.k0, kTile));
+
+  // Thread r < 128 * NT of the softmax warps owns row r % 128 of row tile r / 128.
+  const int x = NT == 2 ? warp >> 2 : 0;
+  const int row = int(threadIdx.x) & (kTile - 1);
+  const int tok = w.tok0 + x * p.tt + row / p.G;
+  const int head = w.kvh * p.G + row % p.G;
+  const bool row_ok = warp < C::SOFT_WARPS && row < p.tt * p.G && tok < w.tok_end;
+  const int64_t part = (int64_t(w.slot) * p.Tq + tok) * p.H + head;
+  if (tiles == 0) {   // no visible key in this chunk: an empty partial
+    pdl_launch_dependents();
+    if (row_ok) p.part_lse[part] = kNegInf;
+    return;
+  }
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::KS; ++i) {
+      mbar_init(&k_full[i], 4);
+      mbar_init(&k_free[i], nact);
+      mbar_init(&v_full[i], 4);
+      mbar_init(&v_free[i], nact);
+    }
+    for (int i = 0; i < NT; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_done[i], 1);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == C::MMA_WARP) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  // the chunk's pages; one out of range is read as zeros
+  {
+    const int first = w.k0 >> p.page_shift;
+    const int n = ((w.k1 - 1) >> p.page_shift) - first + 1;
+    for (int i = threadIdx.x; i < n; i += C::THREADS) {
+      const int pg = __ldg(w.pages + first + i);
+      const bool ok = pg >= 0 && pg < p.num_pages;
+      if (!ok) set_status(p.status, TSEL_DEV_PAGES);
+      s_pages[i] = ok ? pg : -1;
+    }
+  }
+  float qc = 0.f;   // softmax_scale * log2(e) * 2^(row's exponent)
+  if (warp < C::SOFT_WARPS && x < nact) {
+    // Q rows, scaled to fp16, into the K-major A operand
+    uint8_t* sq = smem + C::OFF_Q + x * C::TILE_BYTES;
+    uint32_t v[D / 2];
+    uint32_t top = 0;
+    if (row_ok) {
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
+                                                        tok * p.q_stride + int64_t(head) * D);
+#pragma unroll
+      for (int j = 0; j < D / 8; ++j) {
+        const uint4 t = __ldg(src + j);
+        v[4 * j] = t.x;
+        v[4 * j + 1] = t.y;
+        v[4 * j + 2] = t.z;
+        v[4 * j + 3] = t.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < D / 2; ++j) v[j] = 0;
+    }
+    auto get = [&](uint32_t u) -> float2 {
+      if (p.fp16) return __half22float2(*reinterpret_cast<__half2*>(&u));
+      return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+    };
+#pragma unroll
+    for (int j = 0; j < D / 2; ++j) {
+      const float2 f = get(v[j]);
+      top = max(top, max(__float_as_uint(f.x) & 0x7FFFFFFFu, __float_as_uint(f.y) & 0x7FFFFFFFu));
+    }
+    const int E = max(int(top >> 23), 14);
+    const float up = __uint_as_float(uint32_t(267 - E) << 23);   // largest element into [2^13, 2^14)
+    qc = p.c * __uint_as_float(uint32_t(E - 13) << 23);          // 2^(E - 140)
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) {
+      uint4 t;
+      float2 f;
+      f = get(v[4 * j]);
+      t.x = pack_f16(f.x * up, f.y * up);
+      f = get(v[4 * j + 1]);
+      t.y = pack_f16(f.x * up, f.y * up);
+      f = get(v[4 * j + 2]);
+      t.z = pack_f16(f.x * up, f.y * up);
+      f = get(v[4 * j + 3]);
+      t.w = pack_f16(f.x * up, f.y * up);
+      *reinterpret_cast<uint4*>(sq + (j >> 3) * (kTile * 128) + row * 128 + (((j & 7) ^ (row & 7)) << 4)) = t;
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_launch_dependents();   // after the TMEM allocation
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp < C::SOFT_WARPS) {
+    // ------------------------------------------------------------ softmax
+    if (x < nact) {
+      const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+      const uint32_t ts = tmem + lanes + uint32_t(x * 256), to = ts + 128;
+      const bool any_row = __any_sync(0xffffffffu, row_ok);
+      const int lim = w.causal ? w.lim0 + (tok - w.tok_first) : w.lim0;
+      const int end = row_ok ? min(lim, w.k1) : 0;
+      float m = kNegInf, l = 0.f;
+      int vref = 0;
+      bool ok = true;
+      for (int t = 0; t < tiles; ++t) {
+        ok = warp_wait(&s_full[x], uint32_t(t & 1), abort_flag, T);
+        if (!ok) break;
+        if (any_row) {
+          tc_fence_after();
+          const AttTileMeta& meta = s_meta[t & (kAttMetaRing - 1)];
+          const float ct = fmaxf(qc * meta.k_scale, 1e-38f);
+          const int vis = end - (w.k0 + t * kTile);   // visible columns: [0, vis)
+          const bool full = __all_sync(0xffffffffu, vis >= kTile || !row_ok);
+          uint32_t r0[32], r1[32];
+          tmem_ld32_async(ts, r0);
+          tmem_ld32_async(ts + 32, r1);
+          tmem_wait_ld(r0);
+          tmem_wait_ld(r1);
+          if (!full) {
+            mask_cols(r0, vis);
+            mask_cols(r1, vis - 32);
+          }
+          float top = fmaxf(cols_max(r0), cols_max(r1));
+          tmem_ld32_async(ts + 64, r0);
+          tmem_ld32_async(ts + 96, r1);
+          tmem_wait_ld(r0);
+          tmem_wait_ld(r1);
+          if (!full) {
+            mask_cols(r0, vis - 64);
+            mask_cols(r1, vis - 96);
+          }
+          top = fmaxf(top, fmaxf(cols_max(r0), cols_max(r1))) * ct;
+          const int vnew = meta.v_ref;
+          const bool move = top > m + kAttSlack;
+          if (__any_sync(0xffffffffu, move) || vnew != vref) {
+            float s = 1.f;
+            if (move) {
+              s = ex2(m - top);   // 0 at the row's first visible keys
+              l *= s;
+              m = top;
+            }
+            // V references only grow: 2^(old - new), 0 below 2^-126
+            const int dv = vref - vnew;
+            s *= dv < -126 ? 0.f : __uint_as_float(uint32_t(127 + dv) << 23);
+            vref = vnew;
+            if (t > 0) {
+#pragma unroll
+              for (int cc = 0; cc < D / 16; ++cc) {
+                uint32_t o[16];
+                tmem_ld16(to + cc * 16, o);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * s);
+                tmem_st16(to + cc * 16, o);
+              }
+            }
+          }
+          const float shift = m == kNegInf ? 0.f : kAttLift - m;
+          const float2 c2 = make_float2(ct, ct), s2 = make_float2(shift, shift);
+          float2 acc = make_float2(0.f, 0.f);
+          const bool nan_v = (meta.v_nan[0] | meta.v_nan[1] | meta.v_nan[2] | meta.v_nan[3]) != 0;
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) {
+            uint32_t r[32], h[16];
+            tmem_ld32_async(ts + 32 * cc, r);
+            tmem_wait_ld(r);
+            if (!full) mask_cols(r, vis - 32 * cc);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float2 a = __ffma2_rn(
+                  make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), c2, s2);
+              float2 e = make_float2(ex2(a.x), ex2(a.y));
+              acc = __fadd2_rn(acc, e);
+              if (nan_v) {
+                const uint32_t bits = meta.v_nan[cc] >> (2 * j);
+                if ((bits & 1u) && 32 * cc + 2 * j < vis) e.x = __uint_as_float(0x7FC00000u);
+                if ((bits & 2u) && 32 * cc + 2 * j + 1 < vis) e.y = __uint_as_float(0x7FC00000u);
+              }
+              h[j] = pack_f16(e.x, e.y);
+            }
+            tmem_st16(ts + 16 * cc, h);   // columns whose S has been read
+          }
+          l += acc.x + acc.y;
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        mbar_arrive_lane0(&p_full[x], lane);
+      }
+      if (ok) ok = warp_wait(&o_done[x], uint32_t((tiles - 1) & 1), abort_flag, T);
+      if (!ok) {
+        if (lane == 0) {
+          *abort_flag = 1;
+          set_status(p.status, TSEL_DEV_TIMEOUT);
+        }
+      } else if (any_row) {
+        tc_fence_after();
+        // O' * 2^(vref - 134) / l', both with the same 2^10
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float vs = __uint_as_float(uint32_t(vref - 7) << 23);
+#pragma unroll
+        for (int cc = 0; cc < D / 16; ++cc) {
+          uint32_t o[16];
+          tmem_ld16(to + cc * 16, o);
+          if (row_ok && l != 0.f) {
+            float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + cc * 16);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              dst[j] = make_float4(__uint_as_float(o[4 * j]) * inv * vs, __uint_as_float(o[4 * j + 1]) * inv * vs,
+                                   __uint_as_float(o[4 * j + 2]) * inv * vs, __uint_as_float(o[4 * j + 3]) * inv * vs);
+          }
+        }
+        if (row_ok) p.part_lse[part] = l == 0.f ? kNegInf : m + (log2f(l) - kAttLift);
+      }
+    }
+  } else if (warp < C::CONV_WARP) {
+    // ------------------------------------------------------------ MMA issuers
+    const int xi = warp - C::MMA_WARP;
+    if (lane == 0 && xi < nact) {
+      constexpr uint32_t kIdS = idesc_f16_f32(kTile, kTile, false);
+      constexpr uint32_t kIdO = idesc_f16_f32(kTile, D, true);
+      const uint32_t ts = tmem + uint32_t(xi * 256), to = ts + 128;
+      const uint32_t sq = smem_u32(smem + C::OFF_Q + xi * C::TILE_BYTES);
+      bool ok = true;
+      int issued = 0;
+      for (int t = 0; t < tiles && ok; ++t) {
+        const int st = t % C::KS;
+        const uint32_t ph = uint32_t((t / C::KS) & 1);
+        // P overwrote S: the previous O product must have read it
+        ok = wait_bounded(&k_full[st], ph, abort_flag, T) &&
+             (t == 0 || wait_bounded(&o_done[xi], uint32_t((t - 1) & 1), abort_flag, T));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sk = smem_u32(smem + C::OFF_K + st * C::TILE_BYTES);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+          mma_bf16(ts, smem_desc(sq + off, 2, 1024), smem_desc(sk + off, 2, 1024), kIdS, kk > 0);
+        }
+        mma_commit(&s_full[xi]);
+        mma_commit(&k_free[st]);
+        ok = wait_bounded(&v_full[st], ph, abort_flag, T) &&
+             wait_bounded(&p_full[xi], uint32_t(t & 1), abort_flag, T);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t sv = smem_u32(smem + C::OFF_V + st * C::TILE_BYTES);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          mma_f16_ta(to, ts + kk * 8, smem_desc_mn(sv + kk * 2048, kTile * 128, 1024), kIdO,
+                     t > 0 || kk > 0);
+        mma_commit(&v_free[st]);
+        mma_commit(&o_done[xi]);
+        issued = t + 1;
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        set_status(p.status, TSEL_DEV_TIMEOUT);
+        mma_commit(&o_done[xi]);   // one more phase, for whatever is in flight
+      }
+      // every MMA this thread issued has completed before TMEM is freed
+      if (issued > 0) wait_drain(&o_done[xi], uint32_t((issued - 1) & 1), T);
+      if (!ok) wait_drain(&o_done[xi], uint32_t(issued & 1), T);
+    }
+  } else {
+    // ------------------------------------------------------------ converters
+    const int grp = NT == 2 ? (warp - C::CONV_WARP) >> 2 : 0;
+    const bool do_k = NT == 1 || grp == 0, do_v = NT == 1 || grp == 1;
+    const int tid = (int(threadIdx.x) - 32 * C::CONV_WARP) & (kTile - 1);
+    const int first_page = w.k0 >> p.page_shift;
+    const int mask = (1 << p.page_shift) - 1;
+    uint32_t* fac_k = s_fac;
+    uint32_t* fac_v = s_fac + 2 * kTile;
+    // row (in rows of head_dim codes) of the key at offset j of the chunk, -1 if none
+    auto cache_row = [&](int j) -> int64_t {
+      const int key = w.k0 + j;
+      if (key >= w.k1) return -1;
+      const int pg = s_pages[(key >> p.page_shift) - first_page];
+      if (pg < 0) return -1;
+      return ((int64_t(pg) * p.Hkv + w.kvh) << p.page_shift) + (key & mask);
+    };
+    uint4 kr[NT == 1 ? C::UPT : 1], vr[NT == 1 ? C::UPT : 1], xr[NT == 2 ? C::UPT : 1];
+    auto load = [&](int t, const uint8_t* pages, uint4* dst) {
+#pragma unroll
+      for (int i = 0; i < C::UPT; ++i) {
+        const int u = i * kTile + tid;
+        const int64_t r = t < tiles ? cache_row(t * kTile + u / C::UPT) : -1;
+        dst[i] = r < 0 ? make_uint4(0, 0, 0, 0)
+                       : __ldg(reinterpret_cast<const uint4*>(pages + r * D) + u % C::UPT);
+      }
+    };
+    // exponent bytes of keys 4 * lane .. + 3 of a tile (0 past the end)
+    auto load_exps = [&](int t, const uint8_t* exps) -> uint32_t {
+      const int j = t * kTile + 4 * lane;
+      const int64_t r = t < tiles ? cache_row(j) : -1;
+      if (r < 0) return 0;
+      uint32_t e = __ldg(reinterpret_cast<const uint32_t*>(exps + r));
+      const int left = w.k1 - (w.k0 + j);   // keys of the four inside the chunk
+      return left >= 4 ? e : e & ((1u << (8 * left)) - 1u);
+    };
+    auto convert = [&](uint8_t* tile, const uint32_t* fac, const uint4* src) {
+#pragma unroll
+      for (int i = 0; i < C::UPT; ++i) {
+        const int u = i * kTile + tid;
+        const int r = u / C::UPT, cu = u % C::UPT;   // row; 16-element piece of it
+        const uint32_t f = fac[r];
+        uint4 lo, hi;
+        lo.x = unpack_e4m3(src[i].x & 0xFFFFu, f);
+        lo.y = unpack_e4m3(src[i].x >> 16, f);
+        lo.z = unpack_e4m3(src[i].y & 0xFFFFu, f);
+        lo.w = unpack_e4m3(src[i].y >> 16, f);
+        hi.x = unpack_e4m3(src[i].z & 0xFFFFu, f);
+        hi.y = unpack_e4m3(src[i].z >> 16, f);
+        hi.z = unpack_e4m3(src[i].w & 0xFFFFu, f);
+        hi.w = unpack_e4m3(src[i].w >> 16, f);
+        uint8_t* base = tile + (cu >> 2) * (kTile * 128) + r * 128;
+        const int j0 = 2 * (cu & 3), sw = r & 7;
+        // the lanes of the second 64 columns store their halves the other way
+        // round, so that eight lanes cover all 32 banks
+        const bool flip = (cu >> 2) != 0;
+        const int ja = (j0 + (flip ? 1 : 0)) ^ sw, jb = (j0 + (flip ? 0 : 1)) ^ sw;
+        *reinterpret_cast<uint4*>(base + (ja << 4)) = flip ? hi : lo;
+        *reinterpret_cast<uint4*>(base + (jb << 4)) = flip ? lo : hi;
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+    };
+    uint32_t ke = do_k ? load_exps(0, p.k_exps) : 0u, ve = load_exps(0, p.v_exps);
+    if (NT == 1) {
+      load(0, p.k_pages, kr);
+      load(0, p.v_pages, vr);
+    } else {
+      load(0, do_k ? p.k_pages : p.v_pages, xr);
+    }
+    int vref = 0;
+    bool ok = true;
+    for (int t = 0; t < tiles; ++t) {
+      const int st = t % C::KS, par = t & 1;
+      // references and factors of the tile; this warp's row is key tid
+      const uint32_t kmax = max(8u, __reduce_max_sync(0xffffffffu, max_byte(ke)));
+      const int vmax = int(max(8u, __reduce_max_sync(0xffffffffu, max_byte(ve))));
+      if (vmax > vref) vref = min(vmax + kAttVSlack, 254);
+      const int src_lane = tid >> 2, sh = (tid & 3) * 8;
+      const uint32_t kb = (__shfl_sync(0xffffffffu, ke, src_lane) >> sh) & 0xFFu;
+      const uint32_t vb = (__shfl_sync(0xffffffffu, ve, src_lane) >> sh) & 0xFFu;
+      const unsigned vnan = __ballot_sync(0xffffffffu, vb == 255u);
+      if (do_k) {
+        fac_k[par * kTile + tid] = kb == 255u ? 0x7E007E00u : att_factor(int(kb), int(kmax));
+        AttTileMeta& meta = s_meta[t & (kAttMetaRing - 1)];
+        if (lane == 0) meta.v_nan[tid >> 5] = vnan;
+        if (tid == 0) {
+          meta.k_scale = __uint_as_float((kmax - 7u) << 23);
+          meta.v_ref = vref;
+        }
+      }
+      if (do_v) fac_v[par * kTile + tid] = vb == 255u ? 0u : att_factor(int(vb), vref);
+      // the factors of the next tile go to the other half, so one barrier will do
+      if (NT == 1 || grp == 0)
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+      else
+        asm volatile("bar.sync 2, 128;" ::: "memory");
+      ke = do_k ? load_exps(t + 1, p.k_exps) : 0u;
+      ve = load_exps(t + 1, p.v_exps);
+      if (do_k) {
+        if (t >= C::KS) ok = ok && warp_wait(&k_free[st], uint32_t(((t - C::KS) / C::KS) & 1), abort_flag, T);
+        if (ok) {
+          convert(smem + C::OFF_K + st * C::TILE_BYTES, fac_k + par * kTile, NT == 1 ? kr : xr);
+          mbar_arrive_lane0(&k_full[st], lane);
+          load(t + 1, p.k_pages, NT == 1 ? kr : xr);
+        }
+      }
+      if (do_v) {
+        if (t >= C::KS) ok = ok && warp_wait(&v_free[st], uint32_t(((t - C::KS) / C::KS) & 1), abort_flag, T);
+        if (ok) {
+          convert(smem + C::OFF_V + st * C::TILE_BYTES, fac_v + par * kTile, NT == 1 ? vr : xr);
+          mbar_arrive_lane0(&v_full[st], lane);
+          load(t + 1, p.v_pages, NT == 1 ? vr : xr);
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      *abort_flag = 1;
+      set_status(p.status, TSEL_DEV_TIMEOUT);
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == C::MMA_WARP) tmem_dealloc(tmem, C::TMEM_COLS);
+}
+
+// Joins a row's partial results: out = sum_c 2^(lse_c - lse) o_c, in chunk
+// order. One warp per row, D / 4 lanes of four columns.
+template <int D>
+__global__ void __launch_bounds__(256) attend_join_kernel(const AttParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int total = __ldg(p.cu_q + p.R);
+  if (total < 0 || total > p.Tq) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) set_status(p.status, TSEL_DEV_SEQLENS);
+    return;
+  }
+  const int64_t rows = int64_t(total) * p.H;
+  const int64_t step = int64_t(p.Tq) * p.H;
+  const int64_t nwarps = int64_t(gridDim.x) * 8;
+  for (int64_t r = (int64_t(blockIdx.x) * 256 + threadIdx.x) >> 5; r < rows; r += nwarps) {
+    float m = kNegInf;
+    for (int c = lane; c < p.slots; c += 32) m = fmaxf(m, p.part_lse[c * step + r]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float ref = m == kNegInf ? 0.f : m;
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < p.slots; ++c) {
+      const float wgt = exp2f(p.part_lse[c * step + r] - ref);
+      if (wgt != 0.f) {   // a chunk without visible keys wrote no columns
+        sum += wgt;
+        if (lane < D / 4) {
+          const float4 o = *reinterpret_cast<const float4*>(p.part_o + (c * step + r) * D + 4 * lane);
+          acc.x += wgt * o.x;
+          acc.y += wgt * o.y;
+          acc.z += wgt * o.z;
+          acc.w += wgt * o.w;
+        }
+      }
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const int64_t tok = r / p.H;
+    const int head = int(r - tok * p.H);
+    if (lane < D / 4) {
+      uint2 o;
+      if (p.fp16) {
+        o.x = pack_f16(acc.x * inv, acc.y * inv);
+        o.y = pack_f16(acc.z * inv, acc.w * inv);
+      } else {
+        __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+        __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+        o.x = *reinterpret_cast<uint32_t*>(&a);
+        o.y = *reinterpret_cast<uint32_t*>(&b);
+      }
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + tok * p.out_stride + int64_t(head) * D + 4 * lane) = o;
+    }
+    if (lane == 0 && p.lse != nullptr)
+      p.lse[int64_t(head) * p.Tq + tok] = sum == 0.f ? kNegInf : (ref + log2f(sum)) * 0.69314718055994531f;
+  }
+}
+
+template <int D, int NT>
+cudaError_t launch_attend_t(const AttParams& p, int64_t units, cudaStream_t stream) {
+  using C = AttCfg<D, NT>;
+  auto kern = attend_kernel<D, NT>;
+  static bool attr_set[128] = {};   // per device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 128 || !attr_set[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 128) attr_set[dev] = true;
+  }
+  return launch_kernel(kern, dim3(unsigned(units)), C::THREADS, size_t(C::SMEM_BYTES), stream, 1, p);
+}
+
+}  // namespace
+
+cudaError_t launch_attend(int head_dim, int row_tiles, const AttParams& p, int64_t units,
+                          cudaStream_t stream) {
+#define TSEL_ATT_CASE(DD)                                                        \
+  case DD:                                                                       \
+    return row_tiles == 2 ? launch_attend_t<DD, 2>(p, units, stream)             \
+                          : launch_attend_t<DD, 1>(p, units, stream);
+  switch (head_dim) {
+    TSEL_ATT_CASE(64)
+    TSEL_ATT_CASE(80)
+    TSEL_ATT_CASE(96)
+    TSEL_ATT_CASE(112)
+    TSEL_ATT_CASE(128)
+    default:
+      return cudaErrorInvalidValue;
+  }
+#undef TSEL_ATT_CASE
+}
+
+cudaError_t launch_attend_join(int head_dim, const AttParams& p, int num_sms, cudaStream_t stream) {
+  int64_t blocks = ceil_div(int64_t(p.Tq) * p.H, 8);
+  const int64_t most = int64_t(num_sms) * 8;
+  if (blocks > most) blocks = most;
+#define TSEL_JOIN_CASE(DD)                                                                    \
+  case DD:                                                                                    \
+    return launch_kernel(attend_join_kernel<DD>, dim3(unsigned(blocks)), 256, 0, stream, 1, p);
+  switch (head_dim) {
+    TSEL_JOIN_CASE(64)
+    TSEL_JOIN_CASE(80)
+    TSEL_JOIN_CASE(96)
+    TSEL_JOIN_CASE(112)
+    TSEL_JOIN_CASE(128)
+    default:
+      return cudaErrorInvalidValue;
+  }
+#undef TSEL_JOIN_CASE
+}
+
+}  // namespace tsel

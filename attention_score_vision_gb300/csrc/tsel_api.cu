@@ -163,6 +163,9 @@ uint64_t wait_timeout_ns() {
 namespace tsel {
 // Lets other translation units of the library report a detailed error.
 void record_error(const char* msg) { g_last_error = msg; }
+// ... and size its launches and bound its waits as this one does.
+int device_sms(int* out) { return sm_count(out); }
+uint64_t device_wait_timeout_ns() { return wait_timeout_ns(); }
 }  // namespace tsel
 
 extern "C" {

@@ -73,7 +73,10 @@ typedef enum tsel_status {
 #define TSEL_DEV_REQUESTS  0x2u  /* request offsets or keep counts out of range */
 #define TSEL_DEV_KEEP_IDX  0x4u  /* keep_idx out of range or not strictly ascending */
 #define TSEL_DEV_TIMEOUT   0x8u  /* a bounded device wait gave up */
-#define TSEL_DEV_NAN       0x10u /* NaN score given to the top-B selection or budget */
+#define TSEL_DEV_NAN       0x10u /* NaN score given to the top-B selection or budget; NaN or
+                                    infinity written to the cache */
+#define TSEL_DEV_PAGES     0x20u /* page index or cache slot out of range */
+#define TSEL_DEV_POSITIONS 0x40u /* rope table names an axis the positions do not have */
 
 /* total_keep value of tsel_select_topk when the budgets were computed on the
  * device (tsel_dynamic_budget): keep_idx then has room for total_tokens. */
@@ -409,6 +412,195 @@ TSEL_API tsel_status tsel_gather_compact_counted(const void* hidden, int64_t hid
                                 void* out_hidden, int32_t* out_pos,
                                 int32_t* out_img_id, int32_t* out_cu_seqlens,
                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Rotary positions with several axes                                       */
+/* ------------------------------------------------------------------------ */
+
+/* Element types of the entry points below. */
+#define TSEL_BF16 0
+#define TSEL_FP16 1
+#define TSEL_FP32 2
+
+/* tsel_rope / tsel_cache_write flags */
+#define TSEL_ROPE_ADJACENT 0x1u /* pair i is columns (2i, 2i + 1); without it, (i, num_pairs + i) */
+#define TSEL_ROPE_INVERSE  0x2u /* rotate back (tsel_rope only): the gradient of the rotation */
+
+/* Layouts of tsel_rope_frequencies */
+#define TSEL_ROPE_SECTIONED   0 /* axes in consecutive sections of the pairs, one frequency ladder
+                                   over all of them: pair i turns by base^(-i / pairs) */
+#define TSEL_ROPE_INTERLEAVED 1 /* the same ladder, pair i on axis i mod num_axes while that axis
+                                   has pairs left, the rest on axis 0 */
+#define TSEL_ROPE_PER_AXIS    2 /* sections whose frequencies start anew: pair j of axis a turns by
+                                   base^(-j / sections[a]) (rows and columns of a vision encoder) */
+
+/*
+ * Frequencies (radians per position step) and axes of the pairs of a rotation
+ * whose axis a (time or image, row, column, ...) has sections[a] pairs. Host
+ * only. [VTC] section 3.2: position ids of several axes (mRoPE) stay with the
+ * tokens after pruning.
+ *
+ * sections  num_axes counts (1 to 8 axes; at most 128 pairs in all).
+ * inv_freq  out double [sum of sections]; axis out int32 [sum of sections].
+ * TSEL_ROPE_INTERLEAVED returns TSEL_ERR_INVALID_VALUE when the cycle cannot
+ * give every axis its count.
+ */
+TSEL_API tsel_status tsel_rope_frequencies(double base, const int32_t* sections, int num_axes,
+                                           int layout, double* inv_freq, int32_t* axis);
+
+/*
+ * Packs frequencies and axes into the table the rotating kernels read: per
+ * pair, the fraction of a turn per position step in 61-bit fixed point and the
+ * axis in the low three bits. Host only; the caller copies the table to the
+ * device once. Any frequencies and axes will do (scaled ladders among them):
+ * |inv_freq[i]| <= 1e6, axis[i] in [0, 7], at most 128 pairs.
+ */
+TSEL_API tsel_status tsel_rope_table(const double* inv_freq, const int32_t* axis, int num_pairs,
+                                     uint64_t* table);
+
+/* Bytes of workspace tsel_rope, tsel_cache_write and tsel_cache_read need. */
+TSEL_API size_t tsel_cache_workspace_size(void);
+
+/*
+ * Rotates the first 2 * num_pairs columns of every head of Q and K: with
+ * angle = pos[t][axis_i] * inv_freq_i, pair (a, b) becomes
+ * (a cos - b sin, b cos + a sin); the other columns are copied. The angle is
+ * exact modulo a turn for every int32 position; sine, cosine and products are
+ * fp32, rounded once to the output type. With TSEL_ROPE_INVERSE the pairs turn
+ * back: applied to the gradients of q_out and k_out it gives those of q and k.
+ *
+ * q        [total, num_heads, head_dim], row t at q + t * q_row_stride elements
+ *          (0 = dense). 16-byte aligned, row strides multiples of 16 bytes.
+ * k        [total, num_kv_heads, head_dim], the same; num_kv_heads = 0: no K.
+ * pos      int32 [total, pos_dim] dense (pos_dim in [1, 8]), e.g. out_pos of
+ *          tsel_gather_compact; negative positions are allowed.
+ * table    device, num_pairs entries of tsel_rope_table (0 pairs copy). An axis
+ *          that is not below pos_dim sets TSEL_DEV_POSITIONS; its pair is copied.
+ * head_dim a multiple of 8, at most 256; num_heads and num_kv_heads at most 256.
+ * dtype    TSEL_BF16, TSEL_FP16 or TSEL_FP32.
+ * q_out, k_out  as q and k; may be q and k themselves with the same stride
+ *          (in place), but may not overlap them otherwise.
+ */
+TSEL_API tsel_status tsel_rope(const void* q, int64_t q_row_stride, const void* k,
+                               int64_t k_row_stride, const int32_t* pos, int pos_dim,
+                               const uint64_t* table, int num_pairs, int total, int num_heads,
+                               int num_kv_heads, int head_dim, int dtype, unsigned flags,
+                               void* q_out, int64_t q_out_row_stride, void* k_out,
+                               int64_t k_out_row_stride, void* workspace, size_t workspace_bytes,
+                               void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Quantised paged cache                                                    */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * The cache is four device arrays: k_pages and v_pages, E4M3 codes
+ * [num_pages, num_kv_heads, page_size, head_dim], and k_exps and v_exps, bytes
+ * [num_pages, num_kv_heads, page_size], all 16-byte aligned. A row (one token
+ * and head) stands for code * 2^(byte - 127); byte 255 makes the whole row
+ * NaN. Slot s is place s mod page_size of page s / page_size. page_size is 16,
+ * 32, 64 or 128, head_dim 64, 80, 96, 112 or 128, num_pages * page_size at most
+ * 2^31 - 1.
+ *
+ * tsel_cache_write quantises the K and V rows of `total` tokens into slots
+ * ([LiteVLM]: FP8 deployment; [VTC] section 3.2: the pruned sequence goes to
+ * the KV cache): byte - 127 is the least e >= -127 with max|x| <= 448 * 2^e, a
+ * code is x * 2^-e rounded to the nearest E4M3 value, ties to even. A row with
+ * a NaN or an infinity is stored as NaN and sets TSEL_DEV_NAN. With
+ * num_pairs > 0 K is rotated on its way as by tsel_rope (pos, pos_dim, table,
+ * and TSEL_ROPE_ADJACENT in flags), and quantised from the fp32 rotation.
+ *
+ * k, v     [total, num_kv_heads, head_dim] rows as in tsel_rope.
+ * slots    int32 [total] device; a negative slot skips its token (padding),
+ *          one past the last page sets TSEL_DEV_PAGES and skips it. Slots
+ *          must differ: what two tokens given the same slot leave in it is
+ *          unspecified (nothing else is touched).
+ */
+TSEL_API tsel_status tsel_cache_write(const void* k, int64_t k_row_stride, const void* v,
+                                      int64_t v_row_stride, const int32_t* pos, int pos_dim,
+                                      const uint64_t* table, int num_pairs, const int32_t* slots,
+                                      int total, int num_kv_heads, int head_dim, int dtype,
+                                      unsigned flags, uint8_t* k_pages, uint8_t* v_pages,
+                                      uint8_t* k_exps, uint8_t* v_exps, int num_pages,
+                                      int page_size, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+
+/*
+ * Reads slots back: k_out and v_out [total, num_kv_heads, head_dim] of dtype,
+ * rows of code * 2^(byte - 127) rounded to dtype (exact for TSEL_BF16 and
+ * TSEL_FP32 wherever the value is a normal number of the type), e.g. for
+ * tsel_importance on cached keys. A negative slot gives zeros; one past the last page
+ * sets TSEL_DEV_PAGES and gives zeros. The same slot may be read by several
+ * tokens.
+ */
+TSEL_API tsel_status tsel_cache_read(const uint8_t* k_pages, const uint8_t* v_pages,
+                                     const uint8_t* k_exps, const uint8_t* v_exps, int num_pages,
+                                     int page_size, const int32_t* slots, int total,
+                                     int num_kv_heads, int head_dim, int dtype, void* k_out,
+                                     int64_t k_row_stride, void* v_out, int64_t v_row_stride,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Attention over a shared prefix                                           */
+/* ------------------------------------------------------------------------ */
+
+/* Bytes of workspace tsel_prefix_attention needs for these sizes (0 for sizes
+ * it does not take). */
+TSEL_API size_t tsel_prefix_attention_workspace_size(int num_req, int total_q, int max_seqlen_q,
+                                                     int num_heads, int num_kv_heads, int head_dim,
+                                                     int max_prefix_len, int max_suffix_len);
+
+/*
+ * Attention of a batch of requests over the quantised cache: every request
+ * sees the same prefix (the kept tokens of the images they ask about), read
+ * once for all of them, and then its own suffix. Query row i (of n) of request
+ * r sees the whole prefix and the first suffix_lens[r] - n + i + 1 keys of its
+ * suffix (its own last n tokens are in the cache already; none if that is not
+ * positive). With kvh(h) = h / (H / Hkv) and the rows of the cache as the
+ * values they stand for:
+ *   P[h,i,j] = exp(s * q_{i,h} . k_{j,kvh(h)} - lse[h,i]),
+ *   out[i,h] = sum_j P[h,i,j] v_{j,kvh(h)},   lse natural log.
+ * A row that sees no key gives out = 0 and lse = -inf.
+ *
+ * q             [total_q, num_heads, head_dim] of dtype (TSEL_BF16 or
+ *               TSEL_FP16); rows as in tsel_rope. num_heads in [1, 256],
+ *               num_kv_heads divides it, at most 128 query heads per KV head.
+ * cu_seqlens_q  int32 [num_req + 1] device: 0, monotone, lengths at most
+ *               max_seqlen_q, the last at most total_q. Rows from
+ *               cu_seqlens_q[num_req] on (padding of a captured batch) are
+ *               neither read nor written.
+ * prefix_pages  int32 [ceil(max_prefix_len / page_size)] device: pages of the
+ *               prefix in order; prefix_len: int32 device scalar, at most
+ *               max_prefix_len. Both may be NULL when max_prefix_len is 0.
+ * page_table    int32 device, row r at page_table + r * page_table_stride (at
+ *               least ceil(max_suffix_len / page_size)): the pages of request
+ *               r's suffix in order; suffix_lens int32 [num_req] device, at
+ *               most max_suffix_len. NULL allowed when max_suffix_len is 0.
+ *               Only the pages that hold keys are read.
+ * softmax_scale <= 0 selects 1/sqrt(head_dim).
+ * out           as q; lse fp32 [num_heads, total_q] or NULL.
+ * workspace     >= tsel_prefix_attention_workspace_size(...): partial results
+ *               of the key chunks; nothing in it outlives the call but the
+ *               status word.
+ *
+ * Lengths outside their bounds set TSEL_DEV_SEQLENS, pages outside the cache
+ * TSEL_DEV_PAGES; the rows concerned are then unspecified, and nothing out of
+ * range is touched. Keys that a row does not see never reach it, whatever
+ * their pages hold. Rows stored as NaN make NaN of the rows that see them.
+ * Results are deterministic. Precision: q and the cached rows enter as fp16
+ * after scaling by powers of two (exact but for q elements below 2^-27 of the
+ * largest of their row, K rows below 2^-22 and V rows below 2^-20 of the
+ * largest of their key chunk, which round on that grid), probabilities as
+ * fp16, with sums and statistics in fp32.
+ */
+TSEL_API tsel_status tsel_prefix_attention(
+    const void* q, int64_t q_row_stride, const int32_t* cu_seqlens_q, int num_req, int total_q,
+    int max_seqlen_q, const uint8_t* k_pages, const uint8_t* v_pages, const uint8_t* k_exps,
+    const uint8_t* v_exps, int num_pages, int page_size, const int32_t* prefix_pages,
+    const int32_t* prefix_len, int max_prefix_len, const int32_t* page_table,
+    int64_t page_table_stride, const int32_t* suffix_lens, int max_suffix_len, int num_heads,
+    int num_kv_heads, int head_dim, int dtype, float softmax_scale, void* out,
+    int64_t out_row_stride, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Host helpers                                                             */
