@@ -49,8 +49,8 @@ namespace tsel {
 namespace {
 
 constexpr int kAttMetaRing = 4;
-constexpr float kAttLift = 10.f;      // P = 2^10 at the row's reference
-constexpr float kAttSlack = 5.f;      // the reference may lag the row maximum by 2^5
+constexpr float kAttLift = 6.f;       // P = 2^6 at the row's reference
+constexpr float kAttSlack = 9.f;      // the reference may lag the row maximum by 2^9
 constexpr int kAttVSlack = 2;         // a moved V reference leaves room for 2^2 larger scales
 
 struct AttTileMeta {
@@ -59,31 +59,33 @@ struct AttTileMeta {
   uint32_t v_nan[4];   // keys whose V row is NaN, a bit each
 };
 
-template <int D, int NT>
+template <int D>
 struct AttCfg {
   static constexpr int DC = D > 64 ? 2 : 1;                 // 64-element chunks of a row
   static constexpr int TILE_BYTES = DC * kTile * 128;       // one 128-row fp16 operand
-  static constexpr int KS = NT;                             // K and V stages
-  static constexpr int CONV_GROUPS = NT;                    // two groups: one for K, one for V
-  static constexpr int SOFT_WARPS = 4 * NT;
-  static constexpr int MMA_WARP = SOFT_WARPS;               // NT issuing warps
-  static constexpr int CONV_WARP = MMA_WARP + NT;
-  static constexpr int WARPS = CONV_WARP + 4 * CONV_GROUPS;
+  static constexpr int KS = 2;                              // K and V stages
+  static constexpr int SOFT_PER_TILE = 8;                   // softmax warps of a row tile: two threads per row
+  static constexpr int SOFT_WARPS = 2 * SOFT_PER_TILE;
+  static constexpr int MMA_WARP = SOFT_WARPS;               // one issuing thread
+  static constexpr int CONV_WARP = MMA_WARP + 1;            // four warps for K, four for V
+  static constexpr int WARPS = CONV_WARP + 8;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = NT * TILE_BYTES;
+  static constexpr int OFF_K = 2 * TILE_BYTES;
   static constexpr int OFF_V = OFF_K + KS * TILE_BYTES;
   static constexpr int OFF_FAC = OFF_V + KS * TILE_BYTES;   // uint32 [K, V][tile parity][128]
   static constexpr int OFF_PAGES = OFF_FAC + 2 * 2 * kTile * 4;
-  static constexpr int OFF_META = OFF_PAGES + kAttMaxPages * 4;
-  static constexpr int NUM_BARS = 4 * KS + 3 * NT;
+  static constexpr int OFF_ROW = OFF_PAGES + kAttMaxPages * 4;   // fp32 [row tile][parity][half][128]
+  static constexpr int OFF_META = OFF_ROW + 2 * 2 * 2 * kTile * 4;
+  static constexpr int NUM_BARS = 4 * KS + 3 * 2;
   static constexpr int OFF_BAR = OFF_META + kAttMetaRing * int(sizeof(AttTileMeta));
   static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;
-  static constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;   // + alignment slack
-  static constexpr int UPT = D / 16;                        // 16-code pieces per converter thread and tile
-  static constexpr uint32_t TMEM_COLS = 256 * NT;
+  static constexpr int SMEM_USED = OFF_MISC + 64 + 1024;    // + alignment slack
+  // one CTA per SM (it holds all of TMEM), also for the smaller heads
+  static constexpr int SMEM_BYTES = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
+  static constexpr int STEPS = 4 * DC;                      // 16-code pieces per converter thread and tile
   static_assert(sizeof(AttTileMeta) % 8 == 0 && OFF_META % 8 == 0, "barrier alignment");
-  static_assert(SMEM_BYTES <= (NT == 1 ? 113 * 1024 : 227 * 1024), "shared memory");
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
 };
 
 // Shared-memory descriptor of an MN-major operand with the 128-byte swizzle:
@@ -125,18 +127,22 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
       : "r"(taddr)
       : "memory");
 }
@@ -178,6 +184,45 @@ __device__ __forceinline__ uint32_t max_byte(uint32_t w) {
   return m;
 }
 
+// Largest of NB * 32 columns of S, masked to the visible ones; the first 32
+// stay in r. One 32-column load at a time: a second one in flight would not
+// fit the registers, and spills cost more than the TMEM latency.
+template <int NB>
+__device__ __forceinline__ float att_max(uint32_t taddr, int vis, bool full, uint32_t (&r)[32]) {
+  float top = kNegInf;
+#pragma unroll
+  for (int b = NB - 1; b >= 0; --b) {
+    tmem_ld32_async(taddr + 32 * b, r);
+    tmem_wait_ld(r);
+    if (!full) mask_cols(r, vis - 32 * b);
+    top = fmaxf(top, cols_max(r));
+  }
+  return top;
+}
+
+// exp2(S * c + shift) of 32 columns, added up in acc and packed to fp16. nan:
+// columns whose V row is NaN (bit per column).
+__device__ __forceinline__ void att_exp32(const uint32_t (&r)[32], float2 c2, float2 s2, float2& acc,
+                                          uint32_t (&h)[16]) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float2 a =
+        __ffma2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), c2, s2);
+    const float2 e = make_float2(ex2(a.x), ex2(a.y));
+    acc = __fadd2_rn(acc, e);
+    h[j] = pack_f16(e.x, e.y);
+  }
+}
+
+// Puts NaN into the visible columns of P whose V row is NaN.
+__device__ __forceinline__ void att_poison32(uint32_t (&h)[16], uint32_t nan, int vis) {
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    if (((nan >> (2 * j)) & 1u) && 2 * j < vis) h[j] = (h[j] & 0xFFFF0000u) | 0x7E00u;
+    if (((nan >> (2 * j + 1)) & 1u) && 2 * j + 1 < vis) h[j] = (h[j] & 0xFFFFu) | 0x7E000000u;
+  }
+}
+
 // What a CTA works on: rows [tok0 + x * tt, ...) of KV head kvh for row tile
 // x, keys [k0, k1) of a page list.
 struct AttUnit {
@@ -191,19 +236,19 @@ struct AttUnit {
   bool bad;
 };
 
-__device__ __forceinline__ AttUnit att_unit(const AttParams& p, int nt, int64_t u) {
+__device__ __forceinline__ AttUnit att_unit(const AttParams& p, int64_t u) {
   AttUnit w{};
   if (u < p.units_p) {
     const int g = int(u % p.ntg);
     const int64_t ch = u / p.ntg;
     w.kvh = int(ch % p.Hkv);
     const int c = int(ch / p.Hkv);
-    w.slot = c;
+    w.slot = 2 * c;
     int n = __ldg(p.prefix_len);
     const int rows = __ldg(p.cu_q + p.R);
     w.bad = n < 0 || n > p.max_prefix || rows < 0 || rows > p.Tq;
     if (w.bad) return w;
-    w.tok0 = g * nt * p.tt;
+    w.tok0 = g * 2 * p.tt;
     w.tok_end = rows;
     w.k0 = min(c * p.lp, n);
     w.k1 = min(w.k0 + p.lp, n);
@@ -217,18 +262,18 @@ __device__ __forceinline__ AttUnit att_unit(const AttParams& p, int nt, int64_t 
     u /= p.qt;
     w.kvh = int(u % p.Hkv);
     const int r = int(u / p.Hkv);
-    w.slot = p.nc + c;
+    w.slot = 2 * (p.nc + c);
     const int a = __ldg(p.cu_q + r), b = __ldg(p.cu_q + r + 1);
     const int n = __ldg(p.suffix_lens + r);
     w.bad = a < 0 || b < a || b > p.Tq || b - a > p.max_q || n < 0 || n > p.max_suffix ||
             (r == 0 && a != 0);
     if (w.bad) return w;
     w.tok_first = a;
-    w.tok0 = a + qi * p.tt;
-    w.tok_end = min(b, w.tok0 + p.tt);
+    w.tok0 = a + qi * 2 * p.tt;
+    w.tok_end = min(b, w.tok0 + 2 * p.tt);
     w.causal = 1;
     w.lim0 = n - (b - a) + 1;
-    // keys past the last row's limit are seen by no row of the tile
+    // keys past the last row's limit are seen by no row of the unit
     const int seen = min(n, w.lim0 + (w.tok_end - 1 - a));
     w.k0 = min(c * p.ls, max(seen, 0));
     w.k1 = min(w.k0 + p.ls, max(seen, 0));
@@ -237,10 +282,9 @@ __device__ __forceinline__ AttUnit att_unit(const AttParams& p, int nt, int64_t 
   return w;
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(AttCfg<D, NT>::THREADS, NT == 1 ? 2 : 1)
-    attend_kernel(const AttParams p) {
-  using C = AttCfg<D, NT>;
+template <int D>
+__global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const AttParams p) {
+  using C = AttCfg<D>;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = smem_dyn + ((1024u - (smem_u32(smem_dyn) & 1023u)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -248,9 +292,9 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::THREADS, NT == 1 ? 2 : 1)
   uint64_t* k_free = k_full + C::KS;        // [KS] S products of the tile done
   uint64_t* v_full = k_free + C::KS;        // [KS]
   uint64_t* v_free = v_full + C::KS;        // [KS]
-  uint64_t* s_full = v_free + C::KS;        // [NT] S in TMEM
-  uint64_t* p_full = s_full + NT;           // [NT] P in TMEM
-  uint64_t* o_done = p_full + NT;           // [NT] O product of the tile done
+  uint64_t* s_full = v_free + C::KS;        // [2] S in TMEM
+  uint64_t* p_full = s_full + 2;            // [2] P in TMEM
+  uint64_t* o_done = p_full + 2;            // [2] O product done
   int32_t* s_pages = reinterpret_cast<int32_t*>(smem + C::OFF_PAGES);
   AttTileMeta* s_meta = reinterpret_cast<AttTileMeta*>(smem + C::OFF_META);
   uint32_t* s_fac = reinterpret_cast<uint32_t*>(smem + C::OFF_FAC);
@@ -260,50 +304,62 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::THREADS, NT == 1 ? 2 : 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t T = p.timeout_ns;
   pdl_wait();   // every input may come from an earlier kernel
-  const AttUnit w = att_unit(p, NT, p.unit0 + blockIdx.x);
+  const AttUnit w = att_unit(p, p.unit0 + blockIdx.x);
   if (w.bad) {
     pdl_launch_dependents();
     if (threadIdx.x == 0) set_status(p.status, TSEL_DEV_SEQLENS);
     return;
   }
-  // row tiles with a row
-  const int nact = NT == 2 && w.tok0 + p.tt < w.tok_end ? 2 : (w.tok0 < w.tok_end ? 1 : 0);
-  if (nact == 0) {
+  if (w.tok0 >= w.tok_end) {   // no rows
     pdl_launch_dependents();
     return;
   }
   const int tiles = int(ceil_div(w.k1 - w.k0, kTile));
+  // Two pipelines x = 0, 1 keep the tensor cores and the softmax warps busy in
+  // turn: with two row tiles each takes one and walks every key tile; with one
+  // row tile (split) they take the even and the odd key tiles, and their
+  // results are two partials.
+  const bool split = w.tok0 + p.tt >= w.tok_end;
+  const int n0 = split ? (tiles + 1) >> 1 : tiles, n1 = split ? tiles >> 1 : tiles;
 
-  // Thread r < 128 * NT of the softmax warps owns row r % 128 of row tile r / 128.
-  const int x = NT == 2 ? warp >> 2 : 0;
+  // Softmax warps: pipeline x, row (TMEM lane) 32 * (warp % 4) + lane, the 64
+  // columns of `half`.
+  const int x = (warp >> 3) & 1;
+  const int half = (warp >> 2) & 1;
   const int row = int(threadIdx.x) & (kTile - 1);
-  const int tok = w.tok0 + x * p.tt + row / p.G;
+  const int tok = w.tok0 + (split ? 0 : x * p.tt) + row / p.G;
   const int head = w.kvh * p.G + row % p.G;
   const bool row_ok = warp < C::SOFT_WARPS && row < p.tt * p.G && tok < w.tok_end;
-  const int64_t part = (int64_t(w.slot) * p.Tq + tok) * p.H + head;
-  if (tiles == 0) {   // no visible key in this chunk: an empty partial
+  // this row's partial: slot w.slot, the second pipeline of a split unit in the
+  // next one (which is empty otherwise)
+  const int64_t part = (int64_t(w.slot + (split ? x : 0)) * p.Tq + tok) * p.H + head;
+  if (row_ok && half == 0) {
+    const int64_t next = int64_t(p.Tq) * p.H;
+    if (!split) p.part_lse[part + next] = kNegInf;
+    if ((x == 0 ? n0 : n1) == 0) p.part_lse[part] = kNegInf;
+  }
+  if (tiles == 0) {   // no visible key in this chunk
     pdl_launch_dependents();
-    if (row_ok) p.part_lse[part] = kNegInf;
     return;
   }
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::KS; ++i) {
       mbar_init(&k_full[i], 4);
-      mbar_init(&k_free[i], nact);
+      mbar_init(&k_free[i], 1);
       mbar_init(&v_full[i], 4);
-      mbar_init(&v_free[i], nact);
+      mbar_init(&v_free[i], 1);
     }
-    for (int i = 0; i < NT; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], C::SOFT_PER_TILE);
       mbar_init(&o_done[i], 1);
     }
     *abort_flag = 0;
     fence_barrier_init();
   }
   if (warp == C::MMA_WARP) {
-    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_alloc(tmem_slot, 512);
     tmem_relinquish();
   }
   // the chunk's pages; one out of range is read as zeros
@@ -317,52 +373,48 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::THREADS, NT == 1 ? 2 : 1)
       s_pages[i] = ok ? pg : -1;
     }
   }
+  // Q rows, scaled to fp16, into the K-major A operand; the threads of a row
+  // take half of its columns each.
   float qc = 0.f;   // softmax_scale * log2(e) * 2^(row's exponent)
-  if (warp < C::SOFT_WARPS && x < nact) {
-    // Q rows, scaled to fp16, into the K-major A operand
-    uint8_t* sq = smem + C::OFF_Q + x * C::TILE_BYTES;
-    uint32_t v[D / 2];
-    uint32_t top = 0;
-    if (row_ok) {
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
-                                                        tok * p.q_stride + int64_t(head) * D);
+  float* s_row = reinterpret_cast<float*>(smem + C::OFF_ROW) + x * 4 * kTile;
+  constexpr int QV = D / 16;   // 16-byte pieces of a row per thread
+  uint4 qv[QV];
+  const bool soft = warp < C::SOFT_WARPS;
+  auto q_pair = [&](uint32_t u) -> float2 {
+    if (p.fp16) return __half22float2(*reinterpret_cast<__half2*>(&u));
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+  };
+  uint32_t q_top = 0;
+  if (soft) {
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
+                                                      tok * p.q_stride + int64_t(head) * D) + half * QV;
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j) {
-        const uint4 t = __ldg(src + j);
-        v[4 * j] = t.x;
-        v[4 * j + 1] = t.y;
-        v[4 * j + 2] = t.z;
-        v[4 * j + 3] = t.w;
+    for (int j = 0; j < QV; ++j) qv[j] = row_ok ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < QV; ++j) {
+      const uint32_t u[4] = {qv[j].x, qv[j].y, qv[j].z, qv[j].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 f = q_pair(u[i]);
+        q_top = max(q_top, max(__float_as_uint(f.x) & 0x7FFFFFFFu, __float_as_uint(f.y) & 0x7FFFFFFFu));
       }
-    } else {
-#pragma unroll
-      for (int j = 0; j < D / 2; ++j) v[j] = 0;
     }
-    auto get = [&](uint32_t u) -> float2 {
-      if (p.fp16) return __half22float2(*reinterpret_cast<__half2*>(&u));
-      return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
-    };
-#pragma unroll
-    for (int j = 0; j < D / 2; ++j) {
-      const float2 f = get(v[j]);
-      top = max(top, max(__float_as_uint(f.x) & 0x7FFFFFFFu, __float_as_uint(f.y) & 0x7FFFFFFFu));
-    }
-    const int E = max(int(top >> 23), 14);
+    s_row[half * kTile + row] = __uint_as_float(q_top);
+  }
+  __syncthreads();
+  if (soft) {
+    q_top = max(q_top, __float_as_uint(s_row[(half ^ 1) * kTile + row]));
+    uint8_t* sq = smem + C::OFF_Q + x * C::TILE_BYTES;   // a split unit's rows twice
+    const int E = max(int(q_top >> 23), 14);
     const float up = __uint_as_float(uint32_t(267 - E) << 23);   // largest element into [2^13, 2^14)
     qc = p.c * __uint_as_float(uint32_t(E - 13) << 23);          // 2^(E - 140)
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j) {
-      uint4 t;
-      float2 f;
-      f = get(v[4 * j]);
-      t.x = pack_f16(f.x * up, f.y * up);
-      f = get(v[4 * j + 1]);
-      t.y = pack_f16(f.x * up, f.y * up);
-      f = get(v[4 * j + 2]);
-      t.z = pack_f16(f.x * up, f.y * up);
-      f = get(v[4 * j + 3]);
-      t.w = pack_f16(f.x * up, f.y * up);
-      *reinterpret_cast<uint4*>(sq + (j >> 3) * (kTile * 128) + row * 128 + (((j & 7) ^ (row & 7)) << 4)) = t;
+    for (int i = 0; i < QV; ++i) {
+      const int j = half * QV + i;
+      const float2 a = q_pair(qv[i].x), b = q_pair(qv[i].y), c = q_pair(qv[i].z), d = q_pair(qv[i].w);
+      *reinterpret_cast<uint4*>(sq + (j >> 3) * (kTile * 128) + row * 128 + (((j & 7) ^ (row & 7)) << 4)) =
+          make_uint4(pack_f16(a.x * up, a.y * up), pack_f16(b.x * up, b.y * up),
+                     pack_f16(c.x * up, c.y * up), pack_f16(d.x * up, d.y * up));
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -374,43 +426,39 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::THREADS, NT == 1 ? 2 : 1)
 
   if (warp < C::SOFT_WARPS) {
     // ------------------------------------------------------------ softmax
-    if (x < nact) {
+    const int n = x == 0 ? n0 : n1;
+    if (n > 0) {
       const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
       const uint32_t ts = tmem + lanes + uint32_t(x * 256), to = ts + 128;
       const bool any_row = __any_sync(0xffffffffu, row_ok);
       const int lim = w.causal ? w.lim0 + (tok - w.tok_first) : w.lim0;
-      const int end = row_ok ? min(lim, w.k1) : 0;
+      const int end = (row_ok ? min(lim, w.k1) : 0) - w.k0;
+      // the two warps of the same 32 rows meet at a barrier of their own
+      const int pair_bar = 3 + x * 4 + (warp & 3);
+      auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory"); };
       float m = kNegInf, l = 0.f;
       int vref = 0;
       bool ok = true;
-      for (int t = 0; t < tiles; ++t) {
-        ok = warp_wait(&s_full[x], uint32_t(t & 1), abort_flag, T);
-        if (!ok) break;
+      for (int i = 0; i < n; ++i) {
+        const int t = split ? 2 * i + x : i;   // key tile
+        if (!warp_wait(&s_full[x], uint32_t(i & 1), abort_flag, T)) {
+          // the loop goes on (the warps of a row meet in it), its waits return at once
+          ok = false;
+          if (lane == 0) *abort_flag = 1;
+        }
         if (any_row) {
           tc_fence_after();
           const AttTileMeta& meta = s_meta[t & (kAttMetaRing - 1)];
           const float ct = fmaxf(qc * meta.k_scale, 1e-38f);
-          const int vis = end - (w.k0 + t * kTile);   // visible columns: [0, vis)
+          const int vis = end - t * kTile;   // visible columns: [0, vis)
           const bool full = __all_sync(0xffffffffu, vis >= kTile || !row_ok);
-          uint32_t r0[32], r1[32];
-          tmem_ld32_async(ts, r0);
-          tmem_ld32_async(ts + 32, r1);
-          tmem_wait_ld(r0);
-          tmem_wait_ld(r1);
-          if (!full) {
-            mask_cols(r0, vis);
-            mask_cols(r1, vis - 32);
-          }
-          float top = fmaxf(cols_max(r0), cols_max(r1));
-          tmem_ld32_async(ts + 64, r0);
-          tmem_ld32_async(ts + 96, r1);
-          tmem_wait_ld(r0);
-          tmem_wait_ld(r1);
-          if (!full) {
-            mask_cols(r0, vis - 64);
-            mask_cols(r1, vis - 96);
-          }
-          top = fmaxf(top, fmaxf(cols_max(r0), cols_max(r1))) * ct;
+          uint32_t r[32];
+          float top = att_max<2>(ts + 64 * half, vis - 64 * half, full, r);
+          float* mx = s_row + (i & 1) * 2 * kTile;
+          mx[half * kTile + row] = top;
+          meet();
+          top = fmaxf(top, mx[(half ^ 1) * kTile + row]);
+          top *= ct;
           const int vnew = meta.v_ref;
           const bool move = top > m + kAttSlack;
           if (__any_sync(0xffffffffu, move) || vnew != vref) {
@@ -424,14 +472,13 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::THREADS, NT == 1 ? 2 : 1)
             const int dv = vref - vnew;
             s *= dv < -126 ? 0.f : __uint_as_float(uint32_t(127 + dv) << 23);
             vref = vnew;
-            if (t > 0) {
+            if (i > 0) {
+              for (int cc = half * (D / 16); cc < (half + 1) * (D / 16); ++cc) {
+                uint32_t o[8];
+                tmem_ld8(to + cc * 8, o);
 #pragma unroll
-              for (int cc = 0; cc < D / 16; ++cc) {
-                uint32_t o[16];
-                tmem_ld16(to + cc * 16, o);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * s);
-                tmem_st16(to + cc * 16, o);
+                for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * s);
+                tmem_st8(to + cc * 8, o);
               }
             }
           }
@@ -440,25 +487,18 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::THREADS, NT == 1 ? 2 : 1)
           float2 acc = make_float2(0.f, 0.f);
           const bool nan_v = (meta.v_nan[0] | meta.v_nan[1] | meta.v_nan[2] | meta.v_nan[3]) != 0;
 #pragma unroll
-          for (int cc = 0; cc < 4; ++cc) {
-            uint32_t r[32], h[16];
-            tmem_ld32_async(ts + 32 * cc, r);
-            tmem_wait_ld(r);
-            if (!full) mask_cols(r, vis - 32 * cc);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float2 a = __ffma2_rn(
-                  make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), c2, s2);
-              float2 e = make_float2(ex2(a.x), ex2(a.y));
-              acc = __fadd2_rn(acc, e);
-              if (nan_v) {
-                const uint32_t bits = meta.v_nan[cc] >> (2 * j);
-                if ((bits & 1u) && 32 * cc + 2 * j < vis) e.x = __uint_as_float(0x7FC00000u);
-                if ((bits & 2u) && 32 * cc + 2 * j + 1 < vis) e.y = __uint_as_float(0x7FC00000u);
-              }
-              h[j] = pack_f16(e.x, e.y);
+          for (int b = 0; b < 2; ++b) {
+            // 32 columns; P takes the columns of the first 32 of its 64, which have been read
+            const int blk = half * 2 + b;
+            if (b > 0) {
+              tmem_ld32_async(ts + 32 * blk, r);
+              tmem_wait_ld(r);
+              if (!full) mask_cols(r, vis - 32 * blk);
             }
-            tmem_st16(ts + 16 * cc, h);   // columns whose S has been read
+            uint32_t h[16];
+            att_exp32(r, c2, s2, acc, h);
+            if (nan_v) att_poison32(h, meta.v_nan[blk], vis - 32 * blk);
+            tmem_st16(ts + 64 * (blk >> 1) + 16 * (blk & 1), h);
           }
           l += acc.x + acc.y;
           tmem_wait_st();
@@ -467,150 +507,169 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::THREADS, NT == 1 ? 2 : 1)
         __syncwarp();
         mbar_arrive_lane0(&p_full[x], lane);
       }
-      if (ok) ok = warp_wait(&o_done[x], uint32_t((tiles - 1) & 1), abort_flag, T);
-      if (!ok) {
-        if (lane == 0) {
-          *abort_flag = 1;
-          set_status(p.status, TSEL_DEV_TIMEOUT);
-        }
-      } else if (any_row) {
-        tc_fence_after();
-        // O' * 2^(vref - 134) / l', both with the same 2^10
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const float vs = __uint_as_float(uint32_t(vref - 7) << 23);
+      if (ok) ok = warp_wait(&o_done[x], uint32_t((n - 1) & 1), abort_flag, T);
+      if (!ok && lane == 0) {
+        *abort_flag = 1;
+        set_status(p.status, TSEL_DEV_TIMEOUT);
+      }
+      if (any_row) {
+        float* sum = s_row + (n & 1) * 2 * kTile;   // the parity that the last tile did not use
+        sum[half * kTile + row] = l;
+        meet();
+        l = half == 0 ? l + sum[kTile + row] : sum[row] + l;
+        if (ok) {
+          tc_fence_after();
+          // O' * 2^(vref - 134) / l', both with the same lift
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          const float vs = __uint_as_float(uint32_t(vref - 7) << 23);
 #pragma unroll
-        for (int cc = 0; cc < D / 16; ++cc) {
-          uint32_t o[16];
-          tmem_ld16(to + cc * 16, o);
-          if (row_ok && l != 0.f) {
-            float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + cc * 16);
+          for (int j8 = 0; j8 < D / 16; ++j8) {
+            const int cc = half * (D / 16) + j8;
+            uint32_t o[8];
+            tmem_ld8(to + cc * 8, o);
+            if (row_ok && l != 0.f) {
+              float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + cc * 8);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              dst[j] = make_float4(__uint_as_float(o[4 * j]) * inv * vs, __uint_as_float(o[4 * j + 1]) * inv * vs,
-                                   __uint_as_float(o[4 * j + 2]) * inv * vs, __uint_as_float(o[4 * j + 3]) * inv * vs);
+              for (int j = 0; j < 2; ++j)
+                dst[j] = make_float4(__uint_as_float(o[4 * j]) * inv * vs, __uint_as_float(o[4 * j + 1]) * inv * vs,
+                                     __uint_as_float(o[4 * j + 2]) * inv * vs, __uint_as_float(o[4 * j + 3]) * inv * vs);
+            }
           }
+          if (row_ok && half == 0) p.part_lse[part] = l == 0.f ? kNegInf : m + (log2f(l) - kAttLift);
         }
-        if (row_ok) p.part_lse[part] = l == 0.f ? kNegInf : m + (log2f(l) - kAttLift);
       }
     }
   } else if (warp < C::CONV_WARP) {
-    // ------------------------------------------------------------ MMA issuers
-    const int xi = warp - C::MMA_WARP;
-    if (lane == 0 && xi < nact) {
+    // ------------------------------------------------------------ MMA issuer
+    // The pipelines take turns: O product of one, then its next S product,
+    // while the other's softmax runs. P lies over S, so the O product must
+    // have read it before the next S product is issued.
+    if (lane == 0) {
       constexpr uint32_t kIdS = idesc_f16_f32(kTile, kTile, false);
       constexpr uint32_t kIdO = idesc_f16_f32(kTile, D, true);
-      const uint32_t ts = tmem + uint32_t(xi * 256), to = ts + 128;
-      const uint32_t sq = smem_u32(smem + C::OFF_Q + xi * C::TILE_BYTES);
-      bool ok = true;
-      int issued = 0;
-      for (int t = 0; t < tiles && ok; ++t) {
-        const int st = t % C::KS;
-        const uint32_t ph = uint32_t((t / C::KS) & 1);
-        // P overwrote S: the previous O product must have read it
-        ok = wait_bounded(&k_full[st], ph, abort_flag, T) &&
-             (t == 0 || wait_bounded(&o_done[xi], uint32_t((t - 1) & 1), abort_flag, T));
-        if (!ok) break;
+      const uint32_t sq0 = smem_u32(smem + C::OFF_Q), sk0 = smem_u32(smem + C::OFF_K),
+                     sv0 = smem_u32(smem + C::OFF_V);
+      auto s_product = [&](int xx, int i) -> bool {
+        const int t = split ? 2 * i + xx : i, st = t % C::KS;
+        if (!wait_bounded(&k_full[st], uint32_t((t / C::KS) & 1), abort_flag, T) ||
+            (i > 0 && !wait_bounded(&o_done[xx], uint32_t((i - 1) & 1), abort_flag, T)))
+          return false;
         tc_fence_after();
-        const uint32_t sk = smem_u32(smem + C::OFF_K + st * C::TILE_BYTES);
+        const uint32_t ts = tmem + uint32_t(xx * 256);
+        const uint32_t sq = sq0 + xx * C::TILE_BYTES, sk = sk0 + st * C::TILE_BYTES;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
           mma_bf16(ts, smem_desc(sq + off, 2, 1024), smem_desc(sk + off, 2, 1024), kIdS, kk > 0);
         }
-        mma_commit(&s_full[xi]);
-        mma_commit(&k_free[st]);
-        ok = wait_bounded(&v_full[st], ph, abort_flag, T) &&
-             wait_bounded(&p_full[xi], uint32_t(t & 1), abort_flag, T);
-        if (!ok) break;
+        mma_commit(&s_full[xx]);
+        if (split || xx == 1) mma_commit(&k_free[st]);   // its last reader
+        return true;
+      };
+      auto o_product = [&](int xx, int i) -> bool {
+        const int t = split ? 2 * i + xx : i, st = t % C::KS;
+        if (!wait_bounded(&v_full[st], uint32_t((t / C::KS) & 1), abort_flag, T) ||
+            !wait_bounded(&p_full[xx], uint32_t(i & 1), abort_flag, T))
+          return false;
         tc_fence_after();
-        const uint32_t sv = smem_u32(smem + C::OFF_V + st * C::TILE_BYTES);
+        const uint32_t ts = tmem + uint32_t(xx * 256), sv = sv0 + st * C::TILE_BYTES;
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_f16_ta(to, ts + kk * 8, smem_desc_mn(sv + kk * 2048, kTile * 128, 1024), kIdO,
-                     t > 0 || kk > 0);
-        mma_commit(&v_free[st]);
-        mma_commit(&o_done[xi]);
-        issued = t + 1;
+          mma_f16_ta(ts + 128, ts + (kk >> 2) * 64 + (kk & 3) * 8,
+                     smem_desc_mn(sv + kk * 2048, kTile * 128, 1024), kIdO, i > 0 || kk > 0);
+        mma_commit(&o_done[xx]);
+        if (split || xx == 1) mma_commit(&v_free[st]);
+        return true;
+      };
+      bool ok = s_product(0, 0) && (n1 == 0 || s_product(1, 0));
+      int done0 = 0, done1 = 0;   // O products issued
+      for (int i = 0; i < n0 && ok; ++i) {
+        ok = o_product(0, i);
+        if (!ok) break;
+        done0 = i + 1;
+        if (i + 1 < n0) ok = s_product(0, i + 1);
+        if (!ok || i >= n1) continue;
+        ok = o_product(1, i);
+        if (!ok) break;
+        done1 = i + 1;
+        if (i + 1 < n1) ok = s_product(1, i + 1);
       }
       if (!ok) {
         *abort_flag = 1;
         set_status(p.status, TSEL_DEV_TIMEOUT);
-        mma_commit(&o_done[xi]);   // one more phase, for whatever is in flight
+        // one more phase, for whatever is in flight
+        mma_commit(&o_done[0]);
+        wait_drain(&o_done[0], uint32_t(done0 & 1), T);
       }
       // every MMA this thread issued has completed before TMEM is freed
-      if (issued > 0) wait_drain(&o_done[xi], uint32_t((issued - 1) & 1), T);
-      if (!ok) wait_drain(&o_done[xi], uint32_t(issued & 1), T);
+      if (done0 > 0 && ok) wait_drain(&o_done[0], uint32_t((done0 - 1) & 1), T);
+      if (done1 > 0) wait_drain(&o_done[1], uint32_t((done1 - 1) & 1), T);
     }
   } else {
     // ------------------------------------------------------------ converters
-    const int grp = NT == 2 ? (warp - C::CONV_WARP) >> 2 : 0;
-    const bool do_k = NT == 1 || grp == 0, do_v = NT == 1 || grp == 1;
+    const bool do_k = warp < C::CONV_WARP + 4;   // four warps for K, four for V
     const int tid = (int(threadIdx.x) - 32 * C::CONV_WARP) & (kTile - 1);
     const int first_page = w.k0 >> p.page_shift;
     const int mask = (1 << p.page_shift) - 1;
+    const int keys = w.k1 - w.k0;
     uint32_t* fac_k = s_fac;
     uint32_t* fac_v = s_fac + 2 * kTile;
-    // row (in rows of head_dim codes) of the key at offset j of the chunk, -1 if none
-    auto cache_row = [&](int j) -> int64_t {
-      const int key = w.k0 + j;
-      if (key >= w.k1) return -1;
-      const int pg = s_pages[(key >> p.page_shift) - first_page];
-      if (pg < 0) return -1;
-      return ((int64_t(pg) * p.Hkv + w.kvh) << p.page_shift) + (key & mask);
-    };
-    uint4 kr[NT == 1 ? C::UPT : 1], vr[NT == 1 ? C::UPT : 1], xr[NT == 2 ? C::UPT : 1];
-    auto load = [&](int t, const uint8_t* pages, uint4* dst) {
+    // Step i of a thread: row 32 * (i % 4) + tid / 4, piece tid % 4 of chunk
+    // i / 4. Four lanes read 64 contiguous bytes of a row; eight lanes store
+    // to two neighbouring rows, whose swizzles differ in the lowest bit, so
+    // the 16-byte halves of their pieces cover all 32 banks.
+    const int r0 = tid >> 2, c0 = tid & 3, sw = r0 & 7;
+    const uint8_t* pages = (do_k ? p.k_pages : p.v_pages) + (int64_t(w.kvh) << p.page_shift) * D + 16 * c0;
+    const uint32_t page_bytes = uint32_t(p.Hkv << p.page_shift) * uint32_t(D);
+    uint4 raw[C::STEPS];   // a tile's codes, loaded one tile ahead
+    auto load = [&](int t) {
 #pragma unroll
-      for (int i = 0; i < C::UPT; ++i) {
-        const int u = i * kTile + tid;
-        const int64_t r = t < tiles ? cache_row(t * kTile + u / C::UPT) : -1;
-        dst[i] = r < 0 ? make_uint4(0, 0, 0, 0)
-                       : __ldg(reinterpret_cast<const uint4*>(pages + r * D) + u % C::UPT);
+      for (int i = 0; i < 4; ++i) {
+        const int j = t * kTile + 32 * i + r0;
+        const int pg = j < keys ? s_pages[((w.k0 + j) >> p.page_shift) - first_page] : -1;
+        const uint8_t* src = pages + uint64_t(uint32_t(pg)) * page_bytes + ((w.k0 + j) & mask) * D;
+#pragma unroll
+        for (int cc = 0; cc < C::DC; ++cc)
+          raw[4 * cc + i] = pg >= 0 && 64 * cc + 16 * c0 < D
+                                ? __ldg(reinterpret_cast<const uint4*>(src + 64 * cc))
+                                : make_uint4(0, 0, 0, 0);
       }
     };
     // exponent bytes of keys 4 * lane .. + 3 of a tile (0 past the end)
     auto load_exps = [&](int t, const uint8_t* exps) -> uint32_t {
       const int j = t * kTile + 4 * lane;
-      const int64_t r = t < tiles ? cache_row(j) : -1;
-      if (r < 0) return 0;
-      uint32_t e = __ldg(reinterpret_cast<const uint32_t*>(exps + r));
-      const int left = w.k1 - (w.k0 + j);   // keys of the four inside the chunk
+      const int pg = j < keys ? s_pages[((w.k0 + j) >> p.page_shift) - first_page] : -1;
+      if (pg < 0) return 0;
+      const int64_t r = ((int64_t(pg) * p.Hkv + w.kvh) << p.page_shift) + ((w.k0 + j) & mask);
+      const uint32_t e = __ldg(reinterpret_cast<const uint32_t*>(exps + r));
+      const int left = keys - j;   // keys of the four inside the chunk
       return left >= 4 ? e : e & ((1u << (8 * left)) - 1u);
     };
-    auto convert = [&](uint8_t* tile, const uint32_t* fac, const uint4* src) {
+    auto convert = [&](uint8_t* tile, const uint32_t* fac) {
+      uint8_t* lo_at = tile + r0 * 128 + (((2 * c0) ^ sw) << 4);
+      uint8_t* hi_at = tile + r0 * 128 + (((2 * c0 + 1) ^ sw) << 4);
 #pragma unroll
-      for (int i = 0; i < C::UPT; ++i) {
-        const int u = i * kTile + tid;
-        const int r = u / C::UPT, cu = u % C::UPT;   // row; 16-element piece of it
-        const uint32_t f = fac[r];
-        uint4 lo, hi;
-        lo.x = unpack_e4m3(src[i].x & 0xFFFFu, f);
-        lo.y = unpack_e4m3(src[i].x >> 16, f);
-        lo.z = unpack_e4m3(src[i].y & 0xFFFFu, f);
-        lo.w = unpack_e4m3(src[i].y >> 16, f);
-        hi.x = unpack_e4m3(src[i].z & 0xFFFFu, f);
-        hi.y = unpack_e4m3(src[i].z >> 16, f);
-        hi.z = unpack_e4m3(src[i].w & 0xFFFFu, f);
-        hi.w = unpack_e4m3(src[i].w >> 16, f);
-        uint8_t* base = tile + (cu >> 2) * (kTile * 128) + r * 128;
-        const int j0 = 2 * (cu & 3), sw = r & 7;
-        // the lanes of the second 64 columns store their halves the other way
-        // round, so that eight lanes cover all 32 banks
-        const bool flip = (cu >> 2) != 0;
-        const int ja = (j0 + (flip ? 1 : 0)) ^ sw, jb = (j0 + (flip ? 0 : 1)) ^ sw;
-        *reinterpret_cast<uint4*>(base + (ja << 4)) = flip ? hi : lo;
-        *reinterpret_cast<uint4*>(base + (jb << 4)) = flip ? lo : hi;
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t f = fac[32 * i + r0];
+#pragma unroll
+        for (int cc = 0; cc < C::DC; ++cc) {
+          const uint4 u = raw[4 * cc + i];
+          if (64 * cc + 16 * c0 < D) {
+            const int at = cc * (kTile * 128) + i * (32 * 128);
+            *reinterpret_cast<uint4*>(lo_at + at) =
+                make_uint4(unpack_e4m3(u.x & 0xFFFFu, f), unpack_e4m3(u.x >> 16, f),
+                           unpack_e4m3(u.y & 0xFFFFu, f), unpack_e4m3(u.y >> 16, f));
+            *reinterpret_cast<uint4*>(hi_at + at) =
+                make_uint4(unpack_e4m3(u.z & 0xFFFFu, f), unpack_e4m3(u.z >> 16, f),
+                           unpack_e4m3(u.w & 0xFFFFu, f), unpack_e4m3(u.w >> 16, f));
+          }
+        }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
     };
     uint32_t ke = do_k ? load_exps(0, p.k_exps) : 0u, ve = load_exps(0, p.v_exps);
-    if (NT == 1) {
-      load(0, p.k_pages, kr);
-      load(0, p.v_pages, vr);
-    } else {
-      load(0, do_k ? p.k_pages : p.v_pages, xr);
-    }
+    load(0);
     int vref = 0;
     bool ok = true;
     for (int t = 0; t < tiles; ++t) {
@@ -632,29 +691,21 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::THREADS, NT == 1 ? 2 : 1)
           meta.v_ref = vref;
         }
       }
-      if (do_v) fac_v[par * kTile + tid] = vb == 255u ? 0u : att_factor(int(vb), vref);
+      if (!do_k) fac_v[par * kTile + tid] = vb == 255u ? 0u : att_factor(int(vb), vref);
       // the factors of the next tile go to the other half, so one barrier will do
-      if (NT == 1 || grp == 0)
+      if (do_k)
         asm volatile("bar.sync 1, 128;" ::: "memory");
       else
         asm volatile("bar.sync 2, 128;" ::: "memory");
       ke = do_k ? load_exps(t + 1, p.k_exps) : 0u;
       ve = load_exps(t + 1, p.v_exps);
-      if (do_k) {
-        if (t >= C::KS) ok = ok && warp_wait(&k_free[st], uint32_t(((t - C::KS) / C::KS) & 1), abort_flag, T);
-        if (ok) {
-          convert(smem + C::OFF_K + st * C::TILE_BYTES, fac_k + par * kTile, NT == 1 ? kr : xr);
-          mbar_arrive_lane0(&k_full[st], lane);
-          load(t + 1, p.k_pages, NT == 1 ? kr : xr);
-        }
-      }
-      if (do_v) {
-        if (t >= C::KS) ok = ok && warp_wait(&v_free[st], uint32_t(((t - C::KS) / C::KS) & 1), abort_flag, T);
-        if (ok) {
-          convert(smem + C::OFF_V + st * C::TILE_BYTES, fac_v + par * kTile, NT == 1 ? vr : xr);
-          mbar_arrive_lane0(&v_full[st], lane);
-          load(t + 1, p.v_pages, NT == 1 ? vr : xr);
-        }
+      uint64_t* full = do_k ? k_full : v_full;
+      uint64_t* free_ = do_k ? k_free : v_free;
+      if (t >= C::KS) ok = ok && warp_wait(&free_[st], uint32_t(((t - C::KS) / C::KS) & 1), abort_flag, T);
+      if (ok) {
+        convert(smem + (do_k ? C::OFF_K : C::OFF_V) + st * C::TILE_BYTES, (do_k ? fac_k : fac_v) + par * kTile);
+        mbar_arrive_lane0(&full[st], lane);
+        load(t + 1);
       }
     }
     if (!ok && lane == 0) {
@@ -667,7 +718,7 @@ __global__ void __launch_bounds__(AttCfg<D, NT>::THREADS, NT == 1 ? 2 : 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == C::MMA_WARP) tmem_dealloc(tmem, C::TMEM_COLS);
+  if (warp == C::MMA_WARP) tmem_dealloc(tmem, 512);
 }
 
 // Joins a row's partial results: out = sum_c 2^(lse_c - lse) o_c, in chunk
@@ -727,10 +778,10 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttParams p) {
   }
 }
 
-template <int D, int NT>
+template <int D>
 cudaError_t launch_attend_t(const AttParams& p, int64_t units, cudaStream_t stream) {
-  using C = AttCfg<D, NT>;
-  auto kern = attend_kernel<D, NT>;
+  using C = AttCfg<D>;
+  auto kern = attend_kernel<D>;
   static bool attr_set[128] = {};   // per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -745,22 +796,15 @@ cudaError_t launch_attend_t(const AttParams& p, int64_t units, cudaStream_t stre
 
 }  // namespace
 
-cudaError_t launch_attend(int head_dim, int row_tiles, const AttParams& p, int64_t units,
-                          cudaStream_t stream) {
-#define TSEL_ATT_CASE(DD)                                                        \
-  case DD:                                                                       \
-    return row_tiles == 2 ? launch_attend_t<DD, 2>(p, units, stream)             \
-                          : launch_attend_t<DD, 1>(p, units, stream);
+cudaError_t launch_attend(int head_dim, const AttParams& p, int64_t units, cudaStream_t stream) {
   switch (head_dim) {
-    TSEL_ATT_CASE(64)
-    TSEL_ATT_CASE(80)
-    TSEL_ATT_CASE(96)
-    TSEL_ATT_CASE(112)
-    TSEL_ATT_CASE(128)
-    default:
-      return cudaErrorInvalidValue;
+    case 64: return launch_attend_t<64>(p, units, stream);
+    case 80: return launch_attend_t<80>(p, units, stream);
+    case 96: return launch_attend_t<96>(p, units, stream);
+    case 112: return launch_attend_t<112>(p, units, stream);
+    case 128: return launch_attend_t<128>(p, units, stream);
+    default: return cudaErrorInvalidValue;
   }
-#undef TSEL_ATT_CASE
 }
 
 cudaError_t launch_attend_join(int head_dim, const AttParams& p, int num_sms, cudaStream_t stream) {

@@ -13,22 +13,20 @@ namespace tsel {
 constexpr int kAttMaxChunkKeys = 8192;   // keys of one unit: bounds its page list in shared memory
 constexpr int kAttMinPage = 16;
 constexpr int kAttMaxPages = kAttMaxChunkKeys / kAttMinPage;
-// CTAs resident at once on the 152 SMs, one or two 128-row tiles per CTA. A
-// constant, not a query: the workspace size must follow from the sizes alone.
-constexpr int kAttCtas1 = 304;
-constexpr int kAttCtas2 = 152;
+// CTAs resident at once, one per SM. A constant, not a query: the workspace
+// size must follow from the sizes alone.
+constexpr int kAttCtas = 152;
 
 // How a call is cut into units: (key chunk, KV head, row tiles) of the prefix,
 // and (request, KV head, row tile, key chunk) of the suffixes.
 struct AttPlan {
   int G;        // query heads per KV head
   int tt;       // tokens per 128-row tile
-  int nt;       // row tiles per CTA of the prefix units (1 or 2)
-  int ntg;      // row-tile groups over all rows
+  int ntg;      // pairs of row tiles over all rows
   int nc, lp;   // prefix chunks and keys per chunk
-  int qt;       // row tiles of one request
+  int qt;       // pairs of row tiles of one request
   int sc, ls;   // suffix chunks and keys per chunk
-  int slots;    // partial results per row
+  int slots;    // partial results per row: two for each chunk
   int64_t units_p, units_s;
   int64_t lse_off, o_off, total;   // workspace
 };
@@ -61,17 +59,15 @@ inline AttPlan att_plan(int R, int Tq, int max_q, int H, int Hkv, int d, int max
   AttPlan a{};
   a.G = H / Hkv;
   a.tt = kTile / a.G;
-  const int tiles_q = int(ceil_div(Tq, a.tt));
-  a.nt = tiles_q > 1 ? 2 : 1;
-  a.ntg = int(ceil_div(tiles_q, a.nt));
+  a.ntg = int(ceil_div(Tq, 2 * a.tt));
   const int kp = int(ceil_div(max_prefix, kTile));
   const int ks = int(ceil_div(max_suffix, kTile));
-  a.qt = int(ceil_div(max_q, a.tt));
-  if (Tq > 0) a.nc = att_chunks(int64_t(Hkv) * a.ntg, kp, a.nt == 2 ? kAttCtas2 : kAttCtas1);
+  a.qt = int(ceil_div(max_q, 2 * a.tt));
+  if (Tq > 0) a.nc = att_chunks(int64_t(Hkv) * a.ntg, kp, kAttCtas);
   if (a.nc > 0) a.lp = int(ceil_div(kp, a.nc)) * kTile;
-  if (Tq > 0 && R > 0 && a.qt > 0) a.sc = att_chunks(int64_t(R) * Hkv * a.qt, ks, kAttCtas1);
+  if (Tq > 0 && R > 0 && a.qt > 0) a.sc = att_chunks(int64_t(R) * Hkv * a.qt, ks, kAttCtas);
   if (a.sc > 0) a.ls = int(ceil_div(ks, a.sc)) * kTile;
-  a.slots = a.nc + a.sc;
+  a.slots = 2 * (a.nc + a.sc);
   a.units_p = int64_t(a.nc) * Hkv * a.ntg;
   a.units_s = int64_t(R) * Hkv * a.qt * a.sc;
   a.lse_off = kWsHeaderBytes;
@@ -111,8 +107,7 @@ struct AttParams {
   uint64_t timeout_ns;
 };
 
-cudaError_t launch_attend(int head_dim, int row_tiles, const AttParams& p, int64_t units,
-                          cudaStream_t stream);
+cudaError_t launch_attend(int head_dim, const AttParams& p, int64_t units, cudaStream_t stream);
 cudaError_t launch_attend_join(int head_dim, const AttParams& p, int num_sms, cudaStream_t stream);
 
 }  // namespace tsel

@@ -348,7 +348,7 @@ tsel_status tsel_prefix_attention(
                              max_prefix_len, max_suffix_len);
   if (workspace_bytes < size_t(a.total))
     return fail(TSEL_ERR_WORKSPACE, "workspace %zu < %lld bytes", workspace_bytes, (long long)a.total);
-  if (a.units_p > 0x7FFFFFFFll || a.units_s > 0x7FFFFFFFll)
+  if (a.units_p + a.units_s > 0x7FFFFFFFll)
     return fail(TSEL_ERR_UNSUPPORTED, "too many units of work");
   if (total_q == 0) return TSEL_OK;
   AttParams p{};
@@ -400,18 +400,8 @@ tsel_status tsel_prefix_attention(
   p.status = &reinterpret_cast<WsHeader*>(ws)->status;
   p.timeout_ns = device_wait_timeout_ns();
   cudaError_t e;
-  if (a.nt == 2) {
-    if (a.units_p > 0) {
-      e = launch_attend(head_dim, 2, p, a.units_p, stream);
-      if (e != cudaSuccess) return cuda_fail(e, "prefix attention launch");
-    }
-    if (a.units_s > 0) {
-      p.unit0 = a.units_p;
-      e = launch_attend(head_dim, 1, p, a.units_s, stream);
-      if (e != cudaSuccess) return cuda_fail(e, "suffix attention launch");
-    }
-  } else if (a.units_p + a.units_s > 0) {
-    e = launch_attend(head_dim, 1, p, a.units_p + a.units_s, stream);
+  if (a.units_p + a.units_s > 0) {
+    e = launch_attend(head_dim, p, a.units_p + a.units_s, stream);
     if (e != cudaSuccess) return cuda_fail(e, "attention launch");
   }
   e = launch_attend_join(head_dim, p, sms, stream);

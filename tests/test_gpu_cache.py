@@ -8,7 +8,8 @@ Cache: exact on given rows. Attention: with A = sum_j p_j |v_j| (columnwise) and
 delta the error of a logit (fp32 sums of d products, 2^-23 of their absolute sum
 each, at most d of them), the probabilities are within delta + 2^-11 (fp16) +
 2^-20 (exp2, sums, joining), so out is within A * (2 delta + 2^-11 + 2^-19) plus
-n * 2^-33 max|v| for probabilities below fp16's range plus half a step of the
+n * 2^-31 max|v| for probabilities below fp16's range (its smallest step, 2^-24,
+halved, against 2^6 at the row's reference, which is at most its maximum) plus half a step of the
 output; lse within delta + 2^-20 + |lse| 2^-22."""
 import numpy as np
 import pytest
@@ -356,7 +357,7 @@ class Batch:
         delta = self.d * 2.0 ** -23 * mag + 2.0 ** -22
         vmax = np.nanmax(np.abs(self.v)) if np.isfinite(self.v).any() else 0.0
         n = self.prefix + max(self.lens + [0])
-        tol = av * (2 * delta[..., None] + 2.0 ** -11 + 2.0 ** -19) + n * 2.0 ** -33 * vmax
+        tol = av * (2 * delta[..., None] + 2.0 ** -11 + 2.0 ** -19) + n * 2.0 ** -31 * vmax
         tol = tol + (np.abs(ref) + tol) * _half(self.dtype)
         got, gl = _np(out)[:T], _np(lse)[:, :T]
         fin = np.isfinite(ref)
