@@ -527,26 +527,52 @@ def tsel_gather_compact_counted(hidden: torch.Tensor, pos: Optional[torch.Tensor
 # Rotary positions with several axes
 # ---------------------------------------------------------------------------
 
+# The calls below are made once per layer and decoding step, where the host's
+# share counts: the checks are plain comparisons, and the device is switched and
+# the stream looked up in the cheapest way there is.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _call(fn, device: torch.device, stream, *args) -> None:
+    """fn(*args, stream) on `device` (the library works on the current device)."""
+    index = device.index
+    if stream is None and _raw_stream is not None:
+        handle = _raw_stream(index)
+    else:
+        handle = _stream(stream, device)
+    if torch.cuda.current_device() == index:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, handle)
+    if st != TSEL_OK:
+        _check(st)
+
+
 def _rows(t: torch.Tensor, name: str, device=None, dtype=None, shape=None) -> int:
-    """Checks a [rows, heads, head_dim] tensor; returns its row stride."""
+    """Checks a [rows, heads, head_dim] tensor; returns its row stride (0: dense)."""
+    have = t.shape
     if not t.is_cuda or t.dtype not in _DTYPES:
         raise TypeError(f"{name} must be a CUDA bf16, fp16 or fp32 tensor")
-    if t.dim() != 3:
+    if len(have) != 3:
         raise ValueError(f"{name} must be a [rows, heads, head_dim] tensor")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and have != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    n, h, d = t.shape
+    if t.is_contiguous():
+        return 0
+    n, h, d = have
     if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
         raise ValueError(f"{name} must have contiguous [heads, head_dim] rows")
     return t.stride(0) if n > 1 else 0
 
 
 def _vector(t: torch.Tensor, dtype, name: str, device, numel: Optional[int] = None) -> None:
-    _need(t, dtype, name)
+    if t.dtype != dtype or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA {dtype} tensor")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
     if not t.is_contiguous():
@@ -609,29 +635,28 @@ def tsel_rope(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, tab
     """Rotates q [T, H, d] and k [T, Hkv, d] (or None) by positions pos int32 [T, axes];
     returns (q_out, k_out), which may be q and k themselves. With
     TSEL_ROPE_INVERSE it turns gradients of the outputs into those of the inputs."""
-    dev = q.device
-    total, H, d = q.shape if q.dim() == 3 else (0, 0, 0)
+    dev, dtype = q.device, q.dtype
     qs = _rows(q, "q")
+    total, H, d = q.shape
     Hkv = ks = 0
     if k is not None:
-        Hkv = k.shape[1] if k.dim() == 3 else 0
-        ks = _rows(k, "k", dev, q.dtype, (total, Hkv, d))
+        ks = _rows(k, "k", dev, dtype)
+        Hkv = k.shape[1]
+        if k.shape != (total, Hkv, d):
+            raise ValueError("q and k must have the same rows and head_dim")
     elif k_out is not None:
         raise ValueError("k_out without k")
     pos_p, pos_dim, table_p, pairs = _rope_args(pos, table, total, dev)
-    qos = 0 if q_out is None else _rows(q_out, "q_out", dev, q.dtype, (total, H, d))
-    kos = 0 if k_out is None else _rows(k_out, "k_out", dev, q.dtype, (total, Hkv, d))
+    qos = 0 if q_out is None else _rows(q_out, "q_out", dev, dtype, (total, H, d))
+    kos = 0 if k_out is None else _rows(k_out, "k_out", dev, dtype, (total, Hkv, d))
     if q_out is None:
-        q_out = torch.empty((total, H, d), dtype=q.dtype, device=dev)
+        q_out = torch.empty((total, H, d), dtype=dtype, device=dev)
     if k is not None and k_out is None:
-        k_out = torch.empty((total, Hkv, d), dtype=q.dtype, device=dev)
+        k_out = torch.empty((total, Hkv, d), dtype=dtype, device=dev)
     workspace = _workspace(workspace, 1024, dev)
-    with torch.cuda.device(dev):
-        st = load_library().tsel_rope(
-            q.data_ptr(), qs, _ptr(k), ks, pos_p, pos_dim, table_p, pairs, total, H, Hkv, d,
-            _DTYPES[q.dtype], int(flags), q_out.data_ptr(), qos, _ptr(k_out), kos,
-            workspace.data_ptr(), workspace.numel(), _stream(stream, dev))
-    _check(st)
+    _call(load_library().tsel_rope, dev, stream, q.data_ptr(), qs, _ptr(k), ks, pos_p, pos_dim,
+          table_p, pairs, total, H, Hkv, d, _DTYPES[dtype], flags, q_out.data_ptr(), qos,
+          _ptr(k_out), kos, workspace.data_ptr(), workspace.numel())
     return q_out, k_out
 
 
@@ -658,15 +683,16 @@ def tsel_cache_new(num_pages: int, page_size: int, num_kv_heads: int, head_dim: 
 
 def _cache_args(cache: TselCache, device):
     """(pointers and sizes of the C calls, Hkv, d) of a cache."""
-    shape = cache.k_pages.shape
+    kp, vp, ke, ve = cache
+    for t, name in ((kp, "k_pages"), (vp, "v_pages"), (ke, "k_exps"), (ve, "v_exps")):
+        _vector(t, torch.uint8, name, device)
+    shape = kp.shape
     if len(shape) != 4:
         raise ValueError("k_pages must be a uint8 [pages, heads, page_size, head_dim] tensor")
-    for name in TselCache._fields:
-        t = getattr(cache, name)
-        _vector(t, torch.uint8, name, device)
-        if tuple(t.shape) != tuple(shape if name.endswith("pages") else shape[:3]):
-            raise ValueError(f"{name} does not match k_pages")
-    return ([t.data_ptr() for t in cache], shape[0], shape[2]), shape[1], shape[3]
+    pages, heads, page_size, d = shape
+    if vp.shape != shape or ke.shape != (pages, heads, page_size) or ve.shape != ke.shape:
+        raise ValueError("the cache's tensors do not match one another")
+    return (kp.data_ptr(), vp.data_ptr(), ke.data_ptr(), ve.data_ptr(), pages, page_size), heads, d
 
 
 def tsel_cache_workspace_size() -> int:
@@ -678,22 +704,19 @@ def tsel_cache_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cach
                      flags: int = 0, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """Quantises k and v [T, Hkv, d] into the cache's slots (int32 [T], negative:
     skipped); with a rope table and positions k is rotated on its way."""
-    dev = k.device
+    dev, dtype = k.device, k.dtype
     ks = _rows(k, "k")
     total, Hkv, d = k.shape
-    vs = _rows(v, "v", dev, k.dtype, (total, Hkv, d))
-    (ptrs, pages, page_size), ch, cd = _cache_args(cache, dev)
-    if (ch, cd) != (Hkv, d):
+    vs = _rows(v, "v", dev, dtype, (total, Hkv, d))
+    cache_p, ch, cd = _cache_args(cache, dev)
+    if ch != Hkv or cd != d:
         raise ValueError("k and v do not match the cache's heads and head_dim")
     _vector(slots, torch.int32, "slots", dev, total)
     pos_p, pos_dim, table_p, pairs = _rope_args(pos, table, total, dev)
     workspace = _workspace(workspace, 1024, dev)
-    with torch.cuda.device(dev):
-        st = load_library().tsel_cache_write(
-            k.data_ptr(), ks, v.data_ptr(), vs, pos_p, pos_dim, table_p, pairs, slots.data_ptr(),
-            total, Hkv, d, _DTYPES[k.dtype], int(flags), *ptrs, pages, page_size,
-            workspace.data_ptr(), workspace.numel(), _stream(stream, dev))
-    _check(st)
+    _call(load_library().tsel_cache_write, dev, stream, k.data_ptr(), ks, v.data_ptr(), vs, pos_p,
+          pos_dim, table_p, pairs, slots.data_ptr(), total, Hkv, d, _DTYPES[dtype], flags, *cache_p,
+          workspace.data_ptr(), workspace.numel())
 
 
 def tsel_cache_read(cache: TselCache, slots: torch.Tensor, *, dtype=torch.bfloat16,
@@ -702,7 +725,7 @@ def tsel_cache_read(cache: TselCache, slots: torch.Tensor, *, dtype=torch.bfloat
                     stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Reads slots (int32 [T], negative: zeros) back as k and v [T, Hkv, d] of dtype."""
     dev = cache.k_pages.device
-    (ptrs, pages, page_size), Hkv, d = _cache_args(cache, dev)
+    cache_p, Hkv, d = _cache_args(cache, dev)
     _vector(slots, torch.int32, "slots", dev)
     if dtype not in _DTYPES:
         raise TypeError("dtype must be bf16, fp16 or fp32")
@@ -714,12 +737,9 @@ def tsel_cache_read(cache: TselCache, slots: torch.Tensor, *, dtype=torch.bfloat
     if v_out is None:
         v_out = torch.empty(shape, dtype=dtype, device=dev)
     workspace = _workspace(workspace, 1024, dev)
-    with torch.cuda.device(dev):
-        st = load_library().tsel_cache_read(
-            *ptrs, pages, page_size, slots.data_ptr(), shape[0], Hkv, d, _DTYPES[dtype],
-            k_out.data_ptr(), kos, v_out.data_ptr(), vos, workspace.data_ptr(), workspace.numel(),
-            _stream(stream, dev))
-    _check(st)
+    _call(load_library().tsel_cache_read, dev, stream, *cache_p, slots.data_ptr(), shape[0], Hkv, d,
+          _DTYPES[dtype], k_out.data_ptr(), kos, v_out.data_ptr(), vos, workspace.data_ptr(),
+          workspace.numel())
     return k_out, v_out
 
 
@@ -756,7 +776,8 @@ def tsel_prefix_attention(q: torch.Tensor, cu_seqlens_q: torch.Tensor, max_seqle
     if q.dtype == torch.float32:
         raise TypeError("q must be bf16 or fp16")
     tq, H, d = q.shape
-    (ptrs, pages, page_size), Hkv, cd = _cache_args(cache, dev)
+    cache_p, Hkv, cd = _cache_args(cache, dev)
+    page_size = cache_p[5]
     if cd != d:
         raise ValueError("q does not match the cache's head_dim")
     _vector(cu_seqlens_q, torch.int32, "cu_seqlens_q", dev)
@@ -795,14 +816,12 @@ def tsel_prefix_attention(q: torch.Tensor, cu_seqlens_q: torch.Tensor, max_seqle
         lse = torch.empty((H, tq), dtype=torch.float32, device=dev)
     if workspace is None:
         workspace = _new_workspace(tsel_prefix_attention_workspace_size(R, tq, max_seqlen_q, H, Hkv, d, max_p, max_s), dev)
-    with torch.cuda.device(dev):
-        st = load_library().tsel_prefix_attention(
-            q.data_ptr(), qs, cu_seqlens_q.data_ptr(), R, tq, int(max_seqlen_q), *ptrs, pages, page_size,
-            _ptr(prefix_pages) if max_p > 0 else None, _ptr(prefix_len) if max_p > 0 else None, max_p,
-            _ptr(page_table) if table_stride else None, table_stride, _ptr(suffix_lens) if table_stride else None,
-            max_s, H, Hkv, d, _DTYPES[q.dtype], float(softmax_scale), out.data_ptr(), os_, _ptr(lse),
-            workspace.data_ptr(), workspace.numel(), _stream(stream, dev))
-    _check(st)
+    _call(load_library().tsel_prefix_attention, dev, stream, q.data_ptr(), qs,
+          cu_seqlens_q.data_ptr(), R, tq, max_seqlen_q, *cache_p,
+          _ptr(prefix_pages) if max_p > 0 else None, _ptr(prefix_len) if max_p > 0 else None, max_p,
+          _ptr(page_table) if table_stride else None, table_stride,
+          _ptr(suffix_lens) if table_stride else None, max_s, H, Hkv, d, _DTYPES[q.dtype],
+          softmax_scale, out.data_ptr(), os_, _ptr(lse), workspace.data_ptr(), workspace.numel())
     return out, lse
 
 

@@ -9,10 +9,11 @@
 // its transpose, so it is also the gradient.
 //
 // HBM-bound: every element is read once and written once. A warp takes one
-// token (or a share of its heads when there are few tokens); a lane keeps the
-// cosines and sines of its pairs and walks the token's heads with them, the
-// loads of up to four rows issued before their stores. The angles are computed
-// once per token and lane, not per head.
+// token (or a share of its heads when there are few tokens); its lanes compute
+// the token's angles once, into shared memory, while the first rows are on
+// their way. The rows are then cut into pieces of two halves of up to 16 bytes
+// that go round the lanes, so no lane idles whatever the head dimension, up to
+// three pieces loaded before the first is stored.
 #include "launch_util.cuh"
 #include "rope.cuh"
 
@@ -21,80 +22,72 @@ namespace tsel {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeRows = 4;   // rows a lane loads before it stores any
+constexpr int kRopeWarps = kRopeThreads / 32;
 
 template <typename T, int V>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const RopeParams p) {
+  constexpr int kRopeBatch = sizeof(T) * V > 16 ? 2 : 3;   // pieces a lane loads before it stores any
+  __shared__ __align__(16) float s_cs[kRopeWarps][2 * kRopeMaxPairs];
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = int64_t(blockIdx.x) * kRopeWarps + warp;   // token; blockIdx.y: share of its heads
+  if (t >= p.total) return;
   const int items = p.d / (2 * V);
-  int lpr = 1;   // lanes per row
-  while (lpr < items && lpr < 32) lpr <<= 1;
-  const int sub = lane / lpr, subs = 32 / lpr, l0 = lane % lpr;
   const int rows = p.H + p.Hkv;
-  const int per = (rows + p.parts - 1) / p.parts;
-  const int64_t units = int64_t(p.total) * p.parts;
-  const int64_t nwarps = int64_t(gridDim.x) * (kRopeThreads / 32);
-  const T* q = static_cast<const T*>(p.q);
-  const T* k = static_cast<const T*>(p.k);
-  T* qo = static_cast<T*>(p.q_out);
-  T* ko = static_cast<T*>(p.k_out);
-  for (int64_t u = (int64_t(blockIdx.x) * kRopeThreads + threadIdx.x) >> 5; u < units; u += nwarps) {
-    const int64_t t = u / p.parts;
-    const int r0 = int(u % p.parts) * per;
-    const int r1 = min(r0 + per, rows);
-    for (int item = l0; item < items; item += lpr) {
-      int o1, o2;
-      rope_item(item, V, p.num_pairs, p.adjacent != 0, o1, o2);
-      const bool turned = item * V < p.num_pairs;
-      float c[V], s[V];
+  const int r0 = int(blockIdx.y) * p.per;
+  const int pieces = max(min(p.per, rows - r0), 0) * items;
+  float* cs = s_cs[warp];
+  const bool adjacent = p.adjacent != 0;
+  const int gap = adjacent ? V : p.num_pairs;   // from a turned piece's first half to its second
+  // row r of the token: q rows first, then k rows (their base is H rows back)
+  const T* q = static_cast<const T*>(p.q) + t * p.q_stride;
+  const T* k = static_cast<const T*>(p.k) + (t * p.k_stride - int64_t(p.H) * p.d);
+  T* qo = static_cast<T*>(p.q_out) + t * p.q_out_stride;
+  T* ko = static_cast<T*>(p.k_out) + (t * p.k_out_stride - int64_t(p.H) * p.d);
+  const int k_from = p.H * p.d;
+  const float inv_items = 1.f / float(items);
+  // rounds of at most kRopeBatch pieces per lane, of equal size
+  const int steps = (pieces + 31) >> 5, rounds = (steps + kRopeBatch - 1) / kRopeBatch;
+  const int batch = rounds > 0 ? (steps + rounds - 1) / rounds : 0;
+  for (int round = 0; round < rounds; ++round) {
+    Vec<T, V> a[kRopeBatch], b[kRopeBatch];
+    int item[kRopeBatch], off[kRopeBatch];   // off: of the first half, in the token's rows; -1 none
+#pragma unroll
+    for (int i = 0; i < kRopeBatch; ++i) {
+      const int n = (round * batch + i) * 32 + lane;
+      off[i] = -1;
+      if (i < batch && n < pieces) {
+        const int rr = int((float(n) + 0.5f) * inv_items);   // n / items: both below 2^16
+        item[i] = n - rr * items;
+        const bool turned = item[i] * V < p.num_pairs;
+        off[i] = (r0 + rr) * p.d + item[i] * (turned && !adjacent ? V : 2 * V);
+        const T* src = (off[i] < k_from ? q : k) + off[i];
+        a[i].load(src);
+        b[i].load(src + (turned ? gap : V));
+      }
+    }
+    if (round == 0) {   // the angles, while the first rows are on their way
+      if (rope_angles(cs, p.table, p.num_pairs, p.pos + t * p.pos_dim, p.pos_dim, p.inverse ? -1.f : 1.f))
+        set_status(p.status, TSEL_DEV_POSITIONS);
+      __syncwarp();
+    }
+#pragma unroll
+    for (int i = 0; i < kRopeBatch; ++i) {
+      if (off[i] < 0) continue;
+      const bool turned = item[i] * V < p.num_pairs;
       if (turned) {
-        bool bad = false;
-        rope_angles<V>(p.table, item, p.pos + t * p.pos_dim, p.pos_dim, c, s, bad);
-        if (bad) set_status(p.status, TSEL_DEV_POSITIONS);
-        if (p.inverse) {
-#pragma unroll
-          for (int j = 0; j < V; ++j) s[j] = -s[j];
-        }
+        float c[V], s[V], fa[V], fb[V];
+        rope_fetch<V>(cs, item[i], c, s);
+        a[i].get(fa);
+        b[i].get(fb);
+        rope_turn<V>(fa, fb, c, s, adjacent);
+        a[i].set(fa);
+        b[i].set(fb);
       }
-      for (int base = r0 + sub; base < r1; base += subs * kRopeRows) {
-        Vec<T, V> a[kRopeRows], b[kRopeRows];
-#pragma unroll
-        for (int i = 0; i < kRopeRows; ++i) {
-          const int r = base + i * subs;
-          if (r < r1) {
-            const T* src = r < p.H ? q + t * p.q_stride + int64_t(r) * p.d
-                                   : k + t * p.k_stride + int64_t(r - p.H) * p.d;
-            a[i].load(src + o1);
-            b[i].load(src + o2);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kRopeRows; ++i) {
-          const int r = base + i * subs;
-          if (r < r1) {
-            if (turned) {
-              float fa[V], fb[V];
-#pragma unroll
-              for (int j = 0; j < V; ++j) {
-                fa[j] = to_f32(a[i].e[j]);
-                fb[j] = to_f32(b[i].e[j]);
-              }
-              rope_turn<V>(fa, fb, c, s, p.adjacent != 0);
-#pragma unroll
-              for (int j = 0; j < V; ++j) {
-                a[i].e[j] = from_f32<T>(fa[j]);
-                b[i].e[j] = from_f32<T>(fb[j]);
-              }
-            }
-            T* dst = r < p.H ? qo + t * p.q_out_stride + int64_t(r) * p.d
-                             : ko + t * p.k_out_stride + int64_t(r - p.H) * p.d;
-            a[i].store(dst + o1);
-            b[i].store(dst + o2);
-          }
-        }
-      }
+      T* dst = (off[i] < k_from ? qo : ko) + off[i];
+      a[i].store(dst);
+      b[i].store(dst + (turned ? gap : V));
     }
   }
 }
@@ -102,19 +95,16 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
 template <typename T, int V>
 cudaError_t launch_rope_t(RopeParams p, int num_sms, cudaStream_t stream) {
   // Enough warps to fill the device from few tokens: a token's heads are
-  // shared out until there are about 16 warps per SM, each with a row or more
-  // per lane group.
+  // shared out until there are about 16 warps per SM, each with a piece or more
+  // per lane.
   const int rows = p.H + p.Hkv;
-  int lpr = 1;
-  while (lpr < p.d / (2 * V) && lpr < 32) lpr <<= 1;
-  const int max_parts = int(ceil_div(rows, 32 / lpr));
+  const int max_parts = int(ceil_div(int64_t(rows) * (p.d / (2 * V)), 32));
   const int64_t want = ceil_div(int64_t(num_sms) * 16, p.total);
-  p.parts = int(want < 1 ? 1 : (want > max_parts ? max_parts : want));
-  const int64_t warps = int64_t(p.total) * p.parts;
-  int64_t blocks = ceil_div(warps, kRopeThreads / 32);
-  const int64_t most = int64_t(num_sms) * 8;
-  if (blocks > most) blocks = most;
-  return launch_kernel(rope_kernel<T, V>, dim3(unsigned(blocks)), kRopeThreads, 0, stream, 1, p);
+  int parts = int(want < 1 ? 1 : (want > max_parts ? max_parts : want));
+  if (parts > rows) parts = rows;
+  p.per = int(ceil_div(rows, parts));
+  const dim3 grid(unsigned(ceil_div(p.total, kRopeWarps)), unsigned(ceil_div(rows, p.per)));
+  return launch_kernel(rope_kernel<T, V>, grid, kRopeThreads, 0, stream, 1, p);
 }
 
 template <typename T>

@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 
@@ -54,6 +55,29 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { retu
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
 
+// Two 16-bit values in one word (the first in the low half).
+template <typename T>
+__device__ __forceinline__ void to_f32x2(uint32_t w, float& x, float& y) {
+  if constexpr (sizeof(T) == 2) {
+    if constexpr (std::is_same<T, __half>::value) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+      x = f.x, y = f.y;
+    } else {
+      x = __uint_as_float(w << 16);
+      y = __uint_as_float(w & 0xFFFF0000u);
+    }
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint32_t from_f32x2(float x, float y) {
+  uint32_t r = 0;
+  if constexpr (std::is_same<T, __half>::value)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(y), "f"(x));
+  return r;
+}
+
 template <int BYTES>
 struct Piece;
 template <>
@@ -73,11 +97,31 @@ struct Vec {
   static constexpr int PIECE = BYTES < 16 ? BYTES : 16;
   static constexpr int N = BYTES / PIECE;
   using P = typename Piece<PIECE>::type;
+  static constexpr bool WORDS = sizeof(T) == 2 && V >= 2;   // 16-bit types: converted two at a time
   union {
     P p[N];
     T e[V];
+    uint32_t w[WORDS ? V / 2 : 1];
   };
   __device__ __forceinline__ Vec() {}
+  __device__ __forceinline__ void get(float (&f)[V]) const {
+    if constexpr (WORDS) {
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) to_f32x2<T>(w[i], f[2 * i], f[2 * i + 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = to_f32(e[i]);
+    }
+  }
+  __device__ __forceinline__ void set(const float (&f)[V]) {
+    if constexpr (WORDS) {
+#pragma unroll
+      for (int i = 0; i < V / 2; ++i) w[i] = from_f32x2<T>(f[2 * i], f[2 * i + 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) e[i] = from_f32<T>(f[i]);
+    }
+  }
   __device__ __forceinline__ void load(const T* src) {
 #pragma unroll
     for (int i = 0; i < N; ++i) p[i] = reinterpret_cast<const P*>(src)[i];
@@ -85,10 +129,6 @@ struct Vec {
   __device__ __forceinline__ void store(T* dst) const {
 #pragma unroll
     for (int i = 0; i < N; ++i) reinterpret_cast<P*>(dst)[i] = p[i];
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < V; ++i) e[i] = from_f32<T>(0.f);
   }
 };
 
@@ -131,22 +171,44 @@ __device__ __forceinline__ void rope_turn(float (&a)[V], float (&b)[V], const fl
   }
 }
 
-// Cosines and sines of the V pairs of an item for one token. A table entry
-// whose axis the positions do not have sets `bad` and leaves its pair as it is.
-template <int V>
-__device__ __forceinline__ void rope_angles(const uint64_t* __restrict__ table, int item,
+constexpr int kRopeMaxPairs = 128;
+
+// Cosines and sines of one token's pairs, shared out over a warp and kept in
+// its shared memory cs[2][kRopeMaxPairs] (a lane group per head would compute
+// each of them several times over). A table entry whose axis the positions do
+// not have returns true and leaves its pair as it is.
+__device__ __forceinline__ bool rope_angles(float* cs, const uint64_t* __restrict__ table, int pairs,
                                             const int32_t* __restrict__ pos_row, int pos_dim,
-                                            float (&c)[V], float (&s)[V], bool& bad) {
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const uint64_t e = __ldg(table + item * V + j);
+                                            float sign) {
+  bool bad = false;
+  for (int i = threadIdx.x & 31; i < pairs; i += 32) {
+    const uint64_t e = __ldg(table + i);
     const int axis = int(e & 7ull);
-    if (axis < pos_dim) {
-      rope_cos_sin(e, __ldg(pos_row + axis), c[j], s[j]);
-    } else {
-      bad = true;
-      c[j] = 1.f;
-      s[j] = 0.f;
+    float c = 1.f, s = 0.f;
+    if (axis < pos_dim) rope_cos_sin(e, __ldg(pos_row + axis), c, s);
+    else bad = true;
+    cs[i] = c;
+    cs[kRopeMaxPairs + i] = sign * s;
+  }
+  return bad;
+}
+
+// The cosines and sines of an item's V pairs.
+template <int V>
+__device__ __forceinline__ void rope_fetch(const float* cs, int item, float (&c)[V], float (&s)[V]) {
+  if constexpr (V >= 4) {
+#pragma unroll
+    for (int j = 0; j < V; j += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(cs + item * V + j);
+      const float4 y = *reinterpret_cast<const float4*>(cs + kRopeMaxPairs + item * V + j);
+      c[j] = x.x, c[j + 1] = x.y, c[j + 2] = x.z, c[j + 3] = x.w;
+      s[j] = y.x, s[j + 1] = y.y, s[j + 2] = y.z, s[j + 3] = y.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      c[j] = cs[item * V + j];
+      s[j] = cs[kRopeMaxPairs + item * V + j];
     }
   }
 }
@@ -169,7 +231,7 @@ struct RopeParams {
   const uint64_t* table;
   int num_pairs, total, H, Hkv, d;
   int adjacent, inverse;
-  int parts;               // warps that share a token's heads
+  int per;                 // heads (Q and K together) a warp takes
   uint32_t* status;
 };
 
@@ -190,7 +252,8 @@ struct CacheParams {
   const uint64_t* table;
   int num_pairs, total, Hkv, d;
   int adjacent;
-  int parts;
+  int lane_shift;          // log2 of the lanes that share a row
+  int per;                 // rows (K and V heads together) a warp takes
   uint32_t* status;
 };
 
