@@ -223,65 +223,6 @@ __device__ __forceinline__ void att_poison32(uint32_t (&h)[16], uint32_t nan, in
   }
 }
 
-// What a CTA works on: rows [tok0 + x * tt, ...) of KV head kvh for row tile
-// x, keys [k0, k1) of a page list.
-struct AttUnit {
-  int kvh, slot;
-  int tok0, tok_end;     // first token of row tile 0; one past the last token
-  int k0, k1;            // keys, in the coordinates of the page list
-  int lim0;              // keys the token tok_first sees; one more for each later token (suffix)
-  int tok_first;
-  int causal;
-  const int32_t* pages;
-  bool bad;
-};
-
-__device__ __forceinline__ AttUnit att_unit(const AttParams& p, int64_t u) {
-  AttUnit w{};
-  if (u < p.units_p) {
-    const int g = int(u % p.ntg);
-    const int64_t ch = u / p.ntg;
-    w.kvh = int(ch % p.Hkv);
-    const int c = int(ch / p.Hkv);
-    w.slot = 2 * c;
-    int n = __ldg(p.prefix_len);
-    const int rows = __ldg(p.cu_q + p.R);
-    w.bad = n < 0 || n > p.max_prefix || rows < 0 || rows > p.Tq;
-    if (w.bad) return w;
-    w.tok0 = g * 2 * p.tt;
-    w.tok_end = rows;
-    w.k0 = min(c * p.lp, n);
-    w.k1 = min(w.k0 + p.lp, n);
-    w.lim0 = n;
-    w.pages = p.prefix_pages;
-  } else {
-    u -= p.units_p;
-    const int c = int(u % p.sc);
-    u /= p.sc;
-    const int qi = int(u % p.qt);
-    u /= p.qt;
-    w.kvh = int(u % p.Hkv);
-    const int r = int(u / p.Hkv);
-    w.slot = 2 * (p.nc + c);
-    const int a = __ldg(p.cu_q + r), b = __ldg(p.cu_q + r + 1);
-    const int n = __ldg(p.suffix_lens + r);
-    w.bad = a < 0 || b < a || b > p.Tq || b - a > p.max_q || n < 0 || n > p.max_suffix ||
-            (r == 0 && a != 0);
-    if (w.bad) return w;
-    w.tok_first = a;
-    w.tok0 = a + qi * 2 * p.tt;
-    w.tok_end = min(b, w.tok0 + 2 * p.tt);
-    w.causal = 1;
-    w.lim0 = n - (b - a) + 1;
-    // keys past the last row's limit are seen by no row of the unit
-    const int seen = min(n, w.lim0 + (w.tok_end - 1 - a));
-    w.k0 = min(c * p.ls, max(seen, 0));
-    w.k1 = min(w.k0 + p.ls, max(seen, 0));
-    w.pages = p.page_table + r * p.table_stride;
-  }
-  return w;
-}
-
 template <int D>
 __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const AttParams p) {
   using C = AttCfg<D>;
@@ -304,13 +245,15 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t T = p.timeout_ns;
   pdl_wait();   // every input may come from an earlier kernel
-  const AttUnit w = att_unit(p, p.unit0 + blockIdx.x);
+  const AttUnit w = att_unit(p, blockIdx.x, 2 * p.tt * p.G);
+  const int tok0 = w.tok_first + w.group * 2 * p.tt;          // of row tile 0
+  const int tok_end = min(w.tok_last, tok0 + 2 * p.tt);
   if (w.bad) {
     pdl_launch_dependents();
     if (threadIdx.x == 0) set_status(p.status, TSEL_DEV_SEQLENS);
     return;
   }
-  if (w.tok0 >= w.tok_end) {   // no rows
+  if (tok0 >= tok_end) {   // no rows
     pdl_launch_dependents();
     return;
   }
@@ -319,7 +262,7 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
   // turn: with two row tiles each takes one and walks every key tile; with one
   // row tile (split) they take the even and the odd key tiles, and their
   // results are two partials.
-  const bool split = w.tok0 + p.tt >= w.tok_end;
+  const bool split = tok0 + p.tt >= tok_end;
   const int n0 = split ? (tiles + 1) >> 1 : tiles, n1 = split ? tiles >> 1 : tiles;
 
   // Softmax warps: pipeline x, row (TMEM lane) 32 * (warp % 4) + lane, the 64
@@ -327,9 +270,9 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
   const int x = (warp >> 3) & 1;
   const int half = (warp >> 2) & 1;
   const int row = int(threadIdx.x) & (kTile - 1);
-  const int tok = w.tok0 + (split ? 0 : x * p.tt) + row / p.G;
+  const int tok = tok0 + (split ? 0 : x * p.tt) + row / p.G;
   const int head = w.kvh * p.G + row % p.G;
-  const bool row_ok = warp < C::SOFT_WARPS && row < p.tt * p.G && tok < w.tok_end;
+  const bool row_ok = warp < C::SOFT_WARPS && row < p.tt * p.G && tok < tok_end;
   // this row's partial: slot w.slot, the second pipeline of a split unit in the
   // next one (which is empty otherwise)
   const int64_t part = (int64_t(w.slot + (split ? x : 0)) * p.Tq + tok) * p.H + head;

@@ -10,42 +10,49 @@
 
 namespace tsel {
 
-constexpr int kAttMaxChunkKeys = 8192;   // keys of one unit: bounds its page list in shared memory
+constexpr int kAttMaxChunkKeys = 8192;   // keys of a wide unit: bounds its page list in shared memory
 constexpr int kAttMinPage = 16;
 constexpr int kAttMaxPages = kAttMaxChunkKeys / kAttMinPage;
-// CTAs resident at once, one per SM. A constant, not a query: the workspace
-// size must follow from the sizes alone.
-constexpr int kAttCtas = 152;
+// CTAs resident at once on the 152 SMs: one wide CTA per SM, three narrow ones.
+// Constants, not queries: the workspace size must follow from the sizes alone.
+constexpr int kAttWideCtas = 152;
+constexpr int kAttNarrowCtas = 456;
+// Query rows (tokens times query heads per KV head) up to which the narrow
+// kernel takes the keys of a prefix or of a request's suffix.
+constexpr int kAttNarrowRows = 32;
+constexpr int kAttNarrowBlock = 16;      // rows of one narrow unit
 
-// How a call is cut into units: (key chunk, KV head, row tiles) of the prefix,
-// and (request, KV head, row tile, key chunk) of the suffixes.
+// How the prefix, or the suffixes, are cut into units: (key chunk, KV head, row
+// group), for the suffixes of each request.
+struct AttPart {
+  int narrow;          // attend_narrow.cu, else attend.cu
+  int groups;          // row groups: pairs of 128-row tiles, or 16-row blocks
+  int chunks, keys;    // key chunks, keys of one
+  int slot0;           // partial results of a row: one for each narrow chunk, two for each wide one
+  int64_t units;
+};
+
 struct AttPlan {
-  int G;        // query heads per KV head
-  int tt;       // tokens per 128-row tile
-  int ntg;      // pairs of row tiles over all rows
-  int nc, lp;   // prefix chunks and keys per chunk
-  int qt;       // pairs of row tiles of one request
-  int sc, ls;   // suffix chunks and keys per chunk
-  int slots;    // partial results per row: two for each chunk
-  int64_t units_p, units_s;
+  int G;               // query heads per KV head
+  int tt;              // tokens per 128-row tile
+  AttPart pre, suf;
+  int slots;
   int64_t lse_off, o_off, total;   // workspace
 };
 
 // Chunks for `base` units of `tiles` 128-key tiles each on `ctas` CTAs: the
 // count with the least estimated time, in key tiles. A unit costs its tiles
-// plus about kAttUnitTiles of start-up and write-out, and joining costs a
-// little for each chunk.
-constexpr int kAttUnitTiles = 3;
-inline int att_chunks(int64_t base, int tiles, int ctas) {
+// plus `start` for its start-up and write-out, and joining costs a little for
+// each chunk.
+inline int att_chunks(int64_t base, int tiles, int ctas, double start, int least) {
   if (tiles <= 1 || base < 1) return tiles < 1 ? 0 : 1;
-  const int least = int(ceil_div(tiles, kAttMaxChunkKeys / kTile));
   int best = least;
   double best_cost = 1e300;
-  for (int n = least; n <= tiles && n <= 256; ++n) {
+  for (int n = least; n <= tiles && n <= 256 + least; ++n) {
     const int per = int(ceil_div(tiles, n));
     if (n > least && int(ceil_div(tiles, per)) < n) continue;   // the same tiles in fewer chunks
     const double waves = double(ceil_div(base * n, ctas));
-    const double cost = waves * (per + kAttUnitTiles) + 0.05 * n;
+    const double cost = waves * (per + start) + 0.05 * n;
     if (cost < best_cost) {
       best_cost = cost;
       best = n;
@@ -54,22 +61,29 @@ inline int att_chunks(int64_t base, int tiles, int ctas) {
   return best;
 }
 
+inline AttPart att_part(int64_t requests, int tokens, int max_keys, int Hkv, int G, int tt, int* slots) {
+  AttPart a{};
+  a.narrow = int64_t(tokens) * G <= kAttNarrowRows;
+  a.groups = int(a.narrow ? ceil_div(int64_t(tokens) * G, kAttNarrowBlock) : ceil_div(tokens, 2 * tt));
+  a.slot0 = *slots;
+  const int tiles = int(ceil_div(max_keys, kTile));
+  const int64_t base = requests * Hkv * a.groups;
+  if (base < 1 || tiles < 1) return a;
+  a.chunks = a.narrow ? att_chunks(base, tiles, kAttNarrowCtas, 1.0, 1)
+                      : att_chunks(base, tiles, kAttWideCtas, 3.0, int(ceil_div(tiles, kAttMaxChunkKeys / kTile)));
+  a.keys = int(ceil_div(tiles, a.chunks)) * kTile;
+  a.units = base * a.chunks;
+  *slots += a.chunks * (a.narrow ? 1 : 2);
+  return a;
+}
+
 inline AttPlan att_plan(int R, int Tq, int max_q, int H, int Hkv, int d, int max_prefix,
                         int max_suffix) {
   AttPlan a{};
   a.G = H / Hkv;
   a.tt = kTile / a.G;
-  a.ntg = int(ceil_div(Tq, 2 * a.tt));
-  const int kp = int(ceil_div(max_prefix, kTile));
-  const int ks = int(ceil_div(max_suffix, kTile));
-  a.qt = int(ceil_div(max_q, 2 * a.tt));
-  if (Tq > 0) a.nc = att_chunks(int64_t(Hkv) * a.ntg, kp, kAttCtas);
-  if (a.nc > 0) a.lp = int(ceil_div(kp, a.nc)) * kTile;
-  if (Tq > 0 && R > 0 && a.qt > 0) a.sc = att_chunks(int64_t(R) * Hkv * a.qt, ks, kAttCtas);
-  if (a.sc > 0) a.ls = int(ceil_div(ks, a.sc)) * kTile;
-  a.slots = 2 * (a.nc + a.sc);
-  a.units_p = int64_t(a.nc) * Hkv * a.ntg;
-  a.units_s = int64_t(R) * Hkv * a.qt * a.sc;
+  a.pre = att_part(1, Tq, max_prefix, Hkv, a.G, a.tt, &a.slots);
+  a.suf = att_part(Tq > 0 ? R : 0, max_q, max_suffix, Hkv, a.G, a.tt, &a.slots);
   a.lse_off = kWsHeaderBytes;
   a.o_off = align_up(a.lse_off + 4 * int64_t(a.slots) * Tq * H, 256);
   a.total = align_up(a.o_off + 4 * int64_t(a.slots) * Tq * H * d, 256);
@@ -96,8 +110,10 @@ struct AttParams {
   int max_suffix;
   int H, Hkv;
   float c;                     // softmax_scale * log2(e)
-  int G, tt, ntg, nc, lp, qt, sc, ls, slots;
-  int64_t unit0, units_p;      // this launch's first unit; prefix units of the call
+  int G, tt, slots;
+  AttPart pre, suf;
+  int64_t pre_units;           // prefix units of this launch (its first ones); the rest are suffix units
+  int late_wait;               // the launch before this one is of the same call: wait for it at the end
   float* part_lse;             // [slots][Tq][H], base 2
   float* part_o;               // [slots][Tq][H][d]
   void* out;
@@ -107,7 +123,65 @@ struct AttParams {
   uint64_t timeout_ns;
 };
 
+// Keys [k0, k1) of a page list and the rows that see them: row i of a suffix
+// sees the first lim0 + i keys (of the suffix's tokens tok_first ...), rows of
+// the prefix the first lim0.
+struct AttUnit {
+  int kvh, slot, group;
+  int tok_first, tok_last;   // tokens [tok_first, tok_last) of the request (prefix: of the batch)
+  int k0, k1;
+  int lim0;
+  int causal;
+  const int32_t* pages;
+  bool bad;
+};
+
+// `per`: rows of a row group; the keys of a suffix unit end where its last row sees no further.
+__device__ __forceinline__ AttUnit att_unit(const AttParams& p, int64_t u, int per) {
+  AttUnit w{};
+  if (u < p.pre_units) {
+    w.group = int(u % p.pre.groups);   // neighbouring units share their keys
+    const int64_t ch = u / p.pre.groups;
+    w.kvh = int(ch % p.Hkv);
+    const int c = int(ch / p.Hkv);
+    w.slot = p.pre.slot0 + c * (p.pre.narrow ? 1 : 2);
+    const int n = __ldg(p.prefix_len);
+    w.tok_last = __ldg(p.cu_q + p.R);
+    w.bad = n < 0 || n > p.max_prefix || w.tok_last < 0 || w.tok_last > p.Tq;
+    if (w.bad) return w;
+    w.k0 = min(c * p.pre.keys, n);
+    w.k1 = min(w.k0 + p.pre.keys, n);
+    w.lim0 = n;
+    w.pages = p.prefix_pages;
+  } else {
+    u -= p.pre_units;
+    const int c = int(u % p.suf.chunks);
+    u /= p.suf.chunks;
+    w.group = int(u % p.suf.groups);
+    u /= p.suf.groups;
+    w.kvh = int(u % p.Hkv);
+    const int r = int(u / p.Hkv);
+    w.slot = p.suf.slot0 + c * (p.suf.narrow ? 1 : 2);
+    const int a = __ldg(p.cu_q + r), b = __ldg(p.cu_q + r + 1);
+    const int n = __ldg(p.suffix_lens + r);
+    w.bad = a < 0 || b < a || b > p.Tq || b - a > p.max_q || n < 0 || n > p.max_suffix ||
+            (r == 0 && a != 0);
+    if (w.bad) return w;
+    w.tok_first = a;
+    w.tok_last = b;
+    w.causal = 1;
+    w.lim0 = n - (b - a) + 1;
+    const int last = min((w.group + 1) * per, (b - a) * p.G);   // rows up to here
+    const int seen = max(min(n, w.lim0 + (last - 1) / p.G), 0);
+    w.k0 = min(c * p.suf.keys, seen);
+    w.k1 = min(w.k0 + p.suf.keys, seen);
+    w.pages = p.page_table + r * p.table_stride;
+  }
+  return w;
+}
+
 cudaError_t launch_attend(int head_dim, const AttParams& p, int64_t units, cudaStream_t stream);
+cudaError_t launch_attend_narrow(int head_dim, const AttParams& p, int64_t units, cudaStream_t stream);
 cudaError_t launch_attend_join(int head_dim, const AttParams& p, int num_sms, cudaStream_t stream);
 
 }  // namespace tsel

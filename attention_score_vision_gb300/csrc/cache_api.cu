@@ -348,7 +348,7 @@ tsel_status tsel_prefix_attention(
                              max_prefix_len, max_suffix_len);
   if (workspace_bytes < size_t(a.total))
     return fail(TSEL_ERR_WORKSPACE, "workspace %zu < %lld bytes", workspace_bytes, (long long)a.total);
-  if (a.units_p + a.units_s > 0x7FFFFFFFll)
+  if (a.pre.units + a.suf.units > 0x7FFFFFFFll)
     return fail(TSEL_ERR_UNSUPPORTED, "too many units of work");
   if (total_q == 0) return TSEL_OK;
   AttParams p{};
@@ -384,14 +384,9 @@ tsel_status tsel_prefix_attention(
   p.c = scale * 1.4426950408889634f;
   p.G = a.G;
   p.tt = a.tt;
-  p.ntg = a.ntg;
-  p.nc = a.nc;
-  p.lp = a.lp;
-  p.qt = a.qt;
-  p.sc = a.sc;
-  p.ls = a.ls;
   p.slots = a.slots;
-  p.units_p = a.units_p;
+  p.pre = a.pre;
+  p.suf = a.suf;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.part_lse = reinterpret_cast<float*>(ws + a.lse_off);
   p.part_o = reinterpret_cast<float*>(ws + a.o_off);
@@ -400,9 +395,18 @@ tsel_status tsel_prefix_attention(
   p.status = &reinterpret_cast<WsHeader*>(ws)->status;
   p.timeout_ns = device_wait_timeout_ns();
   cudaError_t e;
-  if (a.units_p + a.units_s > 0) {
-    e = launch_attend(head_dim, p, a.units_p + a.units_s, stream);
+  const int64_t wide_pre = a.pre.narrow ? 0 : a.pre.units, wide_suf = a.suf.narrow ? 0 : a.suf.units;
+  if (wide_pre + wide_suf > 0) {
+    p.pre_units = wide_pre;
+    e = launch_attend(head_dim, p, wide_pre + wide_suf, stream);
     if (e != cudaSuccess) return cuda_fail(e, "attention launch");
+  }
+  const int64_t narrow = a.pre.units + a.suf.units - wide_pre - wide_suf;
+  if (narrow > 0) {
+    p.pre_units = a.pre.narrow ? a.pre.units : 0;
+    p.late_wait = wide_pre + wide_suf > 0;
+    e = launch_attend_narrow(head_dim, p, narrow, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "few-row attention launch");
   }
   e = launch_attend_join(head_dim, p, sms, stream);
   return e == cudaSuccess ? TSEL_OK : cuda_fail(e, "join launch");
