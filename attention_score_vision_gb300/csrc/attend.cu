@@ -664,13 +664,20 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
   if (warp == C::MMA_WARP) tmem_dealloc(tmem, 512);
 }
 
-// Joins a row's partial results: out = sum_c 2^(lse_c - lse) o_c, in chunk
-// order. One warp per row, D / 4 lanes of four columns.
-template <int D>
-__global__ void __launch_bounds__(256) attend_join_kernel(const AttParams p) {
+// Joins a row's partial results: out = sum_c 2^(lse_c - lse) o_c. WPR warps
+// share a row (its partials go round them) and are added up in their order, so
+// a row with many partials is not one long chain of loads; D / 4 lanes of four
+// columns. Chunks without visible keys have lse = -inf and wrote no columns.
+constexpr int kJoinWarps = 8;
+
+template <int D, int WPR>
+__global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const AttParams p) {
+  __shared__ float s_acc[WPR > 1 ? kJoinWarps : 1][D];
+  __shared__ float s_m[kJoinWarps], s_sum[kJoinWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int part = warp % WPR;
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
   const int total = __ldg(p.cu_q + p.R);
   if (total < 0 || total > p.Tq) {
     if (blockIdx.x == 0 && threadIdx.x == 0) set_status(p.status, TSEL_DEV_SEQLENS);
@@ -678,47 +685,98 @@ __global__ void __launch_bounds__(256) attend_join_kernel(const AttParams p) {
   }
   const int64_t rows = int64_t(total) * p.H;
   const int64_t step = int64_t(p.Tq) * p.H;
-  const int64_t nwarps = int64_t(gridDim.x) * 8;
-  for (int64_t r = (int64_t(blockIdx.x) * 256 + threadIdx.x) >> 5; r < rows; r += nwarps) {
-    float m = kNegInf;
-    for (int c = lane; c < p.slots; c += 32) m = fmaxf(m, p.part_lse[c * step + r]);
+  const int64_t r = int64_t(blockIdx.x) * (kJoinWarps / WPR) + warp / WPR;
+  float m = kNegInf, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (r < rows) {
+    for (int base = 0; base < p.slots; base += 32 * WPR) {
+      const int at = base + lane * WPR + part;   // a lane per partial
+      const float mine = at < p.slots ? p.part_lse[at * step + r] : kNegInf;
+      unsigned live = __ballot_sync(0xffffffffu, mine != kNegInf);
+      float top = mine;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float ref = m == kNegInf ? 0.f : m;
-    float sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = 0; c < p.slots; ++c) {
-      const float wgt = exp2f(p.part_lse[c * step + r] - ref);
-      if (wgt != 0.f) {   // a chunk without visible keys wrote no columns
-        sum += wgt;
-        if (lane < D / 4) {
-          const float4 o = *reinterpret_cast<const float4*>(p.part_o + (c * step + r) * D + 4 * lane);
-          acc.x += wgt * o.x;
-          acc.y += wgt * o.y;
-          acc.z += wgt * o.z;
-          acc.w += wgt * o.w;
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const float now = fmaxf(m, top), ref = now == kNegInf ? 0.f : now;
+      const float old = m == kNegInf ? 0.f : exp2f(m - ref);
+      m = now;
+      sum *= old;
+      acc.x *= old;
+      acc.y *= old;
+      acc.z *= old;
+      acc.w *= old;
+      const float wgt = exp2f(mine - ref);
+      while (live != 0) {   // four partials in flight
+        float wv[4];
+        float4 o[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int c = live != 0 ? __ffs(live) - 1 : -1;
+          live &= live - 1;
+          wv[x] = c >= 0 ? __shfl_sync(0xffffffffu, wgt, c) : 0.f;
+          o[x] = c >= 0 && lane < D / 4
+                     ? *reinterpret_cast<const float4*>(p.part_o + ((base + c * WPR + part) * step + r) * D + 4 * lane)
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if (wv[x] == 0.f) continue;   // too far below the row's largest
+          sum += wv[x];
+          acc.x += wv[x] * o[x].x;
+          acc.y += wv[x] * o[x].y;
+          acc.z += wv[x] * o[x].z;
+          acc.w += wv[x] * o[x].w;
         }
       }
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const int64_t tok = r / p.H;
-    const int head = int(r - tok * p.H);
-    if (lane < D / 4) {
-      uint2 o;
-      if (p.fp16) {
-        o.x = pack_f16(acc.x * inv, acc.y * inv);
-        o.y = pack_f16(acc.z * inv, acc.w * inv);
-      } else {
-        __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-        __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-        o.x = *reinterpret_cast<uint32_t*>(&a);
-        o.y = *reinterpret_cast<uint32_t*>(&b);
-      }
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + tok * p.out_stride + int64_t(head) * D + 4 * lane) = o;
-    }
-    if (lane == 0 && p.lse != nullptr)
-      p.lse[int64_t(head) * p.Tq + tok] = sum == 0.f ? kNegInf : (ref + log2f(sum)) * 0.69314718055994531f;
   }
+  if (WPR > 1) {
+    if (lane < D / 4) *reinterpret_cast<float4*>(&s_acc[warp][4 * lane]) = acc;
+    if (lane == 0) {
+      s_m[warp] = m;
+      s_sum[warp] = sum;
+    }
+    __syncthreads();
+    if (part != 0) return;
+    m = kNegInf;
+#pragma unroll
+    for (int x = 0; x < WPR; ++x) m = fmaxf(m, s_m[warp + x]);
+    sum = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (lane < D / 4) {
+#pragma unroll
+      for (int x = 0; x < WPR; ++x) {
+        // a warp whose partials are all NaN has no maximum, but a NaN sum
+        const float f = s_m[warp + x] == kNegInf ? (s_sum[warp + x] == 0.f ? 0.f : 1.f) : exp2f(s_m[warp + x] - m);
+        if (f == 0.f) continue;
+        const float4 v = *reinterpret_cast<const float4*>(&s_acc[warp + x][4 * lane]);
+        sum += f * s_sum[warp + x];
+        acc.x += f * v.x;
+        acc.y += f * v.y;
+        acc.z += f * v.z;
+        acc.w += f * v.w;
+      }
+    }
+  }
+  if (r >= rows) return;
+  const float ref = m == kNegInf ? 0.f : m;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const int64_t tok = r / p.H;
+  const int head = int(r - tok * p.H);
+  if (lane < D / 4) {
+    uint2 o;
+    if (p.fp16) {
+      o.x = pack_f16(acc.x * inv, acc.y * inv);
+      o.y = pack_f16(acc.z * inv, acc.w * inv);
+    } else {
+      __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+      __nv_bfloat162 b = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+      o.x = *reinterpret_cast<uint32_t*>(&a);
+      o.y = *reinterpret_cast<uint32_t*>(&b);
+    }
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + tok * p.out_stride + int64_t(head) * D + 4 * lane) = o;
+  }
+  if (lane == 0 && p.lse != nullptr)
+    p.lse[int64_t(head) * p.Tq + tok] = sum == 0.f ? kNegInf : (ref + log2f(sum)) * 0.69314718055994531f;
 }
 
 template <int D>
@@ -750,23 +808,26 @@ cudaError_t launch_attend(int head_dim, const AttParams& p, int64_t units, cudaS
   }
 }
 
-cudaError_t launch_attend_join(int head_dim, const AttParams& p, int num_sms, cudaStream_t stream) {
-  int64_t blocks = ceil_div(int64_t(p.Tq) * p.H, 8);
-  const int64_t most = int64_t(num_sms) * 8;
-  if (blocks > most) blocks = most;
-#define TSEL_JOIN_CASE(DD)                                                                    \
-  case DD:                                                                                    \
-    return launch_kernel(attend_join_kernel<DD>, dim3(unsigned(blocks)), 256, 0, stream, 1, p);
+namespace {
+template <int D>
+cudaError_t launch_join_t(const AttParams& p, cudaStream_t stream) {
+  // more than eight partials: the whole CTA takes one row
+  const int per_cta = p.slots > 8 ? 1 : kJoinWarps;
+  const unsigned blocks = unsigned(ceil_div(int64_t(p.Tq) * p.H, per_cta));
+  return p.slots > 8 ? launch_kernel(attend_join_kernel<D, kJoinWarps>, dim3(blocks), 32 * kJoinWarps, 0, stream, 1, p)
+                     : launch_kernel(attend_join_kernel<D, 1>, dim3(blocks), 32 * kJoinWarps, 0, stream, 1, p);
+}
+}  // namespace
+
+cudaError_t launch_attend_join(int head_dim, const AttParams& p, cudaStream_t stream) {
   switch (head_dim) {
-    TSEL_JOIN_CASE(64)
-    TSEL_JOIN_CASE(80)
-    TSEL_JOIN_CASE(96)
-    TSEL_JOIN_CASE(112)
-    TSEL_JOIN_CASE(128)
-    default:
-      return cudaErrorInvalidValue;
+    case 64: return launch_join_t<64>(p, stream);
+    case 80: return launch_join_t<80>(p, stream);
+    case 96: return launch_join_t<96>(p, stream);
+    case 112: return launch_join_t<112>(p, stream);
+    case 128: return launch_join_t<128>(p, stream);
+    default: return cudaErrorInvalidValue;
   }
-#undef TSEL_JOIN_CASE
 }
 
 }  // namespace tsel

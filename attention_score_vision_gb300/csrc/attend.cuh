@@ -13,20 +13,19 @@ namespace tsel {
 constexpr int kAttMaxChunkKeys = 8192;   // keys of a wide unit: bounds its page list in shared memory
 constexpr int kAttMinPage = 16;
 constexpr int kAttMaxPages = kAttMaxChunkKeys / kAttMinPage;
-// CTAs resident at once on the 152 SMs: one wide CTA per SM, three narrow ones.
-// Constants, not queries: the workspace size must follow from the sizes alone.
+// CTAs resident at once on the 152 SMs: one wide CTA per SM, four or three narrow
+// ones. Constants, not queries: the workspace size must follow from the sizes alone.
 constexpr int kAttWideCtas = 152;
-constexpr int kAttNarrowCtas = 456;
+constexpr int kAttNarrowCtas1 = 4 * 152, kAttNarrowCtas2 = 3 * 152;
 // Query rows (tokens times query heads per KV head) up to which the narrow
 // kernel takes the keys of a prefix or of a request's suffix.
 constexpr int kAttNarrowRows = 32;
-constexpr int kAttNarrowBlock = 16;      // rows of one narrow unit
 
 // How the prefix, or the suffixes, are cut into units: (key chunk, KV head, row
 // group), for the suffixes of each request.
 struct AttPart {
-  int narrow;          // attend_narrow.cu, else attend.cu
-  int groups;          // row groups: pairs of 128-row tiles, or 16-row blocks
+  int narrow;          // attend_narrow.cu with 8 or 16 rows to a unit (1, 2), else attend.cu (0)
+  int groups;          // row groups: of 8 or 16 rows, or pairs of 128-row tiles
   int chunks, keys;    // key chunks, keys of one
   int slot0;           // partial results of a row: one for each narrow chunk, two for each wide one
   int64_t units;
@@ -63,13 +62,14 @@ inline int att_chunks(int64_t base, int tiles, int ctas, double start, int least
 
 inline AttPart att_part(int64_t requests, int tokens, int max_keys, int Hkv, int G, int tt, int* slots) {
   AttPart a{};
-  a.narrow = int64_t(tokens) * G <= kAttNarrowRows;
-  a.groups = int(a.narrow ? ceil_div(int64_t(tokens) * G, kAttNarrowBlock) : ceil_div(tokens, 2 * tt));
+  const int64_t rows = int64_t(tokens) * G;
+  a.narrow = rows > kAttNarrowRows ? 0 : (rows > 8 ? 2 : 1);
+  a.groups = int(a.narrow ? ceil_div(rows, 8 * a.narrow) : ceil_div(tokens, 2 * tt));
   a.slot0 = *slots;
   const int tiles = int(ceil_div(max_keys, kTile));
   const int64_t base = requests * Hkv * a.groups;
   if (base < 1 || tiles < 1) return a;
-  a.chunks = a.narrow ? att_chunks(base, tiles, kAttNarrowCtas, 1.0, 1)
+  a.chunks = a.narrow ? att_chunks(base, tiles, a.narrow == 1 ? kAttNarrowCtas1 : kAttNarrowCtas2, 1.0, 1)
                       : att_chunks(base, tiles, kAttWideCtas, 3.0, int(ceil_div(tiles, kAttMaxChunkKeys / kTile)));
   a.keys = int(ceil_div(tiles, a.chunks)) * kTile;
   a.units = base * a.chunks;
@@ -181,7 +181,8 @@ __device__ __forceinline__ AttUnit att_unit(const AttParams& p, int64_t u, int p
 }
 
 cudaError_t launch_attend(int head_dim, const AttParams& p, int64_t units, cudaStream_t stream);
-cudaError_t launch_attend_narrow(int head_dim, const AttParams& p, int64_t units, cudaStream_t stream);
-cudaError_t launch_attend_join(int head_dim, const AttParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_attend_narrow(int head_dim, int row_groups, const AttParams& p, int64_t units,
+                                 cudaStream_t stream);
+cudaError_t launch_attend_join(int head_dim, const AttParams& p, cudaStream_t stream);
 
 }  // namespace tsel

@@ -357,8 +357,6 @@ tsel_status tsel_prefix_attention(
   const int64_t width = int64_t(num_heads) * head_dim;
   TSEL_TRY(check_rows("q", q, &p.q_stride, width, 2));
   TSEL_TRY(check_rows("out", out, &p.out_stride, width, 2));
-  int sms = 0;
-  if (device_sms(&sms) != 0) return fail(TSEL_ERR_CUDA, "cannot query the SM count");
   p.q = q;
   p.fp16 = dtype == TSEL_FP16 ? 1 : 0;
   p.cu_q = cu_seqlens_q;
@@ -394,21 +392,21 @@ tsel_status tsel_prefix_attention(
   p.lse = lse;
   p.status = &reinterpret_cast<WsHeader*>(ws)->status;
   p.timeout_ns = device_wait_timeout_ns();
+  // The wide launch first, then the few-row ones, which do not depend on it:
+  // they start with it and wait for it at their end.
   cudaError_t e;
-  const int64_t wide_pre = a.pre.narrow ? 0 : a.pre.units, wide_suf = a.suf.narrow ? 0 : a.suf.units;
-  if (wide_pre + wide_suf > 0) {
-    p.pre_units = wide_pre;
-    e = launch_attend(head_dim, p, wide_pre + wide_suf, stream);
+  bool launched = false;
+  for (int kind = 0; kind <= 2; ++kind) {
+    const int64_t pre = a.pre.narrow == kind ? a.pre.units : 0, suf = a.suf.narrow == kind ? a.suf.units : 0;
+    if (pre + suf == 0) continue;
+    p.pre_units = pre;
+    p.late_wait = launched;
+    e = kind == 0 ? launch_attend(head_dim, p, pre + suf, stream)
+                  : launch_attend_narrow(head_dim, kind, p, pre + suf, stream);
     if (e != cudaSuccess) return cuda_fail(e, "attention launch");
+    launched = true;
   }
-  const int64_t narrow = a.pre.units + a.suf.units - wide_pre - wide_suf;
-  if (narrow > 0) {
-    p.pre_units = a.pre.narrow ? a.pre.units : 0;
-    p.late_wait = wide_pre + wide_suf > 0;
-    e = launch_attend_narrow(head_dim, p, narrow, stream);
-    if (e != cudaSuccess) return cuda_fail(e, "few-row attention launch");
-  }
-  e = launch_attend_join(head_dim, p, sms, stream);
+  e = launch_attend_join(head_dim, p, stream);
   return e == cudaSuccess ? TSEL_OK : cuda_fail(e, "join launch");
 }
 
