@@ -80,6 +80,7 @@ struct AttCfg {
   static constexpr int NUM_BARS = 4 * KS + 3 * 2;
   static constexpr int OFF_BAR = OFF_META + kAttMetaRing * int(sizeof(AttTileMeta));
   static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;
+  static constexpr int OFF_UNIT = OFF_MISC + 16;            // what the epilogue needs of the unit
   static constexpr int SMEM_USED = OFF_MISC + 64 + 1024;    // + alignment slack
   // one CTA per SM (it holds all of TMEM), also for the smaller heads
   static constexpr int SMEM_BYTES = SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024;
@@ -244,19 +245,34 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t T = p.timeout_ns;
+  // Before the wait for the earlier kernels: what does not touch their memory.
+  // (TMEM may still be held by a CTA of an earlier kernel; none of them waits
+  // for this one.)
+  if (warp == C::MMA_WARP) {
+    if (lane == 0) {
+      for (int i = 0; i < C::KS; ++i) {
+        mbar_init(&k_full[i], 4);
+        mbar_init(&k_free[i], 1);
+        mbar_init(&v_full[i], 4);
+        mbar_init(&v_free[i], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&s_full[i], 1);
+        mbar_init(&p_full[i], C::SOFT_PER_TILE);
+        mbar_init(&o_done[i], 1);
+      }
+      *abort_flag = 0;
+      fence_barrier_init();
+    }
+    __syncwarp();
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
   pdl_wait();   // every input may come from an earlier kernel
   const AttUnit w = att_unit(p, blockIdx.x, 2 * p.tt * p.G);
   const int tok0 = w.tok_first + w.group * 2 * p.tt;          // of row tile 0
   const int tok_end = min(w.tok_last, tok0 + 2 * p.tt);
-  if (w.bad) {
-    pdl_launch_dependents();
-    if (threadIdx.x == 0) set_status(p.status, TSEL_DEV_SEQLENS);
-    return;
-  }
-  if (tok0 >= tok_end) {   // no rows
-    pdl_launch_dependents();
-    return;
-  }
   const int tiles = int(ceil_div(w.k1 - w.k0, kTile));
   // Two pipelines x = 0, 1 keep the tensor cores and the softmax warps busy in
   // turn: with two row tiles each takes one and walks every key tile; with one
@@ -273,106 +289,118 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
   const int tok = tok0 + (split ? 0 : x * p.tt) + row / p.G;
   const int head = w.kvh * p.G + row % p.G;
   const bool row_ok = warp < C::SOFT_WARPS && row < p.tt * p.G && tok < tok_end;
-  // this row's partial: slot w.slot, the second pipeline of a split unit in the
-  // next one (which is empty otherwise)
-  const int64_t part = (int64_t(w.slot + (split ? x : 0)) * p.Tq + tok) * p.H + head;
+  // A row's partial is in slot w.slot; the second pipeline of a split unit has
+  // the next one, which is empty otherwise.
   if (row_ok && half == 0) {
     const int64_t next = int64_t(p.Tq) * p.H;
+    const int64_t part = (int64_t(w.slot + (split ? x : 0)) * p.Tq + tok) * p.H + head;
     if (!split) p.part_lse[part + next] = kNegInf;
     if ((x == 0 ? n0 : n1) == 0) p.part_lse[part] = kNegInf;
   }
-  if (tiles == 0) {   // no visible key in this chunk
+  if (w.bad || tok0 >= tok_end || tiles == 0) {   // bad lengths, no rows, or no visible key in this chunk
+    if (w.bad && threadIdx.x == 0) set_status(p.status, TSEL_DEV_SEQLENS);
+    __syncthreads();
     pdl_launch_dependents();
+    if (warp == C::MMA_WARP) {
+      tc_fence_after();
+      tmem_dealloc(*tmem_slot, 512);
+    }
     return;
   }
 
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < C::KS; ++i) {
-      mbar_init(&k_full[i], 4);
-      mbar_init(&k_free[i], 1);
-      mbar_init(&v_full[i], 4);
-      mbar_init(&v_free[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], C::SOFT_PER_TILE);
-      mbar_init(&o_done[i], 1);
-    }
-    *abort_flag = 0;
-    fence_barrier_init();
-  }
-  if (warp == C::MMA_WARP) {
-    tmem_alloc(tmem_slot, 512);
-    tmem_relinquish();
-  }
-  // the chunk's pages; one out of range is read as zeros
-  {
-    const int first = w.k0 >> p.page_shift;
-    const int n = ((w.k1 - 1) >> p.page_shift) - first + 1;
-    for (int i = threadIdx.x; i < n; i += C::THREADS) {
-      const int pg = __ldg(w.pages + first + i);
+  // The converters fetch the chunk's pages (one out of range is read as zeros)
+  // and their first tile while the others load Q.
+  const int first_page = w.k0 >> p.page_shift;
+  if (warp >= C::CONV_WARP) {
+    const int n = ((w.k1 - 1) >> p.page_shift) - first_page + 1;
+    for (int i = int(threadIdx.x) - 32 * C::CONV_WARP; i < n; i += 32 * 8) {
+      const int pg = __ldg(w.pages + first_page + i);
       const bool ok = pg >= 0 && pg < p.num_pages;
       if (!ok) set_status(p.status, TSEL_DEV_PAGES);
       s_pages[i] = ok ? pg : -1;
     }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
   }
-  // Q rows, scaled to fp16, into the K-major A operand; the threads of a row
-  // take half of its columns each.
+  // Q rows, scaled to fp16, into the K-major A operand (a split unit's rows
+  // twice). A warp loads half the columns of its 32 rows, eight lanes to a row;
+  // the two warps of a row exchange its largest element.
   float qc = 0.f;   // softmax_scale * log2(e) * 2^(row's exponent)
   float* s_row = reinterpret_cast<float*>(smem + C::OFF_ROW) + x * 4 * kTile;
-  constexpr int QV = D / 16;   // 16-byte pieces of a row per thread
-  uint4 qv[QV];
-  const bool soft = warp < C::SOFT_WARPS;
-  auto q_pair = [&](uint32_t u) -> float2 {
-    if (p.fp16) return __half22float2(*reinterpret_cast<__half2*>(&u));
-    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
-  };
-  uint32_t q_top = 0;
-  if (soft) {
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) +
-                                                      tok * p.q_stride + int64_t(head) * D) + half * QV;
+  if (warp < C::SOFT_WARPS) {
+    constexpr int UH = D / 16;   // 16-byte pieces of half a row
+    const int unit = lane & 7, quad = 32 * (warp & 3);
+    uint4 qv[8];
 #pragma unroll
-    for (int j = 0; j < QV; ++j) qv[j] = row_ok ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < 8; ++k) {
+      const int r = quad + 4 * k + (lane >> 3);
+      const int t = tok0 + (split ? 0 : x * p.tt) + r / p.G;
+      const bool in = unit < UH && r < p.tt * p.G && t < tok_end;
+      qv[k] = in ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + t * p.q_stride +
+                                                        int64_t(w.kvh * p.G + r % p.G) * D) + half * UH + unit)
+                 : make_uint4(0, 0, 0, 0);
+    }
+    // magnitudes order like their bits, in both types
+    uint32_t* row_top = reinterpret_cast<uint32_t*>(s_row);
 #pragma unroll
-    for (int j = 0; j < QV; ++j) {
-      const uint32_t u[4] = {qv[j].x, qv[j].y, qv[j].z, qv[j].w};
+    for (int k = 0; k < 8; ++k) {
+      uint32_t m2 = __vmaxu2(__vmaxu2(qv[k].x & 0x7FFF7FFFu, qv[k].y & 0x7FFF7FFFu),
+                             __vmaxu2(qv[k].z & 0x7FFF7FFFu, qv[k].w & 0x7FFF7FFFu));
+      uint32_t top = max(m2 & 0xFFFFu, m2 >> 16);
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
+      if (unit == 0) row_top[half * kTile + quad + 4 * k + (lane >> 3)] = top;
+    }
+    asm volatile("bar.sync %0, 64;" ::"r"(3 + x * 4 + (warp & 3)) : "memory");
+    // fp32 exponent field of a row's largest element, at least 14
+    auto row_exp = [&](int r) -> int {
+      const uint32_t top = max(row_top[r], row_top[kTile + r]);
+      const uint32_t f = p.fp16 ? __float_as_uint(__half2float(__ushort_as_half(uint16_t(top)))) : top << 16;
+      return max(int(f >> 23), 14);
+    };
+    uint8_t* sq = smem + C::OFF_Q + x * C::TILE_BYTES;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int r = quad + 4 * k + (lane >> 3), j = half * UH + unit;
+      const float up = __uint_as_float(uint32_t(267 - row_exp(r)) << 23);   // largest element into [2^13, 2^14)
+      const uint32_t u[4] = {qv[k].x, qv[k].y, qv[k].z, qv[k].w};
+      uint32_t h[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float2 f = q_pair(u[i]);
-        q_top = max(q_top, max(__float_as_uint(f.x) & 0x7FFFFFFFu, __float_as_uint(f.y) & 0x7FFFFFFFu));
+        const float2 f = p.fp16 ? __half22float2(*reinterpret_cast<const __half2*>(&u[i]))
+                                : make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xFFFF0000u));
+        h[i] = pack_f16(f.x * up, f.y * up);
       }
+      if (unit < UH)
+        *reinterpret_cast<uint4*>(sq + (j >> 3) * (kTile * 128) + r * 128 + (((j & 7) ^ (r & 7)) << 4)) =
+            make_uint4(h[0], h[1], h[2], h[3]);
     }
-    s_row[half * kTile + row] = __uint_as_float(q_top);
-  }
-  __syncthreads();
-  if (soft) {
-    q_top = max(q_top, __float_as_uint(s_row[(half ^ 1) * kTile + row]));
-    uint8_t* sq = smem + C::OFF_Q + x * C::TILE_BYTES;   // a split unit's rows twice
-    const int E = max(int(q_top >> 23), 14);
-    const float up = __uint_as_float(uint32_t(267 - E) << 23);   // largest element into [2^13, 2^14)
-    qc = p.c * __uint_as_float(uint32_t(E - 13) << 23);          // 2^(E - 140)
-#pragma unroll
-    for (int i = 0; i < QV; ++i) {
-      const int j = half * QV + i;
-      const float2 a = q_pair(qv[i].x), b = q_pair(qv[i].y), c = q_pair(qv[i].z), d = q_pair(qv[i].w);
-      *reinterpret_cast<uint4*>(sq + (j >> 3) * (kTile * 128) + row * 128 + (((j & 7) ^ (row & 7)) << 4)) =
-          make_uint4(pack_f16(a.x * up, a.y * up), pack_f16(b.x * up, b.y * up),
-                     pack_f16(c.x * up, c.y * up), pack_f16(d.x * up, d.y * up));
-    }
+    qc = p.c * __uint_as_float(uint32_t(row_exp(row) - 13) << 23);   // 2^(E - 140)
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  pdl_launch_dependents();   // after the TMEM allocation
-  const uint32_t tmem = *tmem_slot;
+  if (threadIdx.x == 0) {
+    int32_t* s_unit = reinterpret_cast<int32_t*>(smem + C::OFF_UNIT);
+    s_unit[0] = w.slot;
+    s_unit[1] = tok0;
+    s_unit[2] = tok_end;
+    s_unit[3] = w.kvh;
+    s_unit[4] = split ? 1 : 0;
+  }
+  // Barriers initialised, TMEM allocated, Q in shared memory.
+  auto set_up = [&]() {
+    __syncthreads();
+    tc_fence_after();
+    pdl_launch_dependents();
+  };
 
   if (warp < C::SOFT_WARPS) {
+    set_up();
+    const uint32_t tmem = *tmem_slot;
     // ------------------------------------------------------------ softmax
     const int n = x == 0 ? n0 : n1;
     if (n > 0) {
       const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-      const uint32_t ts = tmem + lanes + uint32_t(x * 256), to = ts + 128;
+      const uint32_t s_at = tmem + lanes + uint32_t(x * 256);   // O: 128 columns on
       const bool any_row = __any_sync(0xffffffffu, row_ok);
       const int lim = w.causal ? w.lim0 + (tok - w.tok_first) : w.lim0;
       const int end = (row_ok ? min(lim, w.k1) : 0) - w.k0;
@@ -396,7 +424,7 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
           const int vis = end - t * kTile;   // visible columns: [0, vis)
           const bool full = __all_sync(0xffffffffu, vis >= kTile || !row_ok);
           uint32_t r[32];
-          float top = att_max<2>(ts + 64 * half, vis - 64 * half, full, r);
+          float top = att_max<2>(s_at + 64 * half, vis - 64 * half, full, r);
           float* mx = s_row + (i & 1) * 2 * kTile;
           mx[half * kTile + row] = top;
           meet();
@@ -418,10 +446,10 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
             if (i > 0) {
               for (int cc = half * (D / 16); cc < (half + 1) * (D / 16); ++cc) {
                 uint32_t o[8];
-                tmem_ld8(to + cc * 8, o);
+                tmem_ld8(s_at + 128 + cc * 8, o);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * s);
-                tmem_st8(to + cc * 8, o);
+                tmem_st8(s_at + 128 + cc * 8, o);
               }
             }
           }
@@ -434,14 +462,14 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
             // 32 columns; P takes the columns of the first 32 of its 64, which have been read
             const int blk = half * 2 + b;
             if (b > 0) {
-              tmem_ld32_async(ts + 32 * blk, r);
+              tmem_ld32_async(s_at + 32 * blk, r);
               tmem_wait_ld(r);
               if (!full) mask_cols(r, vis - 32 * blk);
             }
             uint32_t h[16];
             att_exp32(r, c2, s2, acc, h);
             if (nan_v) att_poison32(h, meta.v_nan[blk], vis - 32 * blk);
-            tmem_st16(ts + 64 * (blk >> 1) + 16 * (blk & 1), h);
+            tmem_st16(s_at + 64 * (blk >> 1) + 16 * (blk & 1), h);
           }
           l += acc.x + acc.y;
           tmem_wait_st();
@@ -462,23 +490,44 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
         l = half == 0 ? l + sum[kTile + row] : sum[row] + l;
         if (ok) {
           tc_fence_after();
-          // O' * 2^(vref - 134) / l', both with the same lift
+          const int32_t* s_unit = reinterpret_cast<const int32_t*>(smem + C::OFF_UNIT);
+          const int tok = s_unit[1] + (s_unit[4] ? 0 : x * p.tt) + row / p.G;
+          const bool row_ok = row < p.tt * p.G && tok < s_unit[2];
+          const int64_t part = (int64_t(s_unit[0] + (s_unit[4] ? x : 0)) * p.Tq + tok) * p.H + s_unit[3] * p.G + row % p.G;
+          if (row_ok && half == 0) p.part_lse[part] = l == 0.f ? kNegInf : m + (log2f(l) - kAttLift);
+          // O' * 2^(vref - 134) / l', both with the same lift; -1: not written
           const float inv = l == 0.f ? 0.f : 1.f / l;
           const float vs = __uint_as_float(uint32_t(vref - 7) << 23);
-#pragma unroll
-          for (int j8 = 0; j8 < D / 16; ++j8) {
-            const int cc = half * (D / 16) + j8;
+          const int64_t at = row_ok && l != 0.f ? part * D + half * (D / 2) : -1;
+          // 32 columns at a time through shared memory (4 KB of Q's, which is
+          // done with), so that eight lanes store 128 bytes of a row
+          uint8_t* buf = smem + C::OFF_Q + x * C::TILE_BYTES + (warp & 7) * (C::TILE_BYTES / 8 < 4096 ? C::TILE_BYTES / 8 : 4096);
+          constexpr int UNITS = C::TILE_BYTES / 8 < 4096 ? 4 : 8;   // 16-byte pieces of a row at a time
+#pragma unroll 1
+          for (int c0 = 0; c0 < D / 2; c0 += 4 * UNITS) {
             uint32_t o[8];
-            tmem_ld8(to + cc * 8, o);
-            if (row_ok && l != 0.f) {
-              float4* dst = reinterpret_cast<float4*>(p.part_o + part * D + cc * 8);
 #pragma unroll
-              for (int j = 0; j < 2; ++j)
-                dst[j] = make_float4(__uint_as_float(o[4 * j]) * inv * vs, __uint_as_float(o[4 * j + 1]) * inv * vs,
-                                     __uint_as_float(o[4 * j + 2]) * inv * vs, __uint_as_float(o[4 * j + 3]) * inv * vs);
+            for (int i = 0; i < UNITS / 2; ++i) {
+              if (c0 + 8 * i < D / 2) {
+                tmem_ld8(s_at + 128 + half * (D / 2) + c0 + 8 * i, o);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                  *reinterpret_cast<float4*>(buf + (row & 31) * (16 * UNITS) + (((2 * i + j) ^ (row & (UNITS - 1))) << 4)) =
+                      make_float4(__uint_as_float(o[4 * j]) * inv * vs, __uint_as_float(o[4 * j + 1]) * inv * vs,
+                                  __uint_as_float(o[4 * j + 2]) * inv * vs, __uint_as_float(o[4 * j + 3]) * inv * vs);
+              }
             }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < UNITS; ++k) {
+              const int idx = 32 * k + lane, r = idx / UNITS, u = idx % UNITS;
+              const int64_t dst = __shfl_sync(0xffffffffu, at, r);
+              if (dst >= 0 && c0 + 4 * u < D / 2)
+                *reinterpret_cast<float4*>(p.part_o + dst + c0 + 4 * u) =
+                    *reinterpret_cast<const float4*>(buf + r * (16 * UNITS) + ((u ^ (r & (UNITS - 1))) << 4));
+            }
+            __syncwarp();
           }
-          if (row_ok && half == 0) p.part_lse[part] = l == 0.f ? kNegInf : m + (log2f(l) - kAttLift);
         }
       }
     }
@@ -487,6 +536,8 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
     // The pipelines take turns: O product of one, then its next S product,
     // while the other's softmax runs. P lies over S, so the O product must
     // have read it before the next S product is issued.
+    set_up();
+    const uint32_t tmem = *tmem_slot;
     if (lane == 0) {
       constexpr uint32_t kIdS = idesc_f16_f32(kTile, kTile, false);
       constexpr uint32_t kIdO = idesc_f16_f32(kTile, D, true);
@@ -552,7 +603,6 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
     // ------------------------------------------------------------ converters
     const bool do_k = warp < C::CONV_WARP + 4;   // four warps for K, four for V
     const int tid = (int(threadIdx.x) - 32 * C::CONV_WARP) & (kTile - 1);
-    const int first_page = w.k0 >> p.page_shift;
     const int mask = (1 << p.page_shift) - 1;
     const int keys = w.k1 - w.k0;
     uint32_t* fac_k = s_fac;
@@ -613,6 +663,7 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
     };
     uint32_t ke = do_k ? load_exps(0, p.k_exps) : 0u, ve = load_exps(0, p.v_exps);
     load(0);
+    set_up();
     int vref = 0;
     bool ok = true;
     for (int t = 0; t < tiles; ++t) {
@@ -661,7 +712,7 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == C::MMA_WARP) tmem_dealloc(tmem, 512);
+  if (warp == C::MMA_WARP) tmem_dealloc(*tmem_slot, 512);
 }
 
 // Joins a row's partial results: out = sum_c 2^(lse_c - lse) o_c. WPR warps
@@ -811,11 +862,13 @@ cudaError_t launch_attend(int head_dim, const AttParams& p, int64_t units, cudaS
 namespace {
 template <int D>
 cudaError_t launch_join_t(const AttParams& p, cudaStream_t stream) {
-  // more than eight partials: the whole CTA takes one row
-  const int per_cta = p.slots > 8 ? 1 : kJoinWarps;
-  const unsigned blocks = unsigned(ceil_div(int64_t(p.Tq) * p.H, per_cta));
-  return p.slots > 8 ? launch_kernel(attend_join_kernel<D, kJoinWarps>, dim3(blocks), 32 * kJoinWarps, 0, stream, 1, p)
-                     : launch_kernel(attend_join_kernel<D, 1>, dim3(blocks), 32 * kJoinWarps, 0, stream, 1, p);
+  // few rows with more than eight partials: the whole CTA takes one row (2,048
+  // rows of 38 partials: 15 -> 10 us; 18,320 rows of 14: 24 against 45 us)
+  const int64_t rows = int64_t(p.Tq) * p.H;
+  const bool shared = p.slots > 8 && rows <= 8192;
+  const unsigned blocks = unsigned(ceil_div(rows, shared ? 1 : kJoinWarps));
+  return shared ? launch_kernel(attend_join_kernel<D, kJoinWarps>, dim3(blocks), 32 * kJoinWarps, 0, stream, 1, p)
+                : launch_kernel(attend_join_kernel<D, 1>, dim3(blocks), 32 * kJoinWarps, 0, stream, 1, p);
 }
 }  // namespace
 

@@ -112,7 +112,7 @@ struct AttParams {
   float c;                     // softmax_scale * log2(e)
   int G, tt, slots;
   AttPart pre, suf;
-  int64_t pre_units;           // prefix units of this launch (its first ones); the rest are suffix units
+  uint32_t pre_units;          // prefix units of this launch (its first ones); the rest are suffix units
   int late_wait;               // the launch before this one is of the same call: wait for it at the end
   float* part_lse;             // [slots][Tq][H], base 2
   float* part_o;               // [slots][Tq][H][d]
@@ -137,13 +137,13 @@ struct AttUnit {
 };
 
 // `per`: rows of a row group; the keys of a suffix unit end where its last row sees no further.
-__device__ __forceinline__ AttUnit att_unit(const AttParams& p, int64_t u, int per) {
+__device__ __forceinline__ AttUnit att_unit(const AttParams& p, uint32_t u, int per) {
   AttUnit w{};
   if (u < p.pre_units) {
-    w.group = int(u % p.pre.groups);   // neighbouring units share their keys
-    const int64_t ch = u / p.pre.groups;
-    w.kvh = int(ch % p.Hkv);
-    const int c = int(ch / p.Hkv);
+    const uint32_t ch = u / uint32_t(p.pre.groups);   // neighbouring units share their keys
+    w.group = int(u - ch * uint32_t(p.pre.groups));
+    const int c = int(ch / uint32_t(p.Hkv));
+    w.kvh = int(ch) - c * p.Hkv;
     w.slot = p.pre.slot0 + c * (p.pre.narrow ? 1 : 2);
     const int n = __ldg(p.prefix_len);
     w.tok_last = __ldg(p.cu_q + p.R);
@@ -155,12 +155,11 @@ __device__ __forceinline__ AttUnit att_unit(const AttParams& p, int64_t u, int p
     w.pages = p.prefix_pages;
   } else {
     u -= p.pre_units;
-    const int c = int(u % p.suf.chunks);
-    u /= p.suf.chunks;
-    w.group = int(u % p.suf.groups);
-    u /= p.suf.groups;
-    w.kvh = int(u % p.Hkv);
-    const int r = int(u / p.Hkv);
+    const uint32_t a1 = u / uint32_t(p.suf.chunks), a2 = a1 / uint32_t(p.suf.groups);
+    const int c = int(u - a1 * uint32_t(p.suf.chunks));
+    w.group = int(a1 - a2 * uint32_t(p.suf.groups));
+    const int r = int(a2 / uint32_t(p.Hkv));
+    w.kvh = int(a2) - r * p.Hkv;
     w.slot = p.suf.slot0 + c * (p.suf.narrow ? 1 : 2);
     const int a = __ldg(p.cu_q + r), b = __ldg(p.cu_q + r + 1);
     const int n = __ldg(p.suffix_lens + r);

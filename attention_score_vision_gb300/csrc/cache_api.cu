@@ -399,7 +399,7 @@ tsel_status tsel_prefix_attention(
   for (int kind = 0; kind <= 2; ++kind) {
     const int64_t pre = a.pre.narrow == kind ? a.pre.units : 0, suf = a.suf.narrow == kind ? a.suf.units : 0;
     if (pre + suf == 0) continue;
-    p.pre_units = pre;
+    p.pre_units = uint32_t(pre);
     p.late_wait = launched;
     e = kind == 0 ? launch_attend(head_dim, p, pre + suf, stream)
                   : launch_attend_narrow(head_dim, kind, p, pre + suf, stream);
