@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
     tc_fence_before();
   }
   pdl_wait();   // every input may come from an earlier kernel
-  const AttUnit w = att_unit(p, blockIdx.x, 2 * p.tt * p.G);
+  const AttUnit w = att_unit<uint32_t>(p, blockIdx.x, 2 * p.tt * p.G);
   const int tok0 = w.tok_first + w.group * 2 * p.tt;          // of row tile 0
   const int tok_end = min(w.tok_last, tok0 + 2 * p.tt);
   const int tiles = int(ceil_div(w.k1 - w.k0, kTile));

@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kNarThreads, NarCfg<D, NB>::CTAS) attend_narro
   // With late_wait the launch before this one is the wide kernel of the same
   // call. It let this one start after its own wait, so the inputs are final;
   // its completion is waited for at the end, for the launch that joins both.
-  const AttUnit w = att_unit(p, blockIdx.x, C::ROWS);
+  const AttUnit w = att_unit<int64_t>(p, blockIdx.x, C::ROWS);
   const int row0 = w.group * C::ROWS;
   const int rows = w.bad ? 0 : min((w.tok_last - w.tok_first) * p.G - row0, C::ROWS);
   if (w.bad && threadIdx.x == 0) set_status(p.status, TSEL_DEV_SEQLENS);
