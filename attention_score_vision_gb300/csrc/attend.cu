@@ -862,13 +862,15 @@ cudaError_t launch_attend(int head_dim, const AttParams& p, int64_t units, cudaS
 namespace {
 template <int D>
 cudaError_t launch_join_t(const AttParams& p, cudaStream_t stream) {
-  // few rows with more than eight partials: the whole CTA takes one row (2,048
-  // rows of 38 partials: 15 -> 10 us; 18,320 rows of 14: 24 against 45 us)
+  // Warps to a row with more than eight partials: all eight while the rows are
+  // fewer than the CTAs that fit (64 rows of 73 partials: a call takes 25.7 us,
+  // with two 26.9), two while a warp each would leave SMs idle (2,048 rows of 38:
+  // 82 us, with eight 85, with one 86); one otherwise (4,544 rows of 17: 90.5
+  // us, with two 91.1, with eight 96.3).
   const int64_t rows = int64_t(p.Tq) * p.H;
-  const bool shared = p.slots > 8 && rows <= 8192;
-  const unsigned blocks = unsigned(ceil_div(rows, shared ? 1 : kJoinWarps));
-  return shared ? launch_kernel(attend_join_kernel<D, kJoinWarps>, dim3(blocks), 32 * kJoinWarps, 0, stream, 1, p)
-                : launch_kernel(attend_join_kernel<D, 1>, dim3(blocks), 32 * kJoinWarps, 0, stream, 1, p);
+  const int wpr = p.slots <= 8 || rows > 4096 ? 1 : (rows > 1024 ? 2 : kJoinWarps);
+  auto kern = wpr == 1 ? attend_join_kernel<D, 1> : (wpr == 2 ? attend_join_kernel<D, 2> : attend_join_kernel<D, kJoinWarps>);
+  return launch_kernel(kern, dim3(unsigned(ceil_div(rows, kJoinWarps / wpr))), 32 * kJoinWarps, 0, stream, 1, p);
 }
 }  // namespace
 

@@ -18,7 +18,10 @@ constexpr int kAttMaxPages = kAttMaxChunkKeys / kAttMinPage;
 constexpr int kAttWideCtas = 152;
 constexpr int kAttNarrowCtas1 = 4 * 152, kAttNarrowCtas2 = 3 * 152;
 // Query rows (tokens times query heads per KV head) up to which the narrow
-// kernel takes the keys of a prefix or of a request's suffix.
+// kernel takes the keys of a prefix or of a request's suffix. Prefixes of 2,000
+// and of 36,831 keys, 8 KV heads of 128: 24 rows narrow 15.6 and 47.7 us, wide
+// 18.2 and 44.1; 32 rows 16.0 and 49.3 against 20.3 and 45.3; 48 rows 20.3 and
+// 62.7 against 21.2 and 47.1; 64 rows 19.4 and 75.9 against 21.8 and 47.8.
 constexpr int kAttNarrowRows = 32;
 
 // How the prefix, or the suffixes, are cut into units: (key chunk, KV head, row
@@ -39,19 +42,28 @@ struct AttPlan {
   int64_t lse_off, o_off, total;   // workspace
 };
 
-// Chunks for `base` units of `tiles` 128-key tiles each on `ctas` CTAs: the
-// count with the least estimated time, in key tiles. A unit costs its tiles
-// plus `start` for its start-up and write-out, and joining costs a little for
-// each chunk.
-inline int att_chunks(int64_t base, int tiles, int ctas, double start, int least) {
+// Chunks, at least `least`, for `base` units of `tiles` 128-key tiles each on
+// `ctas` CTAs: the count with the least estimated time, in key tiles. A unit
+// costs its tiles plus a start-up, and joining costs a little for each chunk.
+//   Wide units (start-up 3 tiles) fill their SMs and take equal times: whole
+// waves of them count.
+//   Narrow units (start-up 1 tile) share theirs. Beyond one full wave they even
+// out over the SMs, less half a unit at the end, but a wave that is barely
+// exceeded costs half of another: 16 requests with 4,000 keys each, 8 KV heads
+// of 128, in 4, 8, 16 chunks: 32.4, 23.2, 27.1 us; 64 such requests in 1, 4, 16
+// chunks: 88.8, 65.1, 79.5 us; a prefix of 36,831 keys and 8 rows in 58, 72, 96
+// chunks (0.8, 0.9, 1.3 waves): 27.2, 25.3, 29.2 us.
+inline int att_chunks(int64_t base, int tiles, int ctas, bool narrow, int least) {
   if (tiles <= 1 || base < 1) return tiles < 1 ? 0 : 1;
   int best = least;
   double best_cost = 1e300;
   for (int n = least; n <= tiles && n <= 256 + least; ++n) {
     const int per = int(ceil_div(tiles, n));
     if (n > least && int(ceil_div(tiles, per)) < n) continue;   // the same tiles in fewer chunks
-    const double waves = double(ceil_div(base * n, ctas));
-    const double cost = waves * (per + start) + 0.05 * n;
+    const double fill = double(base * n) / ctas;
+    const double waves = !narrow ? double(ceil_div(base * n, ctas))
+                                 : (fill <= 1.0 ? 1.0 : (fill < 1.5 ? 1.5 : fill)) + 0.5;
+    const double cost = waves * (per + (narrow ? 1.0 : 3.0)) + 0.05 * n;
     if (cost < best_cost) {
       best_cost = cost;
       best = n;
@@ -69,8 +81,8 @@ inline AttPart att_part(int64_t requests, int tokens, int max_keys, int Hkv, int
   const int tiles = int(ceil_div(max_keys, kTile));
   const int64_t base = requests * Hkv * a.groups;
   if (base < 1 || tiles < 1) return a;
-  a.chunks = a.narrow ? att_chunks(base, tiles, a.narrow == 1 ? kAttNarrowCtas1 : kAttNarrowCtas2, 1.0, 1)
-                      : att_chunks(base, tiles, kAttWideCtas, 3.0, int(ceil_div(tiles, kAttMaxChunkKeys / kTile)));
+  a.chunks = a.narrow ? att_chunks(base, tiles, a.narrow == 1 ? kAttNarrowCtas1 : kAttNarrowCtas2, true, 1)
+                      : att_chunks(base, tiles, kAttWideCtas, false, int(ceil_div(tiles, kAttMaxChunkKeys / kTile)));
   a.keys = int(ceil_div(tiles, a.chunks)) * kTile;
   a.units = base * a.chunks;
   *slots += a.chunks * (a.narrow ? 1 : 2);
