@@ -567,7 +567,11 @@ def _rows(t: torch.Tensor, name: str, device=None, dtype=None, shape=None) -> in
     n, h, d = have
     if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
         raise ValueError(f"{name} must have contiguous [heads, head_dim] rows")
-    return t.stride(0) if n > 1 else 0
+    if n <= 1:
+        return 0
+    if t.stride(0) <= 0:   # expanded: 0 would mean dense
+        raise ValueError(f"{name} must not be an expanded tensor")
+    return t.stride(0)
 
 
 def _vector(t: torch.Tensor, dtype, name: str, device, numel: Optional[int] = None) -> None:
@@ -594,9 +598,20 @@ def _rope_args(pos, table, total: int, device):
     return pos.data_ptr(), pos.shape[1], table.data_ptr(), table.numel()
 
 
-def _workspace(workspace: Optional[torch.Tensor], nbytes: int, device) -> torch.Tensor:
+def _new(stream, make, *args, device, **kw):
+    """make(*args, device=device, **kw) with memory of `stream`: what a call
+    allocates is cleared, used and freed in the order of the stream it runs on."""
+    if stream is None:
+        return make(*args, device=device, **kw)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return make(*args, device=device, **kw)
+
+
+def _workspace(workspace: Optional[torch.Tensor], nbytes: int, device, stream) -> torch.Tensor:
     if workspace is None:
-        return _new_workspace(nbytes, device)
+        return _new(stream, _new_workspace, nbytes, device=device)
     if workspace.device != device:
         raise ValueError(f"workspace must be on {device}")
     return workspace
@@ -650,10 +665,10 @@ def tsel_rope(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, tab
     qos = 0 if q_out is None else _rows(q_out, "q_out", dev, dtype, (total, H, d))
     kos = 0 if k_out is None else _rows(k_out, "k_out", dev, dtype, (total, Hkv, d))
     if q_out is None:
-        q_out = torch.empty((total, H, d), dtype=dtype, device=dev)
+        q_out = _new(stream, torch.empty, (total, H, d), dtype=dtype, device=dev)
     if k is not None and k_out is None:
-        k_out = torch.empty((total, Hkv, d), dtype=dtype, device=dev)
-    workspace = _workspace(workspace, 1024, dev)
+        k_out = _new(stream, torch.empty, (total, Hkv, d), dtype=dtype, device=dev)
+    workspace = _workspace(workspace, 1024, dev, stream)
     _call(load_library().tsel_rope, dev, stream, q.data_ptr(), qs, _ptr(k), ks, pos_p, pos_dim,
           table_p, pairs, total, H, Hkv, d, _DTYPES[dtype], flags, q_out.data_ptr(), qos,
           _ptr(k_out), kos, workspace.data_ptr(), workspace.numel())
@@ -713,7 +728,7 @@ def tsel_cache_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cach
         raise ValueError("k and v do not match the cache's heads and head_dim")
     _vector(slots, torch.int32, "slots", dev, total)
     pos_p, pos_dim, table_p, pairs = _rope_args(pos, table, total, dev)
-    workspace = _workspace(workspace, 1024, dev)
+    workspace = _workspace(workspace, 1024, dev, stream)
     _call(load_library().tsel_cache_write, dev, stream, k.data_ptr(), ks, v.data_ptr(), vs, pos_p,
           pos_dim, table_p, pairs, slots.data_ptr(), total, Hkv, d, _DTYPES[dtype], flags, *cache_p,
           workspace.data_ptr(), workspace.numel())
@@ -733,10 +748,10 @@ def tsel_cache_read(cache: TselCache, slots: torch.Tensor, *, dtype=torch.bfloat
     kos = 0 if k_out is None else _rows(k_out, "k_out", dev, dtype, shape)
     vos = 0 if v_out is None else _rows(v_out, "v_out", dev, dtype, shape)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=dev)
+        k_out = _new(stream, torch.empty, shape, dtype=dtype, device=dev)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=dev)
-    workspace = _workspace(workspace, 1024, dev)
+        v_out = _new(stream, torch.empty, shape, dtype=dtype, device=dev)
+    workspace = _workspace(workspace, 1024, dev, stream)
     _call(load_library().tsel_cache_read, dev, stream, *cache_p, slots.data_ptr(), shape[0], Hkv, d,
           _DTYPES[dtype], k_out.data_ptr(), kos, v_out.data_ptr(), vos, workspace.data_ptr(),
           workspace.numel())
@@ -801,6 +816,8 @@ def tsel_prefix_attention(q: torch.Tensor, cu_seqlens_q: torch.Tensor, max_seqle
             raise ValueError(f"page_table must be on {dev}")
         if page_table.dim() != 2 or page_table.shape[0] != R or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
             raise ValueError("page_table must be an int32 [requests, pages] tensor with contiguous rows")
+        if R > 1 and page_table.stride(0) < page_table.shape[1]:
+            raise ValueError("page_table rows must not overlap")
         if page_table.shape[1] * page_size < max_s:
             raise ValueError("page_table rows hold fewer than max_suffix_len keys")
         table_stride = page_table.stride(0) if R > 1 else page_table.shape[1]
@@ -808,14 +825,15 @@ def tsel_prefix_attention(q: torch.Tensor, cu_seqlens_q: torch.Tensor, max_seqle
     os_ = 0 if out is None else _rows(out, "out", dev, q.dtype, (tq, H, d))
     if lse is not None:
         _vector(lse, torch.float32, "lse", dev, H * tq)
-    if workspace is not None and workspace.device != dev:
-        raise ValueError(f"workspace must be on {dev}")
-    if out is None:
-        out = torch.empty((tq, H, d), dtype=q.dtype, device=dev)
-    if lse is None and want_lse:
-        lse = torch.empty((H, tq), dtype=torch.float32, device=dev)
     if workspace is None:
-        workspace = _new_workspace(tsel_prefix_attention_workspace_size(R, tq, max_seqlen_q, H, Hkv, d, max_p, max_s), dev)
+        nbytes = tsel_prefix_attention_workspace_size(R, tq, max_seqlen_q, H, Hkv, d, max_p, max_s)
+    else:
+        nbytes = 0
+    workspace = _workspace(workspace, nbytes, dev, stream)
+    if out is None:
+        out = _new(stream, torch.empty, (tq, H, d), dtype=q.dtype, device=dev)
+    if lse is None and want_lse:
+        lse = _new(stream, torch.empty, (H, tq), dtype=torch.float32, device=dev)
     _call(load_library().tsel_prefix_attention, dev, stream, q.data_ptr(), qs,
           cu_seqlens_q.data_ptr(), R, tq, max_seqlen_q, *cache_p,
           _ptr(prefix_pages) if max_p > 0 else None, _ptr(prefix_len) if max_p > 0 else None, max_p,

@@ -12,6 +12,7 @@ namespace tsel {
 
 constexpr int kAttMaxChunkKeys = 8192;   // keys of a wide unit: bounds its page list in shared memory
 constexpr int kAttMinPage = 16;
+constexpr int kAttMaxKeys = 1 << 30;     // of a prefix or a suffix: key numbers and chunk ends stay in 31 bits
 constexpr int kAttMaxPages = kAttMaxChunkKeys / kAttMinPage;
 // CTAs resident at once on the 152 SMs: one wide CTA per SM, four or three narrow
 // ones. Constants, not queries: the workspace size must follow from the sizes alone.
@@ -40,6 +41,7 @@ struct AttPlan {
   AttPart pre, suf;
   int slots;
   int64_t lse_off, o_off, total;   // workspace
+  bool too_large;      // units or partial results past what is counted in 31 bits or fits any memory
 };
 
 // Chunks, at least `least`, for `base` units of `tiles` 128-key tiles each on
@@ -96,6 +98,8 @@ inline AttPlan att_plan(int R, int Tq, int max_q, int H, int Hkv, int d, int max
   a.tt = kTile / a.G;
   a.pre = att_part(1, Tq, max_prefix, Hkv, a.G, a.tt, &a.slots);
   a.suf = att_part(Tq > 0 ? R : 0, max_q, max_suffix, Hkv, a.G, a.tt, &a.slots);
+  a.too_large = a.pre.units + a.suf.units > 0x7FFFFFFFll || double(a.slots) * Tq * H * d > 1e15;
+  if (a.too_large) return a;
   a.lse_off = kWsHeaderBytes;
   a.o_off = align_up(a.lse_off + 4 * int64_t(a.slots) * Tq * H, 256);
   a.total = align_up(a.o_off + 4 * int64_t(a.slots) * Tq * H * d, 256);

@@ -81,9 +81,11 @@ int page_shift_of(int page_size) {
   return -1;
 }
 
+bool cache_head_dim(int d) { return d == 64 || d == 80 || d == 96 || d == 112 || d == 128; }
+
 tsel_status check_cache(const void* kp, const void* vp, const void* ke, const void* ve,
                         int num_pages, int page_size, int num_kv_heads, int head_dim) {
-  if (!(head_dim == 64 || head_dim == 80 || head_dim == 96 || head_dim == 112 || head_dim == 128))
+  if (!cache_head_dim(head_dim))
     return fail(TSEL_ERR_UNSUPPORTED, "head_dim=%d (supported: 64, 80, 96, 112, 128)", head_dim);
   if (page_shift_of(page_size) < 0)
     return fail(TSEL_ERR_UNSUPPORTED, "page_size=%d (supported: 16, 32, 64, 128)", page_size);
@@ -307,11 +309,13 @@ size_t tsel_prefix_attention_workspace_size(int num_req, int total_q, int max_se
                                             int num_heads, int num_kv_heads, int head_dim,
                                             int max_prefix_len, int max_suffix_len) {
   if (num_req < 0 || total_q < 0 || max_seqlen_q < 0 || num_kv_heads < 1 ||
-      num_heads < num_kv_heads || num_heads % num_kv_heads != 0 ||
-      num_heads / num_kv_heads > kTile || head_dim < 1 || max_prefix_len < 0 || max_suffix_len < 0)
+      num_heads < num_kv_heads || num_heads > 256 || num_heads % num_kv_heads != 0 ||
+      num_heads / num_kv_heads > kTile || !cache_head_dim(head_dim) || max_prefix_len < 0 ||
+      max_suffix_len < 0 || max_prefix_len > kAttMaxKeys || max_suffix_len > kAttMaxKeys)
     return 0;
-  return size_t(att_plan(num_req, total_q, max_seqlen_q, num_heads, num_kv_heads, head_dim,
-                         max_prefix_len, max_suffix_len).total);
+  const AttPlan a = att_plan(num_req, total_q, max_seqlen_q, num_heads, num_kv_heads, head_dim,
+                             max_prefix_len, max_suffix_len);
+  return a.too_large ? 0 : size_t(a.total);
 }
 
 tsel_status tsel_prefix_attention(
@@ -333,6 +337,9 @@ tsel_status tsel_prefix_attention(
     return fail(TSEL_ERR_UNSUPPORTED, "%d query heads per KV head (at most %d)",
                 num_heads / num_kv_heads, kTile);
   TSEL_TRY(check_cache(k_pages, v_pages, k_exps, v_exps, num_pages, page_size, num_kv_heads, head_dim));
+  if (max_prefix_len > kAttMaxKeys || max_suffix_len > kAttMaxKeys)
+    return fail(TSEL_ERR_UNSUPPORTED, "prefix of %d or suffix of %d keys (at most %d)", max_prefix_len,
+                max_suffix_len, kAttMaxKeys);
   if (!(softmax_scale == softmax_scale) || std::isinf(softmax_scale))
     return fail(TSEL_ERR_INVALID_VALUE, "softmax_scale");
   if (cu_seqlens_q == nullptr) return fail(TSEL_ERR_INVALID_VALUE, "null cu_seqlens_q");
@@ -346,10 +353,9 @@ tsel_status tsel_prefix_attention(
   TSEL_TRY(check_header(workspace, workspace_bytes));
   const AttPlan a = att_plan(num_req, total_q, max_seqlen_q, num_heads, num_kv_heads, head_dim,
                              max_prefix_len, max_suffix_len);
+  if (a.too_large) return fail(TSEL_ERR_UNSUPPORTED, "too many units of work");
   if (workspace_bytes < size_t(a.total))
     return fail(TSEL_ERR_WORKSPACE, "workspace %zu < %lld bytes", workspace_bytes, (long long)a.total);
-  if (a.pre.units + a.suf.units > 0x7FFFFFFFll)
-    return fail(TSEL_ERR_UNSUPPORTED, "too many units of work");
   if (total_q == 0) return TSEL_OK;
   AttParams p{};
   p.q_stride = q_row_stride;

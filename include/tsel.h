@@ -576,9 +576,11 @@ TSEL_API size_t tsel_prefix_attention_workspace_size(int num_req, int total_q, i
  *               least ceil(max_suffix_len / page_size)): the pages of request
  *               r's suffix in order; suffix_lens int32 [num_req] device, at
  *               most max_suffix_len. NULL allowed when max_suffix_len is 0.
- *               Only the pages that hold keys are read.
+ *               Only the pages that hold keys are read. max_prefix_len and
+ *               max_suffix_len are at most 2^30.
  * softmax_scale <= 0 selects 1/sqrt(head_dim).
  * out           as q; lse fp32 [num_heads, total_q] or NULL.
+ *               out may be q itself with the same stride.
  * workspace     >= tsel_prefix_attention_workspace_size(...): partial results
  *               of the key chunks; nothing in it outlives the call but the
  *               status word.

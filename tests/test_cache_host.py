@@ -206,7 +206,8 @@ def test_attention_host_checks(lib):
                        (dict(ms=-1), 1), (dict(cu=0), 1), (dict(pp=0), 1), (dict(pl=0), 1), (dict(pt=0), 1), (dict(sl=0), 1),
                        (dict(pts=3), 1), (dict(q=0), 1), (dict(q=8), 1), (dict(out=0), 1), (dict(qs=64), 1), (dict(os=260), 1),
                        (dict(scale=math.nan), 1), (dict(scale=math.inf), 1), (dict(ws=0), 1), (dict(ws=64), 3), (dict(wsb=4096), 3),
-                       (dict(kp=0), 1), (dict(ve=8), 1)):
+                       (dict(kp=0), 1), (dict(ve=8), 1), (dict(mp=2 ** 30 + 1), 2), (dict(ms=2 ** 30 + 1, pts=2 ** 27), 2),
+                       (dict(R=2 ** 31 - 1, tq=2 ** 31 - 1, mq=2 ** 31 - 1, mp=2 ** 30), 2)):
         assert _attend(lib, **over) == code, over
 
 
@@ -215,8 +216,10 @@ def test_attention_workspace_size(tsel):
     assert size(0, 0, 0, 4, 2, 64, 0, 0) == 1024
     assert size(64, 64, 1, 32, 8, 128, 40000, 1000) > 64 * 32 * 128 * 4
     for bad in ((-1, 4, 1, 4, 2, 64, 10, 10), (1, -4, 1, 4, 2, 64, 10, 10), (1, 4, 1, 5, 2, 64, 10, 10), (1, 4, 1, 4, 2, 64, -1, 10),
-                (1, 4, 1, 256, 1, 64, 10, 10)):
+                (1, 4, 1, 256, 1, 64, 10, 10), (1, 4, 1, 4, 2, 72, 10, 10), (1, 4, 1, 512, 256, 64, 10, 10), (1, 4, 1, 4, 2, 64, 2 ** 30 + 1, 10),
+                (1, 4, 1, 4, 2, 64, 10, 2 ** 30 + 1), (2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 1, 256, 256, 128, 2 ** 30, 2 ** 30)):
         assert size(*bad) == 0
+    assert size(1, 4, 1, 4, 2, 64, 2 ** 30, 2 ** 30) > 0
 
 
 # ------------------------------------------------------------------ refusals of the binding
@@ -273,6 +276,8 @@ def test_binding_refuses_what_the_kernels_cannot_see(tsel):
         lambda: tsel.tsel_rope(q, _Fake((5, 2, 64), bf, device=1), pos, table),
         lambda: tsel.tsel_rope(_Fake((5, 4, 64), bf, strides=(256, 1, 4)), k, pos, table),
         lambda: tsel.tsel_rope(q, None, pos, table, k_out=k),
+        lambda: tsel.tsel_rope(_Fake((5, 4, 64), bf, strides=(0, 64, 1)), k, pos, table),   # one row, expanded
+        lambda: tsel.tsel_cache_write(_Fake((5, 2, 64), bf, strides=(0, 64, 1)), k, slots, cache),
         lambda: tsel.tsel_rope(q, k, pos, table, q_out=k),
         lambda: tsel.tsel_cache_write(k, k, _Fake((4,), i32), cache),
         lambda: tsel.tsel_cache_write(k, k, _Fake((5,), torch.int64), cache),
@@ -295,6 +300,7 @@ def test_binding_refuses_what_the_kernels_cannot_see(tsel):
     bad += [attend(q=_Fake((5, 4, 64), torch.float32)), attend(cu=_Fake((3,), torch.int64)), attend(cu=_Fake((0,), i32)),
             attend(pp=None), attend(pl=None), attend(pp=_Fake((6,), i32)), attend(pt=None), attend(sl=None), attend(sl=_Fake((3,), i32)),
             attend(pt=_Fake((2, 3), i32)), attend(pt=_Fake((3, 4), i32)), attend(pt=_Fake((2, 4), i32, strides=(1, 2))),
+            attend(pt=_Fake((2, 4), i32, strides=(0, 1))), attend(out=_Fake((5, 4, 64), bf, strides=(0, 64, 1))),
             attend(cache=_fake_cache(tsel, d=80)), attend(out=_Fake((4, 4, 64), bf)), attend(lse=_Fake((3, 5), torch.float32)),
             attend(pp=_Fake((7,), i32, device=1)), attend(workspace=_Fake((1 << 20,), torch.uint8, device=1))]
     for i, fn in enumerate(bad):

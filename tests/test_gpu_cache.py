@@ -587,6 +587,167 @@ def test_attention_in_captured_graphs_that_share_a_workspace(tsel):
             assert torch.equal(o, eo) and torch.equal(l, el)
 
 
+WIDE = [
+    # more than 32 rows of a KV head: 128-row products; suffixes of both kinds beside them
+    ([33], [33], 513, 2, 2, 96, 64, HF),                 # one row more than the few-row kernel takes
+    ([45, 1, 20], [300, 1, 45], 700, 3, 1, 64, 16, HF),  # three heads: 42 tokens to a tile
+    ([50, 3], [64, 3], 1300, 4, 2, 80, 16, BF),
+    ([64, 70], [64, 900], 900, 2, 1, 112, 128, BF),
+    ([35], [500], 2100, 5, 1, 128, 32, HF),
+    ([150], [150], 100, 1, 1, 96, 16, BF),               # causal within and across key tiles
+    ([257], [257], 129, 1, 1, 80, 32, HF),               # three row tiles, the last of one row
+    ([1, 300, 2], [5, 310, 2], 0, 7, 7, 64, 64, BF),     # no prefix
+    ([1] * 40, [7] * 40, 1000, 4, 4, 128, 16, BF),       # prefix wide, suffixes of one row each
+    ([5] * 9, [33 * i for i in range(9)], 300, 6, 2, 112, 16, HF),   # suffixes of 15 rows
+    ([2, 1, 2], [90, 1, 30], 260, 10, 2, 96, 32, BF),    # prefix 25 rows, suffixes 10: two to a unit, both
+    ([1, 1, 1], [90, 1, 30], 260, 10, 2, 80, 32, HF),    # prefix 15 rows, suffixes 5: two launches of the few-row kernel
+]
+
+
+@pytest.mark.parametrize("case", WIDE, ids=[str(i) for i in range(len(WIDE))])
+def test_attention_row_counts_of_both_kernels(tsel, case):
+    rows, lens, prefix, H, Hkv, d, ps, dtype = case
+    b = Batch(tsel, 90 + prefix + d, rows, lens, prefix, H, Hkv, d, ps, dtype)
+    out, lse = b.run()
+    b.check(out, lse)
+
+
+@pytest.mark.parametrize("rows", [7, 8, 9, 15, 16, 17, 31, 32, 33])
+@pytest.mark.parametrize("d,dtype", [(64, HF), (128, BF)])
+def test_attention_around_the_row_limits(tsel, rows, d, dtype):
+    b = Batch(tsel, 200 + rows, [rows], [rows + 40], 270, 2, 2, d, 16, dtype)
+    out, lse = b.run()
+    b.check(out, lse)
+
+
+def _subset(b, out, lse, rows):
+    """Checks some rows of a batch of one request without a suffix."""
+    b.q, b.cu = b.q[rows], np.asarray([0, len(rows)], np.int32)
+    b.check(out[rows], lse[:, rows])
+
+
+def test_attention_chunks_of_the_longest_page_lists(tsel):
+    """76 row-tile pairs over 16,384 keys in pages of 16: two chunks of 512 pages."""
+    b = Batch(tsel, 31, [4864], [0], 16384, 4, 4, 64, 16, BF)
+    out, lse = b.run()
+    _subset(b, out, lse, [0, 127, 128, 255, 256, 2500, 4863])
+
+
+def test_attention_over_a_million_keys(tsel):
+    """More partial results to a row than one round of the joining warps takes."""
+    b = Batch(tsel, 32, [33], [0], 8192 * 130, 1, 1, 64, 128, BF, qscale=3.0)
+    out, lse = b.run()
+    _subset(b, out, lse, [0, 13, 32])
+
+
+@pytest.mark.parametrize("which", ["k_rows", "v_rows"])
+def test_attention_nan_rows_with_many_rows(tsel, which):
+    def nan_row(x):
+        x[100 + 40, 0, 3] = np.nan
+
+    # request 0: its row i sees 21 + i suffix keys, key 40 from i = 20 on
+    b = Batch(tsel, 33, [40, 2], [60, 20], 100, 4, 2, 80, 16, BF, **{which: nan_row})
+    out, lse = b.run()
+    want = torch.zeros(42, 4, dtype=torch.bool)
+    want[20:40, :2] = True
+    assert torch.equal(torch.isnan(out).any(-1).cpu(), want) and torch.equal(torch.isnan(out).all(-1).cpu(), want)
+    assert torch.equal(torch.isnan(lse).T.cpu(), want if which == "k_rows" else torch.zeros_like(want))
+    b.k, b.v = np.nan_to_num(b.k), np.nan_to_num(b.v)
+    ref, _, av, mag = O.prefix_attention(_np(b.q), b.cu, b.k, b.v, b.prefix_rows, b.suffix_rows, 80 ** -0.5)
+    tol = av * (2 * 80 * 2.0 ** -23 * mag[..., None] + 2.0 ** -10) + np.abs(ref) * 2.0 ** -8 + 1e-9
+    ok = ~want.numpy()
+    assert np.all(np.abs(_np(out) - ref)[ok] <= tol[ok])
+
+
+@pytest.mark.parametrize("rows", [[2, 1], [70, 2]])
+def test_attention_bad_pages_reach_their_request_only(tsel, rows):
+    b = Batch(tsel, 34, rows, [90, 20], 200, 4, 2, 64, 16, BF)
+    out, lse = b.run()
+    b.table[0, 2] = -5
+    b.table[0, 4] = 2 ** 30
+    got, gl = b.run(status=tsel.TSEL_DEV_PAGES)
+    n = rows[0]
+    assert torch.equal(got[n:], out[n:]) and torch.equal(gl[:, n:], lse[:, n:])
+    assert torch.isfinite(got).all()                        # the pages' keys are zeros
+
+
+def test_attention_into_q(tsel):
+    for rows in ([3, 1], [60, 1]):
+        b = Batch(tsel, 35, rows, [70, 9], 300, 4, 2, 128, 32, BF)
+        out, lse = b.run()
+        again, _ = b.run(out=b.q)
+        assert again.data_ptr() == b.q.data_ptr() and torch.equal(again, out)
+
+
+def test_calls_on_their_own_streams_at_once(tsel):
+    """Calls that run beside one another, with workspaces and outputs that the
+    calls allocate on the stream they are given."""
+    made = []
+    for i, rows in enumerate(([1] * 6, [90, 3], [4], [200])):
+        b = Batch(tsel, 36 + i, rows, [60] * len(rows) if max(rows) < 60 else [300] * len(rows), 3000, 8, 2, 128, 16, BF)
+        made.append((b, b.args(), b.run()))
+    x = torch.randn(500, 8, 128, device="cuda").to(BF)
+    pos = torch.arange(1000, dtype=torch.int32, device="cuda").view(500, 2)
+    table, _, _ = _table(tsel, [32, 32], "sectioned")
+    turned, _ = tsel.tsel_rope(x, None, pos, table)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in made]
+    for _ in range(5):
+        got = []
+        for st, (b, a, _) in zip(streams, made):
+            handle = st if len(got) % 2 else st.cuda_stream
+            y, _ = tsel.tsel_rope(x, None, pos, table, stream=handle)
+            got.append((y, *tsel.tsel_prefix_attention(b.q, *a, stream=handle)))
+        torch.cuda.synchronize()
+        for (y, o, l), (b, _, (out, lse)) in zip(got, made):
+            assert torch.equal(y, turned) and torch.equal(o, out) and torch.equal(l, lse)
+
+
+def test_attention_graphs_of_many_rows(tsel):
+    """A captured batch whose prefix takes the wide kernel and whose suffixes the
+    few-row one, and one of two wide parts, replayed in turn in one workspace
+    while lengths change in place."""
+    made = []
+    ws = torch.zeros(1 << 24, dtype=torch.uint8, device="cuda")
+    for rows, lens in (([1] * 50, [5 * i for i in range(50)]), ([40, 60, 1], [50, 77, 1])):
+        b = Batch(tsel, 40, rows, lens, 900, 4, 2, 96, 16, HF)
+        a = b.args()
+        tsel.tsel_prefix_attention(b.q, *a, workspace=ws)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got = tsel.tsel_prefix_attention(b.q, *a, workspace=ws)
+        made.append((b, a, g, got, list(lens)))
+    for prefix, cut in ((900, 0), (130, 3), (0, 10), (899, 0)):
+        for b, a, g, got, lens in made:
+            b.prefix, b.lens = prefix, [max(n - cut, 0) for n in lens]
+            a[4].fill_(prefix)
+            a[7].copy_(i32(b.lens))
+        for b, a, g, got, lens in made:
+            g.replay()
+        torch.cuda.synchronize()
+        assert tsel.tsel_read_device_status(ws) == 0
+        for b, a, g, (out, lse), lens in made:
+            o, l = tsel.tsel_prefix_attention(b.q, *a)
+            assert torch.equal(o, out) and torch.equal(l, lse)
+            full, rows_full = b.prefix_rows, b.suffix_rows
+            b.prefix_rows, b.suffix_rows = full[:prefix], [r[:n] for r, n in zip(rows_full, b.lens)]
+            b.check(out, lse)
+            b.prefix_rows, b.suffix_rows = full, rows_full
+
+
+def test_expanded_tensors_are_refused(tsel):
+    b = Batch(tsel, 41, [1, 1], [9, 9], 40, 4, 2, 64, 16, BF)
+    a = b.args()
+    one = b.q[:1].expand(2, 4, 64)
+    table, _, _ = _table(tsel, [32], "sectioned")
+    for call in (lambda: tsel.tsel_prefix_attention(one, *a),
+                 lambda: tsel.tsel_prefix_attention(b.q, *a, out=one),
+                 lambda: tsel.tsel_rope(one, None, i32([[1], [2]]), table),
+                 lambda: tsel.tsel_cache_write(one[:, :2], one[:, :2], i32([0, 1]), b.cache)):
+        with pytest.raises(ValueError):
+            call()
+
+
 # ------------------------------------------------------------------ together
 
 def test_the_path_from_scoring_to_answers(tsel):
