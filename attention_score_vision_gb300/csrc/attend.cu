@@ -48,7 +48,10 @@ namespace tsel {
 
 namespace {
 
-constexpr int kAttMetaRing = 4;
+// The converters write a tile's entry before they wait for its stage. While a
+// pipeline of a split unit is at tile t, its tile t + 2 is converted but not
+// multiplied yet, the other pipeline's t + 3 may be, and t + 4 is entered: five.
+constexpr int kAttMetaRing = 8;
 constexpr float kAttLift = 6.f;       // P = 2^6 at the row's reference
 constexpr float kAttSlack = 9.f;      // the reference may lag the row maximum by 2^9
 constexpr int kAttVSlack = 2;         // a moved V reference leaves room for 2^2 larger scales
@@ -66,8 +69,8 @@ struct AttCfg {
   static constexpr int KS = 2;                              // K and V stages
   static constexpr int SOFT_PER_TILE = 8;                   // softmax warps of a row tile: two threads per row
   static constexpr int SOFT_WARPS = 2 * SOFT_PER_TILE;
-  static constexpr int MMA_WARP = SOFT_WARPS;               // one issuing thread
-  static constexpr int CONV_WARP = MMA_WARP + 1;            // four warps for K, four for V
+  static constexpr int MMA_WARP = SOFT_WARPS;               // one issuing thread for each pipeline
+  static constexpr int CONV_WARP = MMA_WARP + 2;            // four warps for K, four for V
   static constexpr int WARPS = CONV_WARP + 8;
   static constexpr int THREADS = 32 * WARPS;
   static constexpr int OFF_Q = 0;
@@ -77,7 +80,7 @@ struct AttCfg {
   static constexpr int OFF_PAGES = OFF_FAC + 2 * 2 * kTile * 4;
   static constexpr int OFF_ROW = OFF_PAGES + kAttMaxPages * 4;   // fp32 [row tile][parity][half][128]
   static constexpr int OFF_META = OFF_ROW + 2 * 2 * 2 * kTile * 4;
-  static constexpr int NUM_BARS = 4 * KS + 3 * 2;
+  static constexpr int NUM_BARS = 4 * KS + 3 * 4;
   static constexpr int OFF_BAR = OFF_META + kAttMetaRing * int(sizeof(AttTileMeta));
   static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;
   static constexpr int OFF_UNIT = OFF_MISC + 16;            // what the epilogue needs of the unit
@@ -119,6 +122,32 @@ __device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uin
       : "memory");
 }
 
+__device__ __forceinline__ void mma_ss_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts_elect(uint32_t d_tmem, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit_elect(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "elect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
@@ -147,6 +176,9 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
       : "r"(taddr)
       : "memory");
 }
+
+// Keeps the compiler from computing x again where it is used.
+__device__ __forceinline__ void opaque(int& x) { asm volatile("" : "+r"(x)); }
 
 // Two fp32 values as fp16 (x in the low half).
 __device__ __forceinline__ uint32_t pack_f16(float x, float y) {
@@ -185,22 +217,6 @@ __device__ __forceinline__ uint32_t max_byte(uint32_t w) {
   return m;
 }
 
-// Largest of NB * 32 columns of S, masked to the visible ones; the first 32
-// stay in r. One 32-column load at a time: a second one in flight would not
-// fit the registers, and spills cost more than the TMEM latency.
-template <int NB>
-__device__ __forceinline__ float att_max(uint32_t taddr, int vis, bool full, uint32_t (&r)[32]) {
-  float top = kNegInf;
-#pragma unroll
-  for (int b = NB - 1; b >= 0; --b) {
-    tmem_ld32_async(taddr + 32 * b, r);
-    tmem_wait_ld(r);
-    if (!full) mask_cols(r, vis - 32 * b);
-    top = fmaxf(top, cols_max(r));
-  }
-  return top;
-}
-
 // exp2(S * c + shift) of 32 columns, added up in acc and packed to fp16. nan:
 // columns whose V row is NaN (bit per column).
 __device__ __forceinline__ void att_exp32(const uint32_t (&r)[32], float2 c2, float2 s2, float2& acc,
@@ -234,9 +250,9 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
   uint64_t* k_free = k_full + C::KS;        // [KS] S products of the tile done
   uint64_t* v_full = k_free + C::KS;        // [KS]
   uint64_t* v_free = v_full + C::KS;        // [KS]
-  uint64_t* s_full = v_free + C::KS;        // [2] S in TMEM
-  uint64_t* p_full = s_full + 2;            // [2] P in TMEM
-  uint64_t* o_done = p_full + 2;            // [2] O product done
+  uint64_t* s_full = v_free + C::KS;        // [pipeline][half tile] S in TMEM
+  uint64_t* p_full = s_full + 4;            // P in TMEM
+  uint64_t* o_done = p_full + 4;            // O product done
   int32_t* s_pages = reinterpret_cast<int32_t*>(smem + C::OFF_PAGES);
   AttTileMeta* s_meta = reinterpret_cast<AttTileMeta*>(smem + C::OFF_META);
   uint32_t* s_fac = reinterpret_cast<uint32_t*>(smem + C::OFF_FAC);
@@ -252,11 +268,11 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
     if (lane == 0) {
       for (int i = 0; i < C::KS; ++i) {
         mbar_init(&k_full[i], 4);
-        mbar_init(&k_free[i], 1);
+        mbar_init(&k_free[i], 2);
         mbar_init(&v_full[i], 4);
-        mbar_init(&v_free[i], 1);
+        mbar_init(&v_free[i], 2);
       }
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 4; ++i) {
         mbar_init(&s_full[i], 1);
         mbar_init(&p_full[i], C::SOFT_PER_TILE);
         mbar_init(&o_done[i], 1);
@@ -403,16 +419,34 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
       const uint32_t s_at = tmem + lanes + uint32_t(x * 256);   // O: 128 columns on
       const bool any_row = __any_sync(0xffffffffu, row_ok);
       const int lim = w.causal ? w.lim0 + (tok - w.tok_first) : w.lim0;
-      const int end = (row_ok ? min(lim, w.k1) : 0) - w.k0;
+      int end = (row_ok ? min(lim, w.k1) : 0) - w.k0;
+      int min_end = int(__reduce_min_sync(0xffffffffu, row_ok ? max(end, 0) : 0x7FFFFFFF));   // of the warp's rows
+      // What the loop needs of the row is computed here, once: left alone, the
+      // compiler saves registers by dividing rows into tokens again for every tile.
+      opaque(end);
+      opaque(min_end);
       // the two warps of the same 32 rows meet at a barrier of their own
       const int pair_bar = 3 + x * 4 + (warp & 3);
       auto meet = [&]() { asm volatile("bar.sync %0, 64;" ::"r"(pair_bar) : "memory"); };
+      auto meet_any = [&](bool mine) -> bool {
+        uint32_t any;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t"
+            "setp.ne.u32 p, %1, 0;\n\t"
+            "bar.red.or.pred q, %2, 64, p;\n\t"
+            "selp.u32 %0, 1, 0, q;\n\t}"
+            : "=r"(any)
+            : "r"(uint32_t(mine)), "r"(pair_bar)
+            : "memory");
+        return any != 0;
+      };
       float m = kNegInf, l = 0.f;
       int vref = 0;
       bool ok = true;
-      for (int i = 0; i < n; ++i) {
-        const int t = split ? 2 * i + x : i;   // key tile
-        if (!warp_wait(&s_full[x], uint32_t(i & 1), abort_flag, T)) {
+#pragma unroll 1
+      for (int j = 0; j < 2 * n; ++j) {   // half tiles
+        const int i = j >> 1, hh = j & 1, t = split ? 2 * i + x : i;   // key tile
+        if (!warp_wait(&s_full[2 * x + hh], uint32_t(i & 1), abort_flag, T)) {
           // the loop goes on (the warps of a row meet in it), its waits return at once
           ok = false;
           if (lane == 0) *abort_flag = 1;
@@ -420,21 +454,25 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
         if (any_row) {
           tc_fence_after();
           const AttTileMeta& meta = s_meta[t & (kAttMetaRing - 1)];
-          const float ct = fmaxf(qc * meta.k_scale, 1e-38f);
-          const int vis = end - t * kTile;   // visible columns: [0, vis)
-          const bool full = __all_sync(0xffffffffu, vis >= kTile || !row_ok);
+          const int col = 64 * hh + 32 * half;        // first of this thread's columns of the tile
+          const int vis = end - t * kTile - col;      // visible ones: [0, vis)
+          const bool full = t * kTile + col + 32 <= min_end;
           uint32_t r[32];
-          float top = att_max<2>(s_at + 64 * half, vis - 64 * half, full, r);
-          float* mx = s_row + (i & 1) * 2 * kTile;
-          mx[half * kTile + row] = top;
-          meet();
-          top = fmaxf(top, mx[(half ^ 1) * kTile + row]);
-          top *= ct;
+          tmem_ld32_async(s_at + col, r);
+          const float ct = fmaxf(qc * meta.k_scale, 1e-38f);
           const int vnew = meta.v_ref;
-          const bool move = top > m + kAttSlack;
-          if (__any_sync(0xffffffffu, move) || vnew != vref) {
+          const uint32_t nan_v = meta.v_nan[2 * hh + half];
+          tmem_wait_ld(r);
+          if (!full) mask_cols(r, vis);
+          float top = cols_max(r) * ct;
+          // the two warps of the same rows go the same way
+          if (meet_any(top > m + kAttSlack || vnew != vref)) {
+            float* mx = s_row + (j & 1) * 2 * kTile;
+            mx[half * kTile + row] = top;
+            meet();
+            top = fmaxf(top, mx[(half ^ 1) * kTile + row]);
             float s = 1.f;
-            if (move) {
+            if (top > m) {   // also the rows that could still wait: once here, it costs nothing
               s = ex2(m - top);   // 0 at the row's first visible keys
               l *= s;
               m = top;
@@ -443,48 +481,42 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
             const int dv = vref - vnew;
             s *= dv < -126 ? 0.f : __uint_as_float(uint32_t(127 + dv) << 23);
             vref = vnew;
-            if (i > 0) {
+            if (j > 0) {   // once the O product of the half tile before is complete
+              if (!warp_wait(&o_done[2 * x + (hh ^ 1)], uint32_t(((j - 1) >> 1) & 1), abort_flag, T)) {
+                ok = false;
+                if (lane == 0) *abort_flag = 1;
+              }
+              tc_fence_after();
+#pragma unroll 1
               for (int cc = half * (D / 16); cc < (half + 1) * (D / 16); ++cc) {
                 uint32_t o[8];
                 tmem_ld8(s_at + 128 + cc * 8, o);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * s);
+                for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * s);
                 tmem_st8(s_at + 128 + cc * 8, o);
               }
             }
           }
           const float shift = m == kNegInf ? 0.f : kAttLift - m;
-          const float2 c2 = make_float2(ct, ct), s2 = make_float2(shift, shift);
           float2 acc = make_float2(0.f, 0.f);
-          const bool nan_v = (meta.v_nan[0] | meta.v_nan[1] | meta.v_nan[2] | meta.v_nan[3]) != 0;
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            // 32 columns; P takes the columns of the first 32 of its 64, which have been read
-            const int blk = half * 2 + b;
-            if (b > 0) {
-              tmem_ld32_async(s_at + 32 * blk, r);
-              tmem_wait_ld(r);
-              if (!full) mask_cols(r, vis - 32 * blk);
-            }
-            uint32_t h[16];
-            att_exp32(r, c2, s2, acc, h);
-            if (nan_v) att_poison32(h, meta.v_nan[blk], vis - 32 * blk);
-            tmem_st16(s_at + 64 * (blk >> 1) + 16 * (blk & 1), h);
-          }
+          uint32_t h[16];
+          att_exp32(r, make_float2(ct, ct), make_float2(shift, shift), acc, h);
+          if (nan_v) att_poison32(h, nan_v, vis);
+          tmem_st16(s_at + col, h);   // over the first of these columns
           l += acc.x + acc.y;
           tmem_wait_st();
           tc_fence_before();
         }
         __syncwarp();
-        mbar_arrive_lane0(&p_full[x], lane);
+        mbar_arrive_lane0(&p_full[2 * x + hh], lane);
       }
-      if (ok) ok = warp_wait(&o_done[x], uint32_t((n - 1) & 1), abort_flag, T);
+      if (ok) ok = warp_wait(&o_done[2 * x + 1], uint32_t((n - 1) & 1), abort_flag, T);
       if (!ok && lane == 0) {
         *abort_flag = 1;
         set_status(p.status, TSEL_DEV_TIMEOUT);
       }
       if (any_row) {
-        float* sum = s_row + (n & 1) * 2 * kTile;   // the parity that the last tile did not use
+        float* sum = s_row;   // the places that the last half tile did not use
         sum[half * kTile + row] = l;
         meet();
         l = half == 0 ? l + sum[kTile + row] : sum[row] + l;
@@ -533,71 +565,69 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
     }
   } else if (warp < C::CONV_WARP) {
     // ------------------------------------------------------------ MMA issuer
-    // The pipelines take turns: O product of one, then its next S product,
-    // while the other's softmax runs. P lies over S, so the O product must
-    // have read it before the next S product is issued.
+    // A thread for each pipeline. S has room for two half tiles of 64 keys: the
+    // product of one runs while the softmax warps are at the other, so they
+    // only wait for the tensor cores when those are behind. P lies over its S,
+    // so the O product must have read it before the next S product is issued.
+    // Both pipelines read a stage before it is free; where one reads it alone
+    // it stands for both.
     set_up();
-    const uint32_t tmem = *tmem_slot;
-    if (lane == 0) {
-      constexpr uint32_t kIdS = idesc_f16_f32(kTile, kTile, false);
+    const int xx = __shfl_sync(0xffffffffu, warp, 0) - C::MMA_WARP, n = xx == 0 ? n0 : n1;
+    if (n > 0) {
+      constexpr uint32_t kIdS = idesc_f16_f32(kTile, 64, false);
       constexpr uint32_t kIdO = idesc_f16_f32(kTile, D, true);
-      const uint32_t sq0 = smem_u32(smem + C::OFF_Q), sk0 = smem_u32(smem + C::OFF_K),
-                     sv0 = smem_u32(smem + C::OFF_V);
-      auto s_product = [&](int xx, int i) -> bool {
-        const int t = split ? 2 * i + xx : i, st = t % C::KS;
-        if (!wait_bounded(&k_full[st], uint32_t((t / C::KS) & 1), abort_flag, T) ||
-            (i > 0 && !wait_bounded(&o_done[xx], uint32_t((i - 1) & 1), abort_flag, T)))
+      const uint32_t ts = __shfl_sync(0xffffffffu, *tmem_slot, 0) + uint32_t(xx * 256);
+      // advanced by (bytes >> 4)
+      const uint64_t dq = smem_desc(smem_u32(smem + C::OFF_Q) + xx * C::TILE_BYTES, 2, 1024);
+      const uint64_t dk = smem_desc(smem_u32(smem + C::OFF_K), 2, 1024);
+      const uint64_t dv = smem_desc_mn(smem_u32(smem + C::OFF_V), kTile * 128, 1024);
+      auto s_product = [&](int j) -> bool {
+        const int i = j >> 1, hh = j & 1, t = split ? 2 * i + xx : i, st = t % C::KS;
+        if (!warp_wait(&k_full[st], uint32_t((t / C::KS) & 1), abort_flag, T) ||
+            (i > 0 && !warp_wait(&o_done[2 * xx + hh], uint32_t((i - 1) & 1), abort_flag, T)))
           return false;
         tc_fence_after();
-        const uint32_t ts = tmem + uint32_t(xx * 256);
-        const uint32_t sq = sq0 + xx * C::TILE_BYTES, sk = sk0 + st * C::TILE_BYTES;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
-          mma_bf16(ts, smem_desc(sq + off, 2, 1024), smem_desc(sk + off, 2, 1024), kIdS, kk > 0);
+          mma_ss_elect(ts + 64 * hh, dq + (off >> 4), dk + ((st * C::TILE_BYTES + hh * 8192 + off) >> 4), kIdS, kk > 0);
         }
-        mma_commit(&s_full[xx]);
-        if (split || xx == 1) mma_commit(&k_free[st]);   // its last reader
+        commit_elect(&s_full[2 * xx + hh]);
+        if (hh == 1) {
+          commit_elect(&k_free[st]);
+          if (split) commit_elect(&k_free[st]);
+        }
         return true;
       };
-      auto o_product = [&](int xx, int i) -> bool {
-        const int t = split ? 2 * i + xx : i, st = t % C::KS;
-        if (!wait_bounded(&v_full[st], uint32_t((t / C::KS) & 1), abort_flag, T) ||
-            !wait_bounded(&p_full[xx], uint32_t(i & 1), abort_flag, T))
-          return false;
+      bool ok = s_product(0) && s_product(1);
+      int done = 0;   // O products issued
+#pragma unroll 2
+      for (int j = 0; j < 2 * n && ok; ++j) {
+        const int i = j >> 1, hh = j & 1, t = split ? 2 * i + xx : i, st = t % C::KS;
+        ok = warp_wait(&v_full[st], uint32_t((t / C::KS) & 1), abort_flag, T) &&
+             warp_wait(&p_full[2 * xx + hh], uint32_t(i & 1), abort_flag, T);
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t ts = tmem + uint32_t(xx * 256), sv = sv0 + st * C::TILE_BYTES;
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          mma_f16_ta(ts + 128, ts + (kk >> 2) * 64 + (kk & 3) * 8,
-                     smem_desc_mn(sv + kk * 2048, kTile * 128, 1024), kIdO, i > 0 || kk > 0);
-        mma_commit(&o_done[xx]);
-        if (split || xx == 1) mma_commit(&v_free[st]);
-        return true;
-      };
-      bool ok = s_product(0, 0) && (n1 == 0 || s_product(1, 0));
-      int done0 = 0, done1 = 0;   // O products issued
-      for (int i = 0; i < n0 && ok; ++i) {
-        ok = o_product(0, i);
-        if (!ok) break;
-        done0 = i + 1;
-        if (i + 1 < n0) ok = s_product(0, i + 1);
-        if (!ok || i >= n1) continue;
-        ok = o_product(1, i);
-        if (!ok) break;
-        done1 = i + 1;
-        if (i + 1 < n1) ok = s_product(1, i + 1);
+        for (int kk = 0; kk < 4; ++kk)
+          mma_ts_elect(ts + 128, ts + 64 * hh + (kk >> 1) * 32 + (kk & 1) * 8,
+                     dv + ((st * C::TILE_BYTES + (4 * hh + kk) * 2048) >> 4), kIdO, j > 0 || kk > 0);
+        commit_elect(&o_done[2 * xx + hh]);
+        if (hh == 1) {
+          commit_elect(&v_free[st]);
+          if (split) commit_elect(&v_free[st]);
+        }
+        done = j + 1;
+        if (j + 2 < 2 * n) ok = s_product(j + 2);
       }
+      // every MMA this thread issued has completed before TMEM is freed
+      if (done > 0) wait_drain(&o_done[2 * xx + ((done - 1) & 1)], uint32_t(((done - 1) >> 1) & 1), T);
       if (!ok) {
         *abort_flag = 1;
         set_status(p.status, TSEL_DEV_TIMEOUT);
-        // one more phase, for whatever is in flight
-        mma_commit(&o_done[0]);
-        wait_drain(&o_done[0], uint32_t(done0 & 1), T);
+        commit_elect(&o_done[2 * xx + (done & 1)]);   // one more phase, for an S product in flight
+        wait_drain(&o_done[2 * xx + (done & 1)], uint32_t((done >> 1) & 1), T);
       }
-      // every MMA this thread issued has completed before TMEM is freed
-      if (done0 > 0 && ok) wait_drain(&o_done[0], uint32_t((done0 - 1) & 1), T);
-      if (done1 > 0) wait_drain(&o_done[1], uint32_t((done1 - 1) & 1), T);
     }
   } else {
     // ------------------------------------------------------------ converters
