@@ -290,11 +290,12 @@ __global__ void __launch_bounds__(kNarThreads, NarCfg<D, NB>::CTAS) attend_narro
         for (int n = 0; n < NB; ++n) mma_16816(q & 1 ? s1[n] : s[n], a, qb[n][4 * h + q][0], qb[n][4 * h + q][1]);
       }
     }
-    // ---- scales of keys g and g + 8: the byte is a float's exponent; 255 is an
-    // infinity, which makes NaN of the codes 0 that it comes with
+    // ---- scales of keys g and g + 8: the byte is a float's exponent; 0 is the
+    // denormal 2^-127, 255 an infinity, which makes NaN of the codes 0 that it comes with
     const uint8_t* ex = stage + C::SLOTS * 512;
-    const float kf[2] = {__uint_as_float(uint32_t(ex[g]) << 23), __uint_as_float(uint32_t(ex[8 + g]) << 23)};
-    float vf[2] = {__uint_as_float(uint32_t(ex[16 + g]) << 23), __uint_as_float(uint32_t(ex[24 + g]) << 23)};
+    auto scale = [](uint8_t e) -> float { return __uint_as_float(max(uint32_t(e) << 23, 0x400000u)); };
+    const float kf[2] = {scale(ex[g]), scale(ex[8 + g])};
+    float vf[2] = {scale(ex[16 + g]), scale(ex[24 + g])};
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
 #pragma unroll

@@ -640,6 +640,27 @@ def test_attention_over_a_million_keys(tsel):
     _subset(b, out, lse, [0, 13, 32])
 
 
+@pytest.mark.parametrize("rows", [1, 40])
+def test_attention_smallest_scales(tsel, rows):
+    """K and V rows whose scale is the least there is, 2^-127, under large queries."""
+    def tiny(x):
+        x *= 2.0 ** -122
+        x[::3] *= 16.0
+
+    b = Batch(tsel, 42, [rows], [rows + 50], 200, 4, 2, 64, 16, BF, spread=0, k_rows=tiny, qscale=2.0 ** 119)
+    assert (b.cache.k_exps.cpu().numpy() == 0).any()
+    out, lse = b.run()
+    b.check(out, lse)
+
+    def small(x):                                           # of one sign: outputs stay normal numbers
+        x[:] = (1 + np.abs(x)) * 2.0 ** -121
+
+    b = Batch(tsel, 43, [rows], [rows + 50], 200, 4, 2, 64, 16, BF, spread=0, v_rows=small)
+    assert (b.cache.v_exps.cpu().numpy() == 0).any()
+    out, lse = b.run()
+    b.check(out, lse)
+
+
 @pytest.mark.parametrize("which", ["k_rows", "v_rows"])
 def test_attention_nan_rows_with_many_rows(tsel, which):
     def nan_row(x):
