@@ -19,11 +19,16 @@ constexpr int kAttMaxPages = kAttMaxChunkKeys / kAttMinPage;
 constexpr int kAttWideCtas = 152;
 constexpr int kAttNarrowCtas1 = 4 * 152, kAttNarrowCtas2 = 3 * 152;
 // Query rows (tokens times query heads per KV head) up to which the narrow
-// kernel takes the keys of a prefix or of a request's suffix. Prefixes of 2,000
-// and of 36,831 keys, 8 KV heads of 128: 24 rows narrow 15.6 and 47.7 us, wide
-// 18.2 and 44.1; 32 rows 16.0 and 49.3 against 20.3 and 45.3; 48 rows 20.3 and
-// 62.7 against 21.2 and 47.1; 64 rows 19.4 and 75.9 against 21.8 and 47.8.
+// kernel takes the keys of a prefix or of a request's suffix. More than one
+// group of 16 rows reads the keys twice, which pays while start-up counts, or
+// while every SM has requests of its own. 8 KV heads of 128, narrow against wide:
+// 32 rows over one prefix of 600 keys 11.8 and 13.3 us, of 2,000 15.8 and 17.8,
+// of 5,000 18.8 and 17.7, of 12,000 25.0 and 25.4, of 36,831 53.5 and 43.2; 64
+// requests of 32 rows with up to 800 keys 42.7 and 59.3, with 3,000 102 and 148;
+// 64 rows over 2,000 keys 19.4 and 21.8, over 36,831 75.9 and 47.8.
 constexpr int kAttNarrowRows = 32;
+constexpr int kAttNarrowRowsLong = 16;         // past
+constexpr int kAttNarrowKeys = 16384;          // this many keys of few requests
 
 // How the prefix, or the suffixes, are cut into units: (key chunk, KV head, row
 // group), for the suffixes of each request.
@@ -77,7 +82,8 @@ inline int att_chunks(int64_t base, int tiles, int ctas, bool narrow, int least)
 inline AttPart att_part(int64_t requests, int tokens, int max_keys, int Hkv, int G, int tt, int* slots) {
   AttPart a{};
   const int64_t rows = int64_t(tokens) * G;
-  a.narrow = rows > kAttNarrowRows ? 0 : (rows > 8 ? 2 : 1);
+  const bool few = max_keys > kAttNarrowKeys && requests * Hkv < kAttWideCtas;
+  a.narrow = rows > (few ? kAttNarrowRowsLong : kAttNarrowRows) ? 0 : (rows > 8 ? 2 : 1);
   a.groups = int(a.narrow ? ceil_div(rows, 8 * a.narrow) : ceil_div(tokens, 2 * tt));
   a.slot0 = *slots;
   const int tiles = int(ceil_div(max_keys, kTile));

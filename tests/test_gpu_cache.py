@@ -620,6 +620,13 @@ def test_attention_around_the_row_limits(tsel, rows, d, dtype):
     b.check(out, lse)
 
 
+@pytest.mark.parametrize("rows", [16, 17])
+def test_attention_few_rows_over_a_long_prefix(tsel, rows):
+    b = Batch(tsel, 230 + rows, [rows], [20], 17000, 1, 1, 64, 64, BF)
+    out, lse = b.run()
+    b.check(out, lse)
+
+
 def _subset(b, out, lse, rows):
     """Checks some rows of a batch of one request without a suffix."""
     b.q, b.cu = b.q[rows], np.asarray([0, len(rows)], np.int32)
