@@ -10,29 +10,50 @@
 // The prefix is read once for all rows, not once per request: the rows of every
 // request and of the query heads that share a KV head form one matrix, cut into
 // 128-row tiles. The keys are cut into chunks so that few rows still fill the
-// device. A unit is (KV head, one or two row tiles, key chunk); a request's
-// suffix is units of the same kind with its own rows. Each unit writes a
-// normalised partial result and its log-sum-exp, and a second launch joins a
-// row's partials in chunk order (deterministic: no atomics).
+// device. A unit is (KV head, pair of row tiles, key chunk); a request's suffix
+// is units of the same kind with its own rows. Each unit writes normalised
+// partial results and their log-sum-exps, and a last launch joins a row's
+// partials in a fixed order (deterministic: no atomics).
 //
-// Per 128-key tile of a unit:
-//   - converter warps load the E4M3 codes (16 bytes per lane, one tile ahead in
-//     registers), turn them into fp16 — exact, with the row's power-of-two
-//     scale relative to the tile's largest folded into one multiplication — and
-//     store them to 128-byte-swizzled shared memory: K rows as the K-major B
+// A CTA has two pipelines that share the keys: each takes a row tile, or, where
+// there is only one, they take the even and the odd key tiles of it. Per
+// 128-key tile:
+//   - eight converter warps load the E4M3 codes (16 bytes per lane, one tile
+//     ahead in registers), turn them into fp16 — exact, with the row's
+//     power-of-two scale relative to the tile's largest in one multiplication —
+//     and store them to 128-byte-swizzled shared memory: K rows as the K-major B
 //     operand of S = Q K^T, V rows as the MN-major B operand of O = P V.
-//   - one thread per row tile issues both products (tcgen05, kind::f16, fp32
-//     accumulators in TMEM: 128 columns of S and up to 128 of O per row tile).
-//   - four softmax warps per row tile, one row per thread: the running maximum
-//     follows the row when it is exceeded by more than 2^5 (O is then rescaled
-//     in TMEM), P = exp2(S - m + 10) in fp16 overwrites S in TMEM and is the A
-//     operand of the second product.
+//   - one warp per pipeline issues both products (tcgen05, kind::f16, fp32
+//     accumulators in TMEM: two half tiles of 64 columns of S, 128 of O), the S
+//     product of one half tile while the softmax is at the other. The whole warp
+//     runs that code and one elected lane issues: with the loop inside a branch
+//     on one lane, an instruction took 70 to 100 clocks, and the issuer, not the
+//     tensor cores, set the pace (483 us for the question prefills below, 413).
+//   - eight softmax warps per pipeline, two threads to a row, 32 columns each:
+//     P = 2^(S c - m + 6) in fp16 lies over its S in TMEM and is the A operand of
+//     the second product. The reference m may lag the row's maximum by 2^9; past
+//     that (the two warps of a row vote) O is rescaled in TMEM, and then every
+//     row of the warp follows, those that could still wait too (408 -> 387 us).
 // fp16 throughout: q rows are scaled by a power of two so that their largest
-// element is near 2^13 (bf16's eight bits fit, elements below 2^-27 of the
+// element is in [2^13, 2^14) (bf16's eight bits fit; elements below 2^-27 of the
 // largest lose bits), codes have four bits, and P keeps eleven bits down to
-// 2^-24 of the row's maximum. V keeps its codes exactly while a row's scale is
-// within 2^-20 of the largest scale so far in its chunk, K while within 2^-22
-// of its tile's largest; smaller rows are rounded on that grid.
+// 2^-20 of the reference and ends at 2^-30. V keeps its codes exactly while a
+// row's scale is within 2^-20 of the largest scale so far in its chunk, K while
+// within 2^-22 of its tile's largest; smaller rows are rounded on that grid.
+//
+// What bounds it: per 256 x 128 logits the tensor cores need about 2,050 clocks
+// and the instructions (8,000 of the warps, half of them the exponentials and
+// what feeds them) 2,000 of each scheduler; a pass takes about 4,600, the rest
+// is the chain S product, softmax, O product of each pipeline, which TMEM (512
+// columns: S and O of two pipelines) leaves one half tile deep. Schedulers issue
+// in 66% of the cycles, the tensor pipe is busy in 45%. 16 question prefills of
+// up to 142 tokens over 36,831 keys (16 heads on 8 of 128): 362 us of 387 with
+// the join, 0.95 PFLOP/s, 49% of cuBLAS's bf16 rate; 256 rows over the same keys
+// (a step of 64 users): 47 us of 76.
+// Tried and slower: one row per thread with more registers (setmaxnreg; 515 us),
+// P in shared memory (472 to 534), one pipeline with two whole S tiles (535: each
+// key tile is then converted for 128 rows instead of 256), whole key tiles
+// instead of halves (409), rescaling 16 columns of O at a time (458: spills).
 //
 // Masked keys never reach a result: V rows past the last visible key of a tile
 // are zeros whatever the page holds, S of masked keys is replaced, not added
@@ -111,17 +132,9 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_maj
          (uint32_t(M >> 4) << 24);
 }
 
-// D[tmem] (+)= A[tmem] * B[smem].
-__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                           uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
+// Products and commits for a whole warp, of which one elected lane (the same
+// every time) issues: their operands stay in uniform registers.
+// D[tmem] (+)= A[smem] * B[smem]
 __device__ __forceinline__ void mma_ss_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
@@ -131,6 +144,7 @@ __device__ __forceinline__ void mma_ss_elect(uint32_t d_tmem, uint64_t adesc, ui
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// D[tmem] (+)= A[tmem] * B[smem]
 __device__ __forceinline__ void mma_ts_elect(uint32_t d_tmem, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
@@ -217,8 +231,7 @@ __device__ __forceinline__ uint32_t max_byte(uint32_t w) {
   return m;
 }
 
-// exp2(S * c + shift) of 32 columns, added up in acc and packed to fp16. nan:
-// columns whose V row is NaN (bit per column).
+// exp2(S * c + shift) of 32 columns, added up in acc and packed to fp16.
 __device__ __forceinline__ void att_exp32(const uint32_t (&r)[32], float2 c2, float2 s2, float2& acc,
                                           uint32_t (&h)[16]) {
 #pragma unroll
