@@ -609,6 +609,13 @@ def _new(stream, make, *args, device, **kw):
         return make(*args, device=device, **kw)
 
 
+def _like(t: torch.Tensor, stream) -> torch.Tensor:
+    """A dense tensor of t's shape and type."""
+    if stream is None and t.is_contiguous():
+        return torch.empty_like(t)   # the cheapest allocation there is
+    return _new(stream, torch.empty, t.shape, dtype=t.dtype, device=t.device)
+
+
 def _workspace(workspace: Optional[torch.Tensor], nbytes: int, device, stream) -> torch.Tensor:
     if workspace is None:
         return _new(stream, _new_workspace, nbytes, device=device)
@@ -665,9 +672,9 @@ def tsel_rope(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, tab
     qos = 0 if q_out is None else _rows(q_out, "q_out", dev, dtype, (total, H, d))
     kos = 0 if k_out is None else _rows(k_out, "k_out", dev, dtype, (total, Hkv, d))
     if q_out is None:
-        q_out = _new(stream, torch.empty, (total, H, d), dtype=dtype, device=dev)
+        q_out = _like(q, stream)
     if k is not None and k_out is None:
-        k_out = _new(stream, torch.empty, (total, Hkv, d), dtype=dtype, device=dev)
+        k_out = _like(k, stream)
     workspace = _workspace(workspace, 1024, dev, stream)
     _call(load_library().tsel_rope, dev, stream, q.data_ptr(), qs, _ptr(k), ks, pos_p, pos_dim,
           table_p, pairs, total, H, Hkv, d, _DTYPES[dtype], flags, q_out.data_ptr(), qos,
@@ -750,7 +757,7 @@ def tsel_cache_read(cache: TselCache, slots: torch.Tensor, *, dtype=torch.bfloat
     if k_out is None:
         k_out = _new(stream, torch.empty, shape, dtype=dtype, device=dev)
     if v_out is None:
-        v_out = _new(stream, torch.empty, shape, dtype=dtype, device=dev)
+        v_out = _like(k_out, stream)
     workspace = _workspace(workspace, 1024, dev, stream)
     _call(load_library().tsel_cache_read, dev, stream, *cache_p, slots.data_ptr(), shape[0], Hkv, d,
           _DTYPES[dtype], k_out.data_ptr(), kos, v_out.data_ptr(), vos, workspace.data_ptr(),
@@ -825,13 +832,11 @@ def tsel_prefix_attention(q: torch.Tensor, cu_seqlens_q: torch.Tensor, max_seqle
     os_ = 0 if out is None else _rows(out, "out", dev, q.dtype, (tq, H, d))
     if lse is not None:
         _vector(lse, torch.float32, "lse", dev, H * tq)
-    if workspace is None:
-        nbytes = tsel_prefix_attention_workspace_size(R, tq, max_seqlen_q, H, Hkv, d, max_p, max_s)
-    else:
-        nbytes = 0
+    nbytes = 0 if workspace is not None else tsel_prefix_attention_workspace_size(
+        R, tq, max_seqlen_q, H, Hkv, d, max_p, max_s)
     workspace = _workspace(workspace, nbytes, dev, stream)
     if out is None:
-        out = _new(stream, torch.empty, (tq, H, d), dtype=q.dtype, device=dev)
+        out = _like(q, stream)
     if lse is None and want_lse:
         lse = _new(stream, torch.empty, (H, tq), dtype=torch.float32, device=dev)
     _call(load_library().tsel_prefix_attention, dev, stream, q.data_ptr(), qs,

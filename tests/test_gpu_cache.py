@@ -295,6 +295,23 @@ def test_cache_offsets_past_32_bits(tsel):
     assert torch.equal(out[0], v1[0])                       # one key: its V
 
 
+def test_attention_offsets_past_32_bits_with_many_rows(tsel):
+    pages, ps, hkv, d = 36800, 128, 8, 128
+    cache = tsel.TselCache(*[torch.empty(pages, hkv, ps, d, dtype=torch.uint8, device="cuda") for _ in range(2)],
+                           *[torch.empty(pages, hkv, ps, dtype=torch.uint8, device="cuda") for _ in range(2)])
+    slots = np.arange((pages - 1) * ps, (pages - 1) * ps + 100).astype(np.int32)
+    k, v = torch.randn(2, 100, hkv, d, device="cuda").unbind(0)
+    tsel.tsel_cache_write(k, v, i32(slots), cache)
+    q = torch.randn(40, hkv, d, device="cuda").to(BF)
+    out, lse = tsel.tsel_prefix_attention(q, i32([0, 40]), 40, cache, i32([pages - 1]), i32([100]), 128, None, None, 0)
+    kr, vr = tsel.tsel_cache_read(cache, i32(slots), dtype=FP)
+    ref, lref, av, mag = O.prefix_attention(_np(q), [0, 40], _np(kr), _np(vr), np.arange(100), [np.zeros(0, np.int64)], d ** -0.5)
+    delta = d * 2.0 ** -23 * mag + 2.0 ** -22
+    tol = av * (2 * delta[..., None] + 2.0 ** -11 + 2.0 ** -19) + 100 * 2.0 ** -31 * float(vr.abs().max())
+    assert np.all(np.abs(_np(out) - ref) <= tol + (np.abs(ref) + tol) * 2.0 ** -8)
+    assert np.all(np.abs(_np(lse) - lref) <= delta.T + 2.0 ** -20 + np.abs(lref) * 2.0 ** -22)
+
+
 # ------------------------------------------------------------------ attention
 
 class Batch:
