@@ -528,43 +528,39 @@ def tsel_gather_compact_counted(hidden: torch.Tensor, pos: Optional[torch.Tensor
 # ---------------------------------------------------------------------------
 
 # The calls below are made once per layer and decoding step, where the host's
-# share counts: the checks are plain comparisons, and the device is switched and
-# the stream looked up in the cheapest way there is.
+# share counts. Every question to a tensor costs a tenth of a microsecond or two,
+# so the checks ask few of them and compare devices by index, and the device is
+# switched and the stream looked up in the cheapest way there is.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_U8, _I32, _I64, _F32 = torch.uint8, torch.int32, torch.int64, torch.float32
 
 
-def _call(fn, device: torch.device, stream, *args) -> None:
-    """fn(*args, stream) on `device` (the library works on the current device)."""
-    index = device.index
+def _call(fn, index: int, stream, *args) -> None:
+    """fn(*args, stream) on device `index` (the library works on the current device)."""
     if stream is None and _raw_stream is not None:
         handle = _raw_stream(index)
     else:
-        handle = _stream(stream, device)
+        handle = _stream(stream, index)
     if torch.cuda.current_device() == index:
         st = fn(*args, handle)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(index):
             st = fn(*args, handle)
     if st != TSEL_OK:
         _check(st)
 
 
-def _rows(t: torch.Tensor, name: str, device=None, dtype=None, shape=None) -> int:
+def _rows(t: torch.Tensor, name: str, index: int, dtype, shape=None) -> int:
     """Checks a [rows, heads, head_dim] tensor; returns its row stride (0: dense)."""
-    have = t.shape
-    if not t.is_cuda or t.dtype not in _DTYPES:
-        raise TypeError(f"{name} must be a CUDA bf16, fp16 or fp32 tensor")
-    if len(have) != 3:
-        raise ValueError(f"{name} must be a [rows, heads, head_dim] tensor")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if shape is not None and have != shape:
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device}")
     if t.is_contiguous():
         return 0
-    n, h, d = have
+    n, h, d = t.shape
     if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
         raise ValueError(f"{name} must have contiguous [heads, head_dim] rows")
     if n <= 1:
@@ -574,28 +570,40 @@ def _rows(t: torch.Tensor, name: str, device=None, dtype=None, shape=None) -> in
     return t.stride(0)
 
 
-def _vector(t: torch.Tensor, dtype, name: str, device, numel: Optional[int] = None) -> None:
-    if t.dtype != dtype or not t.is_cuda:
+def _first(t: torch.Tensor, name: str):
+    """(shape, dtype, device index) of the tensor that the others have to match."""
+    shape, dtype, index = t.shape, t.dtype, t.get_device()
+    if index < 0 or dtype not in _DTYPES:
+        raise TypeError(f"{name} must be a CUDA bf16, fp16 or fp32 tensor")
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be a [rows, heads, head_dim] tensor")
+    return shape, dtype, index
+
+
+def _vector(t: torch.Tensor, dtype, name: str, index: int, numel: Optional[int] = None) -> int:
+    """Checks a dense tensor; returns its pointer."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be a CUDA {dtype} tensor")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if numel is not None and t.numel() != numel:
         raise ValueError(f"{name} must have {numel} entries")
+    return t.data_ptr()
 
 
-def _rope_args(pos, table, total: int, device):
+def _rope_args(pos, table, total: int, index: int):
     """(pos pointer, pos_dim, table pointer, pairs) of a rotation."""
     if table is None:
         return None, 0, None, 0
     if pos is None:
         raise ValueError("a rope table needs positions")
-    _vector(pos, torch.int32, "pos", device)
-    if pos.dim() != 2 or pos.shape[0] != total:
+    pos_p = _vector(pos, _I32, "pos", index)
+    shape = pos.shape
+    if len(shape) != 2 or shape[0] != total:
         raise ValueError("pos must be an int32 [tokens, axes] tensor")
-    _vector(table, torch.int64, "table", device)
-    return pos.data_ptr(), pos.shape[1], table.data_ptr(), table.numel()
+    return pos_p, shape[1], _vector(table, _I64, "table", index), table.numel()
 
 
 def _new(stream, make, *args, device, **kw):
@@ -616,11 +624,11 @@ def _like(t: torch.Tensor, stream) -> torch.Tensor:
     return _new(stream, torch.empty, t.shape, dtype=t.dtype, device=t.device)
 
 
-def _workspace(workspace: Optional[torch.Tensor], nbytes: int, device, stream) -> torch.Tensor:
+def _workspace(workspace: Optional[torch.Tensor], nbytes: int, index: int, stream) -> torch.Tensor:
     if workspace is None:
-        return _new(stream, _new_workspace, nbytes, device=device)
-    if workspace.device != device:
-        raise ValueError(f"workspace must be on {device}")
+        return _new(stream, _new_workspace, nbytes, device=torch.device("cuda", index))
+    if workspace.get_device() != index:
+        raise ValueError(f"workspace must be on cuda:{index}")
     return workspace
 
 
@@ -657,26 +665,28 @@ def tsel_rope(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, tab
     """Rotates q [T, H, d] and k [T, Hkv, d] (or None) by positions pos int32 [T, axes];
     returns (q_out, k_out), which may be q and k themselves. With
     TSEL_ROPE_INVERSE it turns gradients of the outputs into those of the inputs."""
-    dev, dtype = q.device, q.dtype
-    qs = _rows(q, "q")
-    total, H, d = q.shape
-    Hkv = ks = 0
+    shape, dtype, index = _first(q, "q")
+    qs = _rows(q, "q", index, dtype)
+    total, H, d = shape
+    Hkv = ks = kos = 0
     if k is not None:
-        ks = _rows(k, "k", dev, dtype)
-        Hkv = k.shape[1]
-        if k.shape != (total, Hkv, d):
+        ks = _rows(k, "k", index, dtype)
+        k_shape = k.shape
+        if len(k_shape) != 3 or k_shape[0] != total or k_shape[2] != d:
             raise ValueError("q and k must have the same rows and head_dim")
+        Hkv = k_shape[1]
     elif k_out is not None:
         raise ValueError("k_out without k")
-    pos_p, pos_dim, table_p, pairs = _rope_args(pos, table, total, dev)
-    qos = 0 if q_out is None else _rows(q_out, "q_out", dev, dtype, (total, H, d))
-    kos = 0 if k_out is None else _rows(k_out, "k_out", dev, dtype, (total, Hkv, d))
+    pos_p, pos_dim, table_p, pairs = _rope_args(pos, table, total, index)
+    qos = 0 if q_out is None else _rows(q_out, "q_out", index, dtype, shape)
+    if k_out is not None:
+        kos = _rows(k_out, "k_out", index, dtype, k_shape)
+    workspace = _workspace(workspace, 1024, index, stream)
     if q_out is None:
         q_out = _like(q, stream)
     if k is not None and k_out is None:
         k_out = _like(k, stream)
-    workspace = _workspace(workspace, 1024, dev, stream)
-    _call(load_library().tsel_rope, dev, stream, q.data_ptr(), qs, _ptr(k), ks, pos_p, pos_dim,
+    _call(load_library().tsel_rope, index, stream, q.data_ptr(), qs, _ptr(k), ks, pos_p, pos_dim,
           table_p, pairs, total, H, Hkv, d, _DTYPES[dtype], flags, q_out.data_ptr(), qos,
           _ptr(k_out), kos, workspace.data_ptr(), workspace.numel())
     return q_out, k_out
@@ -703,18 +713,17 @@ def tsel_cache_new(num_pages: int, page_size: int, num_kv_heads: int, head_dim: 
     return TselCache(*codes, *[torch.zeros(shape, dtype=torch.uint8, device=device) for _ in range(2)])
 
 
-def _cache_args(cache: TselCache, device):
+def _cache_args(cache: TselCache, index: int):
     """(pointers and sizes of the C calls, Hkv, d) of a cache."""
     kp, vp, ke, ve = cache
-    for t, name in ((kp, "k_pages"), (vp, "v_pages"), (ke, "k_exps"), (ve, "v_exps")):
-        _vector(t, torch.uint8, name, device)
     shape = kp.shape
     if len(shape) != 4:
         raise ValueError("k_pages must be a uint8 [pages, heads, page_size, head_dim] tensor")
     pages, heads, page_size, d = shape
-    if vp.shape != shape or ke.shape != (pages, heads, page_size) or ve.shape != ke.shape:
+    if vp.shape != shape or ke.shape != shape[:3] or ve.shape != shape[:3]:
         raise ValueError("the cache's tensors do not match one another")
-    return (kp.data_ptr(), vp.data_ptr(), ke.data_ptr(), ve.data_ptr(), pages, page_size), heads, d
+    return (_vector(kp, _U8, "k_pages", index), _vector(vp, _U8, "v_pages", index),
+            _vector(ke, _U8, "k_exps", index), _vector(ve, _U8, "v_exps", index), pages, page_size), heads, d
 
 
 def tsel_cache_workspace_size() -> int:
@@ -726,18 +735,18 @@ def tsel_cache_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cach
                      flags: int = 0, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """Quantises k and v [T, Hkv, d] into the cache's slots (int32 [T], negative:
     skipped); with a rope table and positions k is rotated on its way."""
-    dev, dtype = k.device, k.dtype
-    ks = _rows(k, "k")
-    total, Hkv, d = k.shape
-    vs = _rows(v, "v", dev, dtype, (total, Hkv, d))
-    cache_p, ch, cd = _cache_args(cache, dev)
+    shape, dtype, index = _first(k, "k")
+    ks = _rows(k, "k", index, dtype)
+    vs = _rows(v, "v", index, dtype, shape)
+    total, Hkv, d = shape
+    cache_p, ch, cd = _cache_args(cache, index)
     if ch != Hkv or cd != d:
         raise ValueError("k and v do not match the cache's heads and head_dim")
-    _vector(slots, torch.int32, "slots", dev, total)
-    pos_p, pos_dim, table_p, pairs = _rope_args(pos, table, total, dev)
-    workspace = _workspace(workspace, 1024, dev, stream)
-    _call(load_library().tsel_cache_write, dev, stream, k.data_ptr(), ks, v.data_ptr(), vs, pos_p,
-          pos_dim, table_p, pairs, slots.data_ptr(), total, Hkv, d, _DTYPES[dtype], flags, *cache_p,
+    slots_p = _vector(slots, _I32, "slots", index, total)
+    pos_p, pos_dim, table_p, pairs = _rope_args(pos, table, total, index)
+    workspace = _workspace(workspace, 1024, index, stream)
+    _call(load_library().tsel_cache_write, index, stream, k.data_ptr(), ks, v.data_ptr(), vs, pos_p,
+          pos_dim, table_p, pairs, slots_p, total, Hkv, d, _DTYPES[dtype], flags, *cache_p,
           workspace.data_ptr(), workspace.numel())
 
 
@@ -746,20 +755,22 @@ def tsel_cache_read(cache: TselCache, slots: torch.Tensor, *, dtype=torch.bfloat
                     workspace: Optional[torch.Tensor] = None,
                     stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Reads slots (int32 [T], negative: zeros) back as k and v [T, Hkv, d] of dtype."""
-    dev = cache.k_pages.device
-    cache_p, Hkv, d = _cache_args(cache, dev)
-    _vector(slots, torch.int32, "slots", dev)
+    index = cache.k_pages.get_device()
+    if index < 0:
+        raise TypeError("the cache must be on a CUDA device")
+    cache_p, Hkv, d = _cache_args(cache, index)
+    slots_p = _vector(slots, _I32, "slots", index)
     if dtype not in _DTYPES:
         raise TypeError("dtype must be bf16, fp16 or fp32")
     shape = (slots.numel(), Hkv, d)
-    kos = 0 if k_out is None else _rows(k_out, "k_out", dev, dtype, shape)
-    vos = 0 if v_out is None else _rows(v_out, "v_out", dev, dtype, shape)
+    kos = 0 if k_out is None else _rows(k_out, "k_out", index, dtype, shape)
+    vos = 0 if v_out is None else _rows(v_out, "v_out", index, dtype, shape)
+    workspace = _workspace(workspace, 1024, index, stream)
     if k_out is None:
-        k_out = _new(stream, torch.empty, shape, dtype=dtype, device=dev)
+        k_out = _new(stream, torch.empty, shape, dtype=dtype, device=slots.device)
     if v_out is None:
         v_out = _like(k_out, stream)
-    workspace = _workspace(workspace, 1024, dev, stream)
-    _call(load_library().tsel_cache_read, dev, stream, *cache_p, slots.data_ptr(), shape[0], Hkv, d,
+    _call(load_library().tsel_cache_read, index, stream, *cache_p, slots_p, shape[0], Hkv, d,
           _DTYPES[dtype], k_out.data_ptr(), kos, v_out.data_ptr(), vos, workspace.data_ptr(),
           workspace.numel())
     return k_out, v_out
@@ -793,58 +804,60 @@ def tsel_prefix_attention(q: torch.Tensor, cu_seqlens_q: torch.Tensor, max_seqle
     [R, pages] and suffix_lens int32 [R] (None with max_suffix_len 0). A
     request's last query rows are its last suffix tokens (causal). Rows past
     cu_seqlens_q[R] are left as they are in a given out or lse."""
-    dev = q.device
-    qs = _rows(q, "q")
-    if q.dtype == torch.float32:
+    shape, dtype, index = _first(q, "q")
+    if dtype is _F32:
         raise TypeError("q must be bf16 or fp16")
-    tq, H, d = q.shape
-    cache_p, Hkv, cd = _cache_args(cache, dev)
+    qs = _rows(q, "q", index, dtype)
+    tq, H, d = shape
+    cache_p, Hkv, cd = _cache_args(cache, index)
     page_size = cache_p[5]
     if cd != d:
         raise ValueError("q does not match the cache's head_dim")
-    _vector(cu_seqlens_q, torch.int32, "cu_seqlens_q", dev)
+    cu_p = _vector(cu_seqlens_q, _I32, "cu_seqlens_q", index)
     R = cu_seqlens_q.numel() - 1
     if R < 0:
         raise ValueError("cu_seqlens_q must have at least one entry")
     max_p, max_s = int(max_prefix_len), int(max_suffix_len)
+    prefix_p = len_p = table_p = suffix_p = None
     if max_p > 0:
         if prefix_pages is None or prefix_len is None:
             raise ValueError("max_prefix_len > 0 needs prefix_pages and prefix_len")
-        _vector(prefix_pages, torch.int32, "prefix_pages", dev)
-        _vector(prefix_len, torch.int32, "prefix_len", dev, 1)
+        prefix_p = _vector(prefix_pages, _I32, "prefix_pages", index)
+        len_p = _vector(prefix_len, _I32, "prefix_len", index, 1)
         if prefix_pages.numel() * page_size < max_p:
             raise ValueError("prefix_pages holds fewer than max_prefix_len keys")
     table_stride = 0
     if max_s > 0 and R > 0:
         if page_table is None or suffix_lens is None:
             raise ValueError("max_suffix_len > 0 needs page_table and suffix_lens")
-        _need(page_table, torch.int32, "page_table")
-        if page_table.device != dev:
-            raise ValueError(f"page_table must be on {dev}")
-        if page_table.dim() != 2 or page_table.shape[0] != R or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        if page_table.dtype is not _I32:
+            raise TypeError("page_table must be a CUDA torch.int32 tensor")
+        if page_table.get_device() != index:
+            raise ValueError(f"page_table must be on cuda:{index}")
+        t_shape = page_table.shape
+        if len(t_shape) != 2 or t_shape[0] != R or (t_shape[1] > 1 and page_table.stride(1) != 1):
             raise ValueError("page_table must be an int32 [requests, pages] tensor with contiguous rows")
-        if R > 1 and page_table.stride(0) < page_table.shape[1]:
+        table_stride = page_table.stride(0) if R > 1 else t_shape[1]
+        if table_stride < t_shape[1]:
             raise ValueError("page_table rows must not overlap")
-        if page_table.shape[1] * page_size < max_s:
+        if t_shape[1] * page_size < max_s:
             raise ValueError("page_table rows hold fewer than max_suffix_len keys")
-        table_stride = page_table.stride(0) if R > 1 else page_table.shape[1]
-        _vector(suffix_lens, torch.int32, "suffix_lens", dev, R)
-    os_ = 0 if out is None else _rows(out, "out", dev, q.dtype, (tq, H, d))
+        table_p = page_table.data_ptr()
+        suffix_p = _vector(suffix_lens, _I32, "suffix_lens", index, R)
+    os_ = 0 if out is None else _rows(out, "out", index, dtype, shape)
     if lse is not None:
-        _vector(lse, torch.float32, "lse", dev, H * tq)
+        _vector(lse, _F32, "lse", index, H * tq)
     nbytes = 0 if workspace is not None else tsel_prefix_attention_workspace_size(
         R, tq, max_seqlen_q, H, Hkv, d, max_p, max_s)
-    workspace = _workspace(workspace, nbytes, dev, stream)
+    workspace = _workspace(workspace, nbytes, index, stream)
     if out is None:
         out = _like(q, stream)
     if lse is None and want_lse:
-        lse = _new(stream, torch.empty, (H, tq), dtype=torch.float32, device=dev)
-    _call(load_library().tsel_prefix_attention, dev, stream, q.data_ptr(), qs,
-          cu_seqlens_q.data_ptr(), R, tq, max_seqlen_q, *cache_p,
-          _ptr(prefix_pages) if max_p > 0 else None, _ptr(prefix_len) if max_p > 0 else None, max_p,
-          _ptr(page_table) if table_stride else None, table_stride,
-          _ptr(suffix_lens) if table_stride else None, max_s, H, Hkv, d, _DTYPES[q.dtype],
-          softmax_scale, out.data_ptr(), os_, _ptr(lse), workspace.data_ptr(), workspace.numel())
+        lse = _new(stream, torch.empty, (H, tq), dtype=_F32, device=q.device)
+    _call(load_library().tsel_prefix_attention, index, stream, q.data_ptr(), qs, cu_p, R, tq,
+          max_seqlen_q, *cache_p, prefix_p, len_p, max_p, table_p, table_stride, suffix_p, max_s, H, Hkv, d,
+          _DTYPES[dtype], softmax_scale, out.data_ptr(), os_, _ptr(lse), workspace.data_ptr(),
+          workspace.numel())
     return out, lse
 
 

@@ -241,6 +241,9 @@ class _Fake:
     def stride(self, i):
         return self._strides[i]
 
+    def get_device(self):
+        return self.device.index
+
     def numel(self):
         return int(np.prod(self.shape))
 
