@@ -30,6 +30,8 @@ constexpr int kAttNarrowRows = 32;
 constexpr int kAttNarrowRowsLong = 16;         // past
 constexpr int kAttNarrowKeys = 16384;          // this many keys of few requests
 
+constexpr int kAttJoinedTiles = 1024;          // 128-key tiles of suffixes that a prefix's narrow launch takes along
+
 // How the prefix, or the suffixes, are cut into units: (key chunk, KV head, row
 // group), for the suffixes of each request.
 struct AttPart {
@@ -79,11 +81,12 @@ inline int att_chunks(int64_t base, int tiles, int ctas, bool narrow, int least)
   return best;
 }
 
-inline AttPart att_part(int64_t requests, int tokens, int max_keys, int Hkv, int G, int tt, int* slots) {
+// `two`: units of 16 rows even where 8 would do.
+inline AttPart att_part(int64_t requests, int tokens, int max_keys, int Hkv, int G, int tt, bool two, int* slots) {
   AttPart a{};
   const int64_t rows = int64_t(tokens) * G;
   const bool few = max_keys > kAttNarrowKeys && requests * Hkv < kAttWideCtas;
-  a.narrow = rows > (few ? kAttNarrowRowsLong : kAttNarrowRows) ? 0 : (rows > 8 ? 2 : 1);
+  a.narrow = rows > (few ? kAttNarrowRowsLong : kAttNarrowRows) ? 0 : (rows > 8 || two ? 2 : 1);
   a.groups = int(a.narrow ? ceil_div(rows, 8 * a.narrow) : ceil_div(tokens, 2 * tt));
   a.slot0 = *slots;
   const int tiles = int(ceil_div(max_keys, kTile));
@@ -102,8 +105,14 @@ inline AttPlan att_plan(int R, int Tq, int max_q, int H, int Hkv, int d, int max
   AttPlan a{};
   a.G = H / Hkv;
   a.tt = kTile / a.G;
-  a.pre = att_part(1, Tq, max_prefix, Hkv, a.G, a.tt, &a.slots);
-  a.suf = att_part(Tq > 0 ? R : 0, max_q, max_suffix, Hkv, a.G, a.tt, &a.slots);
+  a.pre = att_part(1, Tq, max_prefix, Hkv, a.G, a.tt, false, &a.slots);
+  // Beside a prefix in units of 16 rows, short suffixes join its launch: 8 users
+  // of 1,228 shared keys and up to 142, 1,000, 4,000 of their own on 8 KV heads
+  // of 128 take 10.9, 14.1, 23.2 us in one launch and 11.9, 15.9, 21.9 in two
+  // (called, not replayed: 24.5, 25.0, 24.4 and 25.9, 26.5, 26.5).
+  const bool two = a.pre.narrow == 2 && a.pre.units > 0 &&
+                   int64_t(R) * Hkv * ceil_div(max_suffix, kTile) <= kAttJoinedTiles;
+  a.suf = att_part(Tq > 0 ? R : 0, max_q, max_suffix, Hkv, a.G, a.tt, two, &a.slots);
   a.too_large = a.pre.units + a.suf.units > 0x7FFFFFFFll || double(a.slots) * Tq * H * d > 1e15;
   if (a.too_large) return a;
   a.lse_off = kWsHeaderBytes;
