@@ -617,7 +617,7 @@ WIDE = [
     ([1] * 40, [7] * 40, 1000, 4, 4, 128, 16, BF),       # prefix wide, suffixes of one row each
     ([5] * 9, [33 * i for i in range(9)], 300, 6, 2, 112, 16, HF),   # suffixes of 15 rows
     ([2, 1, 2], [90, 1, 30], 260, 10, 2, 96, 32, BF),    # prefix 25 rows, suffixes 10: two to a unit, both
-    ([1, 1, 1], [90, 1, 30], 260, 10, 2, 80, 32, HF),    # prefix 15 rows, suffixes 5: two launches of the few-row kernel
+    ([1, 1, 1], [90, 1, 30], 260, 10, 2, 80, 32, HF),    # prefix 15 rows, suffixes 5 in its launch
 ]
 
 
@@ -641,6 +641,13 @@ def test_attention_around_the_row_limits(tsel, rows, d, dtype):
 def test_attention_few_rows_over_a_long_prefix(tsel, rows):
     b = Batch(tsel, 230 + rows, [rows], [20], 17000, 1, 1, 64, 64, BF)
     out, lse = b.run()
+    b.check(out, lse)
+
+
+def test_attention_two_launches_of_the_few_row_kernel(tsel):
+    """Prefix units of 16 rows, and suffixes with room for too many keys to join their launch."""
+    b = Batch(tsel, 44, [1, 1, 1], [90, 1, 300], 260, 10, 2, 80, 32, HF)
+    out, lse = b.run(max_s=25600)
     b.check(out, lse)
 
 
