@@ -23,7 +23,9 @@
 //
 // 36,831 tokens on 8 KV heads of 128, bf16 (227 MB): write 42 us, 5.4 TB/s or 79%
 // of the copy rate, read 40 us, 84%; 131,072 tokens rotated, written and read
-// back (1.6 GB): 306 us, 78%; 200 tokens written 2.7 us, 142 read 2.4 us.
+// back (1.6 GB): 303 us, 79% (the rotated write 172: its schedulers issue in 71% of
+// the cycles, for angles, addresses and conversions); 200 tokens written 2.7 us,
+// 142 read 2.4 us.
 #include "launch_util.cuh"
 #include "rope.cuh"
 
@@ -42,14 +44,10 @@ __device__ __forceinline__ uint32_t e4m3x2(float x, float y) {
   return r;
 }
 
-// Largest magnitude of the three, its sign without meaning; NaN when one of them is.
+// Largest magnitude of the three; NaN when one of them is.
 __device__ __forceinline__ float max3_abs(float m, float x, float y) {
   float r;
-  asm("{\n\t.reg .f32 a;\n\t"
-      "max.NaN.xorsign.abs.f32 a, %2, %3;\n\t"
-      "max.NaN.xorsign.abs.f32 %0, %1, a;\n\t}"
-      : "=f"(r)
-      : "f"(m), "f"(x), "f"(y));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(x), "f"(y));
   return r;
 }
 
@@ -60,7 +58,9 @@ __device__ __forceinline__ void encode(const float (&f)[V], float up, bool finit
     uint32_t* w = reinterpret_cast<uint32_t*>(&c.p[0]);
 #pragma unroll
     for (int j = 0; j < V; j += 4) {
-      const uint32_t x = e4m3x2(f[j] * up, f[j + 1] * up) | (e4m3x2(f[j + 2] * up, f[j + 3] * up) << 16);
+      const float2 up2 = make_float2(up, up);
+      const float2 lo = __fmul2_rn(make_float2(f[j], f[j + 1]), up2), hi = __fmul2_rn(make_float2(f[j + 2], f[j + 3]), up2);
+      const uint32_t x = e4m3x2(lo.x, lo.y) | (e4m3x2(hi.x, hi.y) << 16);
       w[j / 4] = finite ? x : 0u;
     }
   } else {
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kCacheThreads, sizeof(T) * V > 16 ? 3 : 4) cac
 #pragma unroll
         for (int j = 0; j < V; ++j) most = max3_abs(most, fa[n][j], fb[n][j]);
       }
-      uint32_t top = __float_as_uint(most) & 0x7FFFFFFFu;
+      uint32_t top = __float_as_uint(most);
       for (int o = lpr >> 1; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
       // e + 127: exponent field - 8 when 1.m <= 1.75 (448 = 1.75 * 2^8), - 7 above
       const bool finite = top < 0x7F800000u;
