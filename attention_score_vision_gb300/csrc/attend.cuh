@@ -66,9 +66,9 @@ inline int att_chunks(int64_t base, int tiles, int ctas, bool narrow, int least)
   if (tiles <= 1 || base < 1) return tiles < 1 ? 0 : 1;
   int best = least;
   double best_cost = 1e300;
-  for (int n = least; n <= tiles && n <= 256 + least; ++n) {
-    const int per = int(ceil_div(tiles, n));
-    if (n > least && int(ceil_div(tiles, per)) < n) continue;   // the same tiles in fewer chunks
+  int per = 0;
+  for (int n = least; n <= tiles && n <= 256 + least; n = per > 1 ? int(ceil_div(tiles, per - 1)) : tiles + 1) {
+    per = int(ceil_div(tiles, n));   // the next count is the least that makes it smaller
     const double fill = double(base * n) / ctas;
     const double waves = !narrow ? double(ceil_div(base * n, ctas))
                                  : (fill <= 1.0 ? 1.0 : (fill < 1.5 ? 1.5 : fill)) + 0.5;
