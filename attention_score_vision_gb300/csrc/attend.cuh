@@ -169,9 +169,9 @@ struct AttUnit {
 
 // `per`: rows of a row group; the keys of a suffix unit end where its last row sees no further.
 // U, the type that the unit number is divided in, only changes what the compiler
-// makes of the rest: uint32_t in the wide kernel (16 question prefills: 432 us,
-// 451 with int64_t), int64_t in the narrow one (four users of a six-view
-// request: 8.6 us, 10.2 with uint32_t).
+// makes of the rest: uint32_t in the wide kernel (16 question prefills: 387 us,
+// 436 with int64_t), int64_t in the narrow one (four users of a six-view
+// request: 8.6 us, 10.4 with uint32_t).
 template <typename U>
 __device__ __forceinline__ AttUnit att_unit(const AttParams& p, U u, int per) {
   AttUnit w{};
