@@ -144,7 +144,6 @@ struct AttParams {
   int G, tt, slots;
   AttPart pre, suf;
   uint32_t pre_units;          // prefix units of this launch (its first ones); the rest are suffix units
-  int late_wait;               // the launch before this one is of the same call: wait for it at the end
   float* part_lse;             // [slots][Tq][H], base 2
   float* part_o;               // [slots][Tq][H][d]
   void* out;

@@ -112,22 +112,15 @@ __global__ void __launch_bounds__(kNarThreads, NarCfg<D, NB>::CTAS) attend_narro
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;   // fragment group and place in it
-  if (!p.late_wait) pdl_wait();
+  pdl_wait();   // also where the launch before is of the same call: only this wait makes earlier kernels' writes visible here
   pdl_launch_dependents();
-  // With late_wait the launch before this one is the wide kernel of the same
-  // call. It let this one start after its own wait, so the inputs are final;
-  // its completion is waited for at the end, for the launch that joins both.
   const AttUnit w = att_unit<int64_t>(p, blockIdx.x, C::ROWS);
   const int row0 = w.group * C::ROWS;
   const int rows = w.bad ? 0 : min((w.tok_last - w.tok_first) * p.G - row0, C::ROWS);
   if (w.bad && threadIdx.x == 0) set_status(p.status, TSEL_DEV_SEQLENS);
-  if (rows <= 0) {
-    if (p.late_wait) pdl_wait();
-    return;
-  }
+  if (rows <= 0) return;
   const int keys = w.k1 - w.k0;
   if (keys <= 0) {   // no visible key in this chunk: an empty partial
-    if (p.late_wait) pdl_wait();
     if (int(threadIdx.x) < rows) {
       const int r = row0 + int(threadIdx.x);
       p.part_lse[(int64_t(w.slot) * p.Tq + w.tok_first + r / p.G) * p.H + w.kvh * p.G + r % p.G] = kNegInf;
@@ -451,7 +444,6 @@ __global__ void __launch_bounds__(kNarThreads, NarCfg<D, NB>::CTAS) attend_narro
     }
   }
   __syncthreads();
-  if (p.late_wait) pdl_wait();
   for (int x = threadIdx.x; x < rows * (D / 4); x += kNarThreads) {
     const int rr = x / (D / 4), col = 4 * (x - rr * (D / 4));
     float top = kNegInf, sum = 0.f;

@@ -398,19 +398,17 @@ tsel_status tsel_prefix_attention(
   p.lse = lse;
   p.status = &reinterpret_cast<WsHeader*>(ws)->status;
   p.timeout_ns = device_wait_timeout_ns();
-  // The wide launch first, then the few-row ones, which do not depend on it:
-  // they start with it and wait for it at their end.
+  // The wide launch first, then the few-row ones. Neither reads what the other
+  // writes, but a kernel sees earlier kernels' writes (Q, cached rows, lengths)
+  // only after its own wait, which is also for the launch before it.
   cudaError_t e;
-  bool launched = false;
   for (int kind = 0; kind <= 2; ++kind) {
     const int64_t pre = a.pre.narrow == kind ? a.pre.units : 0, suf = a.suf.narrow == kind ? a.suf.units : 0;
     if (pre + suf == 0) continue;
     p.pre_units = uint32_t(pre);
-    p.late_wait = launched;
     e = kind == 0 ? launch_attend(head_dim, p, pre + suf, stream)
                   : launch_attend_narrow(head_dim, kind, p, pre + suf, stream);
     if (e != cudaSuccess) return cuda_fail(e, "attention launch");
-    launched = true;
   }
   e = launch_attend_join(head_dim, p, stream);
   return e == cudaSuccess ? TSEL_OK : cuda_fail(e, "join launch");

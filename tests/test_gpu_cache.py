@@ -856,3 +856,46 @@ def test_the_path_from_scoring_to_answers(tsel):
     s2, _ = tsel.tsel_importance(qq[6:], kb16, i32([0, 9]), i32([0, B]), 9, B)
     _, s2_ref = oracle.importance(bits(qq[6:].contiguous()), bits(kb16), [0, 9], [0, B])
     assert np.max(np.abs(s2.cpu().numpy() - s2_ref) / s2_ref) <= 2e-3
+
+
+def test_attention_reads_what_the_calls_before_it_wrote(tsel):
+    """Decoding steps one right behind another: Q rotated in place, each
+    request's last cached token overwritten, then attention whose prefix takes
+    the wide kernel and whose suffixes the few-row one, all in the same memory.
+    Without a pause, and from one graph, every step is what it is when each call
+    is waited for."""
+    R, steps = 48, 12
+    b = Batch(tsel, 50, [1] * R, [20 + 3 * i for i in range(R)], 700, 8, 4, 128, 16, BF)
+    a = b.args()
+    ws = torch.zeros(1 << 24, dtype=torch.uint8, device="cuda")
+    rng = np.random.default_rng(51)
+    k, v = (torch.from_numpy(rng.standard_normal((steps, R, 4, 128))).to(BF).cuda() for _ in range(2))
+    slots = i32([r[-1] for r in b.suffix_rows])
+    pos = i32(rng.integers(0, 999, (R, 2)))
+    table, _, _ = _table(tsel, [32, 32], "sectioned")
+    q0 = b.q.clone()
+    out, lse = (torch.empty((steps,) + s, dtype=t, device="cuda") for s, t in (((R, 8, 128), BF), ((8, R), FP)))
+
+    def run(pause):
+        b.q.copy_(q0)
+        for i in range(steps):
+            for call in (lambda: tsel.tsel_rope(b.q, None, pos, table, q_out=b.q, workspace=ws),
+                         lambda: tsel.tsel_cache_write(k[i], v[i], slots, b.cache, workspace=ws),
+                         lambda: tsel.tsel_prefix_attention(b.q, *a, out=out[i], lse=lse[i], workspace=ws)):
+                call()
+                if pause:
+                    torch.cuda.synchronize()
+
+    run(True)
+    want = out.clone(), lse.clone()
+    assert all(not torch.equal(out[i], out[i + 1]) for i in range(steps - 1))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run(False)
+    for again in (lambda: run(False), g.replay, lambda: run(False), g.replay):
+        out.zero_()
+        lse.zero_()
+        again()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert tsel.tsel_read_device_status(ws) == 0
