@@ -812,8 +812,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const AttP
                      : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          if (wv[x] == 0.f) continue;   // too far below the row's largest
+        for (int x = 0; x < 4; ++x) {   // a weight of 0 (too far below the row's largest) drops numbers, but no NaN
           sum += wv[x];
           acc.x += wv[x] * o[x].x;
           acc.y += wv[x] * o[x].y;
@@ -841,7 +840,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const AttP
       for (int x = 0; x < WPR; ++x) {
         // a warp whose partials are all NaN has no maximum, but a NaN sum
         const float f = s_m[warp + x] == kNegInf ? (s_sum[warp + x] == 0.f ? 0.f : 1.f) : exp2f(s_m[warp + x] - m);
-        if (f == 0.f) continue;
         const float4 v = *reinterpret_cast<const float4*>(&s_acc[warp + x][4 * lane]);
         sum += f * s_sum[warp + x];
         acc.x += f * v.x;

@@ -899,3 +899,39 @@ def test_attention_reads_what_the_calls_before_it_wrote(tsel):
         torch.cuda.synchronize()
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
     assert tsel.tsel_read_device_status(ws) == 0
+
+
+@pytest.mark.parametrize("rows,prefix", [([1], 300), ([1], 9000), ([2] * 40, 300), ([90], 9000)])
+def test_attention_nan_row_under_far_larger_logits(tsel, rows, prefix):
+    """A NaN V row makes NaN of every row that sees it, also where another chunk
+    holds logits so much higher that its own chunk's weight is 0 in fp32."""
+    def high(k):
+        k[prefix - 1] = 40.0                   # q is positive: 40 * 64 * mean q / 8, some 250 above the rest
+        k[:prefix - 1] = np.minimum(k[:prefix - 1], 1.0)
+
+    def nan_row(v):
+        v[3, 0, 7] = np.nan
+
+    b = Batch(tsel, 60, rows, [n + 5 for n in rows], prefix, 4, 2, 64, 16, BF, spread=0, k_rows=high, v_rows=nan_row)
+    b.q = b.q.abs() + 0.25
+    out, lse = b.run()
+    assert torch.isnan(out[:, :2]).all() and torch.isfinite(out[:, 2:]).all() and torch.isfinite(lse).all()
+    b.check(out, lse)
+
+
+@pytest.mark.parametrize("rows", [[1], [2] * 40])
+def test_attention_nan_row_of_a_suffix_under_a_far_larger_prefix(tsel, rows):
+    """... between a request's suffix and the prefix: the other requests stay finite."""
+    def high(k):
+        k[9] = 40.0
+        k[300:] = np.minimum(k[300:], 1.0)
+
+    def nan_row(v):
+        v[300, 1, 0] = np.nan                  # the first suffix key of request 0
+
+    b = Batch(tsel, 61, rows, [n + 5 for n in rows], 300, 4, 2, 64, 16, BF, spread=0, k_rows=high, v_rows=nan_row)
+    b.q = b.q.abs() + 0.25
+    out, lse = b.run()
+    want = torch.zeros(len(b.q), 4, dtype=torch.bool)
+    want[:rows[0], 2:] = True
+    assert torch.equal(torch.isnan(out).any(-1).cpu(), want) and torch.isfinite(lse).all()
