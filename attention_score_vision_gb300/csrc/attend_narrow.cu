@@ -290,9 +290,11 @@ __global__ void __launch_bounds__(kNarThreads, NarCfg<D, NB>::CTAS) attend_narro
       }
     }
     // ---- scales of keys g and g + 8: the byte is a float's exponent; 0 is the
-    // denormal 2^-127, 255 an infinity, which makes NaN of the codes 0 that it comes with
+    // denormal 2^-127, 255 makes NaN of the row whatever its codes
     const uint8_t* ex = stage + C::SLOTS * 512;
-    auto scale = [](uint8_t e) -> float { return __uint_as_float(max(uint32_t(e) << 23, 0x400000u)); };
+    auto scale = [](uint8_t e) -> float {
+      return __uint_as_float(e == 255 ? 0x7FC00000u : max(uint32_t(e) << 23, 0x400000u));
+    };
     const float kf[2] = {scale(ex[g]), scale(ex[8 + g])};
     float vf[2] = {scale(ex[16 + g]), scale(ex[24 + g])};
 #pragma unroll
@@ -363,7 +365,7 @@ __global__ void __launch_bounds__(kNarThreads, NarCfg<D, NB>::CTAS) attend_narro
       }
     }
     // ---- P, with V's scales relative to the reference, as B fragments
-    const float vr[2] = {vf[0] * vinv, vf[1] * vinv};   // at most 1, or infinite
+    const float vr[2] = {vf[0] * vinv, vf[1] * vinv};   // at most 1, or NaN
     uint32_t pb[NB][2];
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
@@ -375,7 +377,7 @@ __global__ void __launch_bounds__(kNarThreads, NarCfg<D, NB>::CTAS) attend_narro
           const float pr = ex2(fmaf(s[n][2 * x + y], qc[n][y], shift[n][y]));
           l[n][y] += pr;
           e[y] = pr * vr[x];
-          if (!full && key0 + 8 * x + g >= end[n][y]) e[y] = 0.f;   // not 0 * infinity
+          if (!full && key0 + 8 * x + g >= end[n][y]) e[y] = 0.f;   // not 0 * NaN
         }
         pb[n][x] = transpose8(f16x2(e[0], e[1]));
       }

@@ -935,3 +935,35 @@ def test_attention_nan_row_of_a_suffix_under_a_far_larger_prefix(tsel, rows):
     want = torch.zeros(len(b.q), 4, dtype=torch.bool)
     want[:rows[0], 2:] = True
     assert torch.equal(torch.isnan(out).any(-1).cpu(), want) and torch.isfinite(lse).all()
+
+
+def _reread(b):
+    """The batch's cache as values, after a test wrote to its pages itself."""
+    codes = [t.cpu().numpy() for t in b.cache]
+    flat = lambda c: np.ascontiguousarray(np.moveaxis(c, 1, 2)).reshape((-1, b.Hkv) + c.shape[3:])   # noqa: E731
+    b.k, b.v = O.dequantise(flat(codes[0]), flat(codes[2])), O.dequantise(flat(codes[1]), flat(codes[3]))
+
+
+def _at(b, slot):
+    return int(slot) // b.ps, int(slot) % b.ps
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("which", [0, 1], ids=["k", "v"])
+@pytest.mark.parametrize("where", ["prefix", "suffix"])
+def test_attention_scale_byte_255_is_nan_whatever_the_codes(tsel, rows, which, where):
+    """A visible row whose byte is 255 while its codes are ordinary ones makes NaN
+    of the rows that see it, in both kernels, as the cache read has it."""
+    b = Batch(tsel, 62, [rows, 2], [rows + 20, 30], 200, 4, 2, 64, 16, BF, spread=0)
+    page, off = _at(b, b.prefix_rows[150] if where == "prefix" else b.suffix_rows[0][3])
+    b.cache[2 + which][page, 1, off] = 255
+    assert b.cache[which][page, 1, off].any()
+    _reread(b)
+    out, lse = b.run()
+    b.check(out, lse)
+    want = torch.zeros(rows + 2, 4, dtype=torch.bool)
+    want[:None if where == "prefix" else rows, 2:] = True
+    assert torch.equal(torch.isnan(out).all(-1).cpu(), want)
+    assert torch.equal(torch.isnan(lse).T.cpu(), want if which == 0 else torch.zeros_like(want))
+    got = tsel.tsel_cache_read(b.cache, i32([page * 16 + off]))[which]
+    assert torch.isnan(got[0, 1]).all() and torch.isfinite(got[0, 0]).all()
