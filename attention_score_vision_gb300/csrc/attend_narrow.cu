@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kNarThreads, NarCfg<D, NB>::CTAS) attend_narro
       const float sv = dv < -126 ? 0.f : __uint_as_float(uint32_t(127 + dv) << 23);
       vref = vnew;
       vtop = __uint_as_float(uint32_t(vnew) << 23);
-      vinv = __uint_as_float(uint32_t(254 - vnew) << 23);
+      vinv = __uint_as_float(max(uint32_t(254 - vnew) << 23, 0x400000u));   // 2^-127 is a denormal
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
         float so[2];

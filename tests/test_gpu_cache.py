@@ -967,3 +967,19 @@ def test_attention_scale_byte_255_is_nan_whatever_the_codes(tsel, rows, which, w
     assert torch.equal(torch.isnan(lse).T.cpu(), want if which == 0 else torch.zeros_like(want))
     got = tsel.tsel_cache_read(b.cache, i32([page * 16 + off]))[which]
     assert torch.isnan(got[0, 1]).all() and torch.isfinite(got[0, 0]).all()
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("byte", [247, 252, 253, 254])
+def test_attention_largest_scale_bytes_of_v(tsel, rows, byte):
+    """V rows of the largest scales, values of 2^118 to 2^126, beside ordinary ones."""
+    b = Batch(tsel, 63, [rows], [rows + 20], 200, 4, 2, 64, 16, BF, spread=0)
+    rng = np.random.default_rng(64)
+    for slot in (b.prefix_rows[7], b.prefix_rows[160], b.suffix_rows[0][0]):
+        page, off = _at(b, slot)
+        b.cache.v_pages[page, :, off] = torch.from_numpy(rng.integers(1, 48, (2, 64)).astype(np.uint8)).cuda()   # 2^-9 to 0.47
+        b.cache.v_exps[page, :, off] = byte
+    _reread(b)
+    out, lse = b.run()
+    assert torch.isfinite(out).all() and (out[:, :, :].abs() > 2.0 ** (byte - 150)).any()
+    b.check(out, lse)
