@@ -729,6 +729,8 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
         }
       }
       if (!do_k) fac_v[par * kTile + tid] = vb == 255u ? 0u : att_factor(int(vb), vref);
+      // the codes of a V row of byte 255 may be E4M3's NaN, which a factor of 0 would let through to rows that do not see it
+      const bool drop = __any_sync(0xffffffffu, !do_k && __vcmpeq4(ve, 0xFFFFFFFFu) != 0u);
       // the factors of the next tile go to the other half, so one barrier will do
       if (do_k)
         asm volatile("bar.sync 1, 128;" ::: "memory");
@@ -740,6 +742,11 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
       uint64_t* free_ = do_k ? k_free : v_free;
       if (t >= C::KS) ok = ok && warp_wait(&free_[st], uint32_t(((t - C::KS) / C::KS) & 1), abort_flag, T);
       if (ok) {
+        if (drop) {   // rows of factor 0, whatever their codes
+#pragma unroll
+          for (int i = 0; i < 4 * C::DC; ++i)
+            if (fac_v[par * kTile + 32 * (i & 3) + r0] == 0u) raw[i] = make_uint4(0, 0, 0, 0);
+        }
         convert(smem + (do_k ? C::OFF_K : C::OFF_V) + st * C::TILE_BYTES, (do_k ? fac_k : fac_v) + par * kTile);
         mbar_arrive_lane0(&full[st], lane);
         load(t + 1);

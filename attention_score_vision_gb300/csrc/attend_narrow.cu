@@ -315,7 +315,8 @@ __global__ void __launch_bounds__(kNarThreads, NarCfg<D, NB>::CTAS) attend_narro
         if (key >= keys) vf[x] = 0.f;   // whatever the page holds there
       }
     }
-    bool move = fmaxf(vf[0], vf[1]) > vtop;
+    bool move = !(vf[0] <= vtop && vf[1] <= vtop);   // also for a NaN
+    bool v_nan = false;   // the block has V rows of scale byte 255
     float top[NB][2];
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
@@ -326,6 +327,7 @@ __global__ void __launch_bounds__(kNarThreads, NarCfg<D, NB>::CTAS) attend_narro
       }
     }
     if (__any_sync(0xffffffffu, move)) {
+      v_nan = __any_sync(0xffffffffu, vf[0] != vf[0] || vf[1] != vf[1]);
       // the largest finite scale; V references only grow
       uint32_t ev = 0;
 #pragma unroll
@@ -386,6 +388,11 @@ __global__ void __launch_bounds__(kNarThreads, NarCfg<D, NB>::CTAS) attend_narro
     uint4 vr4[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) vr4[t] = *reinterpret_cast<const uint4*>(codes + (2 * C::KSLOTS + t) * 512);
+    if (v_nan) {   // P holds the NaN of the rows that see them; their codes, which may be E4M3's NaN, reach no others
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        if (ex[16 + 2 * c + (t & 1) + 8 * (t >> 1)] == 255) vr4[t] = make_uint4(0, 0, 0, 0);
+    }
 #pragma unroll
     for (int q = 0; q < C::CB / 4; ++q) {
       const uint32_t a = (&vr4[0].x)[q], b = (&vr4[1].x)[q], d = (&vr4[2].x)[q], e = (&vr4[3].x)[q];

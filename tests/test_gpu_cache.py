@@ -983,3 +983,25 @@ def test_attention_largest_scale_bytes_of_v(tsel, rows, byte):
     out, lse = b.run()
     assert torch.isfinite(out).all() and (out[:, :, :].abs() > 2.0 ** (byte - 150)).any()
     b.check(out, lse)
+
+
+@pytest.mark.parametrize("rows", [[4, 1], [40, 2]])
+@pytest.mark.parametrize("code", [0x7F, 0xFF, 0x7E, 0x00])
+def test_attention_hidden_rows_of_byte_255_never_reach(tsel, rows, code):
+    """Drafted keys marked as NaN by their scale byte, whatever their codes (E4M3's
+    NaN among them): rows of the request that do not see them stay as they were."""
+    b = Batch(tsel, 65, rows, [n + 20 for n in rows], 100, 4, 2, 64, 16, BF, spread=1)
+    clean, lse0 = b.run()
+    n = rows[0]
+    page, off = _at(b, b.suffix_rows[0][20 + n // 2])       # seen from row n // 2 on
+    for t in b.cache[:2]:
+        t[page, 0, off] = code
+    for t in b.cache[2:]:
+        t[page, 0, off] = 255
+    _reread(b)
+    out, lse = b.run()
+    want = torch.zeros(len(b.q), 4, dtype=torch.bool)
+    want[n // 2:n, :2] = True
+    assert torch.equal(torch.isnan(out).all(-1).cpu(), want) and torch.equal(torch.isnan(out).any(-1).cpu(), want)
+    assert torch.equal(torch.isnan(lse).T.cpu(), want)
+    b.check(out, lse)
