@@ -58,7 +58,10 @@
 // Masked keys never reach a result: V rows past the last visible key of a tile
 // are zeros whatever the page holds, S of masked keys is replaced, not added
 // to, and a row stored as NaN (scale byte 255) enters through S (K) or P (V) of
-// the rows that see it only.
+// the rows that see it only. Not looked for: a NaN code under another byte in a
+// V row that later rows of the same unit see (0 times NaN in the second
+// product). The cache write leaves none, and a test of every code would lengthen
+// every conversion.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -498,8 +498,9 @@ TSEL_API tsel_status tsel_rope(const void* q, int64_t q_row_stride, const void* 
  * [num_pages, num_kv_heads, page_size, head_dim], and k_exps and v_exps, bytes
  * [num_pages, num_kv_heads, page_size], all 16-byte aligned. A row (one token
  * and head) stands for code * 2^(byte - 127); byte 255 makes the whole row
- * NaN. Slot s is place s mod page_size of page s / page_size. page_size is 16,
- * 32, 64 or 128, head_dim 64, 80, 96, 112 or 128, num_pages * page_size at most
+ * NaN, whatever its codes. Slot s is place s mod page_size of page
+ * s / page_size. page_size is 16, 32, 64 or 128, head_dim 64, 80, 96, 112 or
+ * 128, num_pages * page_size at most
  * 2^31 - 1.
  *
  * tsel_cache_write quantises the K and V rows of `total` tokens into slots
@@ -587,13 +588,19 @@ TSEL_API size_t tsel_prefix_attention_workspace_size(int num_req, int total_q, i
  *
  * Lengths outside their bounds set TSEL_DEV_SEQLENS, pages outside the cache
  * TSEL_DEV_PAGES; the rows concerned are then unspecified, and nothing out of
- * range is touched. Keys that a row does not see never reach it, whatever
- * their pages hold. Rows stored as NaN make NaN of the rows that see them.
+ * range is touched. Rows stored as NaN (byte 255) make NaN of the rows that see
+ * them. Keys that a row does not see never reach it, whatever their pages hold,
+ * with one exception: E4M3's NaN as a code (0x7F, 0xFF) under another byte, which
+ * tsel_cache_write never leaves. In a V row it makes NaN of its column in the
+ * rows that see the key, and may in rows of the same request that come before
+ * them.
  * Results are deterministic. Precision: q and the cached rows enter as fp16
  * after scaling by powers of two (exact but for q elements below 2^-27 of the
  * largest of their row, K rows below 2^-22 and V rows below 2^-20 of the
- * largest of their key chunk, which round on that grid), probabilities as
- * fp16, with sums and statistics in fp32.
+ * largest of their key chunk, keys of later rows among them, which round on that
+ * grid), probabilities as fp16 (with up to 32 rows of a KV head after they were
+ * multiplied by V's scale relative to that largest), with sums and statistics in
+ * fp32.
  */
 TSEL_API tsel_status tsel_prefix_attention(
     const void* q, int64_t q_row_stride, const int32_t* cu_seqlens_q, int num_req, int total_q,

@@ -1005,3 +1005,27 @@ def test_attention_hidden_rows_of_byte_255_never_reach(tsel, rows, code):
     assert torch.equal(torch.isnan(out).all(-1).cpu(), want) and torch.equal(torch.isnan(out).any(-1).cpu(), want)
     assert torch.equal(torch.isnan(lse).T.cpu(), want)
     b.check(out, lse)
+
+
+@pytest.mark.parametrize("rows", [[4, 1], [40, 2]])
+def test_attention_nan_codes_under_an_ordinary_byte(tsel, rows):
+    """E4M3's NaN as a code, which the cache write never leaves: rows that see the
+    key are NaN (in that column for V, whole for K). A K row reaches no others, a
+    V row no other request, no other KV head and no other column."""
+    for which in (0, 1):
+        b = Batch(tsel, 66, rows, [n + 20 for n in rows], 100, 4, 2, 64, 16, BF, spread=1)
+        clean, lse0 = b.run()
+        n = rows[0]
+        page, off = _at(b, b.suffix_rows[0][20 + n // 2])
+        b.cache[which][page, 0, off, 5] = 0x7F
+        out, lse = b.run()
+        nan = torch.isnan(out).cpu()
+        assert nan[n // 2:n, :2, 5].all()
+        if which == 0:
+            assert nan[n // 2:n, :2].all() and not nan[:n // 2].any() and not nan[n:].any() and not nan[:, 2:].any()
+            hidden = torch.cat([out[:n // 2], out[n:]]).float(), torch.cat([clean[:n // 2], clean[n:]]).float()
+            assert torch.allclose(*hidden, rtol=2.0 ** -6, atol=2.0 ** -6)
+        else:
+            assert torch.equal(out[n:], clean[n:]) and torch.equal(out[:n, 2:], clean[:n, 2:]) and torch.equal(lse, lse0)
+            rest = torch.arange(64) != 5
+            assert torch.equal(out[..., rest], clean[..., rest])
