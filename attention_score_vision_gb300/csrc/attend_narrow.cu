@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kNarThreads, NarCfg<D, NB>::CTAS) attend_narro
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
           const int E = max(int(top >> 23), 14);
           const float up = __uint_as_float(uint32_t(267 - E) << 23);   // largest element into [2^13, 2^14)
-          const float mine_c = fmaxf(p.c * __uint_as_float(uint32_t(E - 13) << 23), 1e-38f);   // 2^(E - 140)
+          const float mine_c = p.c * __uint_as_float(uint32_t(E - 13) << 23);   // 2^(E - 140)
 #pragma unroll
           for (int s = 0; s < C::KSTEPS; ++s) {
 #pragma unroll
@@ -290,7 +290,9 @@ __global__ void __launch_bounds__(kNarThreads, NarCfg<D, NB>::CTAS) attend_narro
       }
     }
     // ---- scales of keys g and g + 8: the byte is a float's exponent; 0 is the
-    // denormal 2^-127, 255 makes NaN of the row whatever its codes
+    // denormal 2^-127, 255 makes NaN of the row whatever its codes. The two
+    // scales of a logit are multiplied first: with either alone it can leave
+    // fp32's range (large keys under small queries).
     const uint8_t* ex = stage + C::SLOTS * 512;
     auto scale = [](uint8_t e) -> float {
       return __uint_as_float(e == 255 ? 0x7FC00000u : max(uint32_t(e) << 23, 0x400000u));
@@ -300,7 +302,7 @@ __global__ void __launch_bounds__(kNarThreads, NarCfg<D, NB>::CTAS) attend_narro
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) s[n][x] = (s[n][x] + s1[n][x]) * kf[x >> 1];
+      for (int x = 0; x < 4; ++x) s[n][x] = (s[n][x] + s1[n][x]) * (kf[x >> 1] * qc[n][x & 1]);
     }
     const bool full = key0 + kNarKeys <= min_end;
     if (!full) {
@@ -322,7 +324,7 @@ __global__ void __launch_bounds__(kNarThreads, NarCfg<D, NB>::CTAS) attend_narro
     for (int n = 0; n < NB; ++n) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        top[n][x] = fmaxf(s[n][x], s[n][2 + x]) * qc[n][x];
+        top[n][x] = fmaxf(s[n][x], s[n][2 + x]);
         move = move || top[n][x] > m[n][x] + kNarSlack;
       }
     }
@@ -376,7 +378,7 @@ __global__ void __launch_bounds__(kNarThreads, NarCfg<D, NB>::CTAS) attend_narro
         float e[2];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const float pr = ex2(fmaf(s[n][2 * x + y], qc[n][y], shift[n][y]));
+          const float pr = ex2(s[n][2 * x + y] + shift[n][y]);
           l[n][y] += pr;
           e[y] = pr * vr[x];
           if (!full && key0 + 8 * x + g >= end[n][y]) e[y] = 0.f;   // not 0 * NaN

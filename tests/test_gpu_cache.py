@@ -1029,3 +1029,32 @@ def test_attention_nan_codes_under_an_ordinary_byte(tsel, rows):
             assert torch.equal(out[n:], clean[n:]) and torch.equal(out[:n, 2:], clean[:n, 2:]) and torch.equal(lse, lse0)
             rest = torch.arange(64) != 5
             assert torch.equal(out[..., rest], clean[..., rest])
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("kexp,qexp", [(112, -110), (100, -100), (-100, 105)])
+def test_attention_far_scales_of_k_and_q(tsel, rows, kexp, qexp):
+    """Some K rows of 2^112 under queries of 2^-110: the logits are ordinary numbers
+    although a product of codes and scale alone passes fp32's range; and the other way round."""
+    def far(k):
+        k[::3] *= 2.0 ** kexp
+
+    b = Batch(tsel, 67, [rows], [rows + 40], 260, 4, 2, 64, 16, BF, spread=0, k_rows=far if kexp > 0 else lambda k: np.multiply(k, 2.0 ** kexp, out=k),
+              qscale=2.0 ** qexp)
+    out, lse = b.run()
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    b.check(out, lse)
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_attention_largest_scale_bytes_of_k(tsel, rows):
+    b = Batch(tsel, 68, [rows], [rows + 20], 200, 4, 2, 64, 16, BF, spread=0, qscale=2.0 ** -114)
+    rng = np.random.default_rng(69)
+    for i, byte in ((7, 254), (60, 253), (160, 250), (199, 248)):
+        page, off = _at(b, b.prefix_rows[i])
+        codes = rng.integers(1, 8, (2, 64)) | np.where(rng.random((2, 64)) < 0.5, 128, 0)     # +-2^-9 to 2^-6.2
+        b.cache.k_pages[page, :, off] = torch.from_numpy(codes.astype(np.uint8)).cuda()
+        b.cache.k_exps[page, :, off] = byte
+    _reread(b)
+    out, lse = b.run()
+    b.check(out, lse)
