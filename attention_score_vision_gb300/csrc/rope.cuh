@@ -7,7 +7,7 @@
 // the position is taken modulo 2^64, that is modulo one turn, exactly: range
 // reduction loses nothing (in floating point 32 bits lose 2^-24 of the whole
 // angle, and 64-bit arithmetic is slow on this part), and the phase is off by
-// the entry's rounding alone, 2^-62 of a turn for each step of position. It is
+// the entry's rounding alone, 2^-61 of a turn for each step of position. It is
 // then reduced to an eighth of a turn on either side of the nearest quarter in
 // integers, and what is left is rounded to fp32's 24 significant bits (not cut
 // to a fixed step: the slow pairs' small angles keep their bits; it costs 0.7%

@@ -465,7 +465,7 @@ TSEL_API size_t tsel_cache_workspace_size(void);
  * Rotates the first 2 * num_pairs columns of every head of Q and K: with
  * angle = pos[t][axis_i] * inv_freq_i, pair (a, b) becomes
  * (a cos - b sin, b cos + a sin); the other columns are copied. The angle is
- * within |pos| 2^-62 turns of that for every int32 position, sine and cosine
+ * within |pos| 2^-61 turns of that for every int32 position, sine and cosine
  * are fp32 values within 4 * 2^-24 of their own size, the products are fp32,
  * rounded once to the output type. With TSEL_ROPE_INVERSE the pairs turn
  * back: applied to the gradients of q_out and k_out it gives those of q and k.

@@ -1064,7 +1064,7 @@ def test_attention_largest_scale_bytes_of_k(tsel, rows):
 def test_rope_small_angles_keep_their_bits(tsel, adjacent):
     """Sines and cosines alone (pairs (0, 1) and (1, 0)), relative to their own size:
     2^-24 for the phase as fp32, an ulp (2^-23) for the function, and the table's
-    2^-62 of a turn per step of position."""
+    2^-61 of a turn per step of position (a frequency is rounded in two parts)."""
     for f, a in (O.rope_frequencies(1e6, [24, 20, 20], "interleaved"), O.rope_frequencies(1e4, [64, 0, 0], "sectioned"),
                  (np.asarray([1e-6, 1e-5, 3e-8, 1.3e-4, 6.283185, 3.1415927, 1.5707964, -1e-3]), np.zeros(8, np.int64))):
         table = tsel.tsel_rope_table(f.tolist(), a.tolist())
@@ -1076,5 +1076,5 @@ def test_rope_small_angles_keep_their_bits(tsel, adjacent):
         x[:, 1, first] = 1                     # -> (cos, sin)
         got, _ = tsel.tsel_rope(torch.from_numpy(x).cuda(), None, i32(pos), table, flags=tsel.TSEL_ROPE_ADJACENT if adjacent else 0)
         ref = O.rope(x, pos, f, a, adjacent)
-        step = np.abs(pos[:, :1, None].astype(np.float64)) * 2 * np.pi * 2.0 ** -62
+        step = np.abs(pos[:, :1, None].astype(np.float64)) * 2 * np.pi * 2.0 ** -61
         assert np.all(np.abs(_np(got) - ref) <= np.abs(ref) * 4 * 2.0 ** -24 + step)
