@@ -658,13 +658,45 @@ def tsel_rope_table(inv_freq: Sequence[float], axis: Sequence[int], device="cuda
     return table.to(device)
 
 
+class _Rotation(torch.autograd.Function):
+    """tsel_rope on the tape: the gradient of a rotation is the rotation back."""
+
+    @staticmethod
+    def forward(ctx, q, k, pos, table, flags, workspace, stream):
+        q_out, k_out = tsel_rope(q, k, pos, table, flags=flags, workspace=workspace, stream=stream)
+        ctx.save_for_backward(pos, table)
+        ctx.flags, ctx.workspace = flags ^ TSEL_ROPE_INVERSE, workspace
+        ctx.set_materialize_grads(False)
+        # each output depends on its own input alone
+        ctx.mark_non_differentiable(*[t for t, need in zip((q_out, k_out), ctx.needs_input_grad) if t is not None and not need])
+        return q_out, k_out
+
+    @staticmethod
+    def backward(ctx, *grads):
+        pos, table = ctx.saved_tensors
+        turned = [None, None]
+        # a gradient may come expanded or transposed
+        given = [i for i in (0, 1) if ctx.needs_input_grad[i] and grads[i] is not None]
+        if given:
+            g = [grads[i].contiguous() for i in given] + [None]
+            back = tsel_rope(g[0], g[1], pos, table, flags=ctx.flags, workspace=ctx.workspace)
+            for i, t in zip(given, back):
+                turned[i] = t
+        return (*turned, None, None, None, None, None)
+
+
 def tsel_rope(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, table: torch.Tensor, *,
               flags: int = 0, q_out: Optional[torch.Tensor] = None,
               k_out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
               stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
     """Rotates q [T, H, d] and k [T, Hkv, d] (or None) by positions pos int32 [T, axes];
     returns (q_out, k_out), which may be q and k themselves. With
-    TSEL_ROPE_INVERSE it turns gradients of the outputs into those of the inputs."""
+    TSEL_ROPE_INVERSE it turns gradients of the outputs into those of the inputs.
+
+    Where autograd records (grad mode, and q or k requires a gradient) the
+    outputs carry gradients; they are then new tensors, q_out and k_out are
+    refused. The backward pass runs on the stream that was current in the forward
+    call; to capture it into a graph, let no eager graph of the same leaves live."""
     shape, dtype, index = _first(q, "q")
     qs = _rows(q, "q", index, dtype)
     total, H, d = shape
@@ -681,6 +713,10 @@ def tsel_rope(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, tab
     qos = 0 if q_out is None else _rows(q_out, "q_out", index, dtype, shape)
     if k_out is not None:
         kos = _rows(k_out, "k_out", index, dtype, k_shape)
+    if torch.is_grad_enabled() and (q.requires_grad or (k is not None and k.requires_grad)):
+        if q_out is not None or k_out is not None:
+            raise ValueError("q_out and k_out cannot be written where autograd records q or k")
+        return _Rotation.apply(q, k, pos, table, flags, workspace, stream)
     workspace = _workspace(workspace, 1024, index, stream)
     if q_out is None:
         q_out = _like(q, stream)

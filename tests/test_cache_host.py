@@ -310,3 +310,19 @@ def test_binding_refuses_what_the_kernels_cannot_see(tsel):
         with pytest.raises((TypeError, ValueError)):
             fn()
             pytest.fail(f"call {i} was not refused")
+
+
+def test_binding_refuses_outputs_where_autograd_records(tsel):
+    """A recorded rotation returns new tensors."""
+    bf = torch.bfloat16
+
+    def fake(shape, grad):
+        t = _Fake(shape, bf)
+        t.requires_grad = grad
+        return t
+
+    pos, table = _Fake((5, 3), torch.int32), _Fake((32,), torch.int64)
+    for grads in ((True, False, False, False), (False, True, False, False), (True, True, False, False)):
+        q, k, qo, ko = (fake((5, h, 64), g) for h, g in zip((4, 2, 4, 2), grads))
+        with pytest.raises(ValueError, match="autograd records"):
+            tsel.tsel_rope(q, k, pos, table, q_out=qo, k_out=ko)

@@ -1078,3 +1078,56 @@ def test_rope_small_angles_keep_their_bits(tsel, adjacent):
         ref = O.rope(x, pos, f, a, adjacent)
         step = np.abs(pos[:, :1, None].astype(np.float64)) * 2 * np.pi * 2.0 ** -61
         assert np.all(np.abs(_np(got) - ref) <= np.abs(ref) * 4 * 2.0 ** -24 + step)
+
+
+def test_rope_carries_gradients(tsel):
+    """Where autograd records, the rotation is part of the graph: gradients of
+    shared, expanded and partly needed inputs against the formula's, and through
+    the backward pass itself."""
+    table, f, a = _table(tsel, [6, 5, 5], "interleaved", base=1e4)
+    rng = np.random.default_rng(70)
+    x, y, gx, gy = (torch.from_numpy(rng.standard_normal((9, h, 40))).float().cuda() for h in (4, 2, 4, 2))
+    pos = rng.integers(0, 500, (9, 3)).astype(np.int32)
+    for flags, inverse in ((0, False), (tsel.TSEL_ROPE_INVERSE, True)):
+        q, k = x.clone().requires_grad_(), y.clone().requires_grad_()
+        qo, ko = tsel.tsel_rope(q, k, i32(pos), table, flags=flags)
+        plain = tsel.tsel_rope(x, y, i32(pos), table, flags=flags)
+        assert torch.equal(qo, plain[0]) and torch.equal(ko, plain[1]) and not plain[0].requires_grad
+        ((qo * gx).sum() + (ko * gy).sum()).backward()
+        _close_rotation(q.grad, _np(gx), pos, f, a, False, not inverse, FP)
+        _close_rotation(k.grad, _np(gy), pos, f, a, False, not inverse, FP)
+    q = x.clone().requires_grad_()
+    qo, ko = tsel.tsel_rope(q, y, i32(pos), table)          # K needs none
+    assert qo.requires_grad and not ko.requires_grad
+    qo.sum().backward()                                     # an expanded gradient
+    _close_rotation(q.grad, np.ones((9, 4, 40)), pos, f, a, False, True, FP)
+    q.grad = None
+    qo, none = tsel.tsel_rope(q, None, i32(pos), table)
+    g, = torch.autograd.grad((qo ** 2).sum(), q, create_graph=True)
+    assert none is None and torch.allclose(g, 2 * q, atol=1e-5)    # the rotation keeps lengths
+    h, = torch.autograd.grad((g * gx).sum(), q)
+    assert torch.allclose(h, 2 * gx, atol=1e-5)
+    with torch.no_grad():
+        assert not tsel.tsel_rope(q, None, i32(pos), table)[0].requires_grad
+
+
+def test_rope_gradients_in_a_captured_graph(tsel):
+    table, f, a = _table(tsel, [16, 16], "sectioned")
+    rng = np.random.default_rng(71)
+    pos = i32(rng.integers(0, 99, (7, 2)))
+    q = torch.from_numpy(rng.standard_normal((7, 2, 64))).float().cuda().requires_grad_()
+    g = torch.from_numpy(rng.standard_normal((7, 2, 64))).float().cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            got, = torch.autograd.grad(tsel.tsel_rope(q, None, pos, table)[0], q, g)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, = torch.autograd.grad(tsel.tsel_rope(q, None, pos, table)[0], q, g)
+    for seed in (1, 2):
+        g.copy_(torch.from_numpy(np.random.default_rng(seed).standard_normal((7, 2, 64))))
+        graph.replay()
+        want, _ = tsel.tsel_rope(g, None, pos, table, flags=tsel.TSEL_ROPE_INVERSE)
+        assert torch.equal(out, want)
