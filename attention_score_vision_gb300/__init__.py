@@ -624,6 +624,14 @@ def _like(t: torch.Tensor, stream) -> torch.Tensor:
     return _new(stream, torch.empty, t.shape, dtype=t.dtype, device=t.device)
 
 
+def _written(*outs) -> None:
+    """Tells autograd that a call writes into tensors it was given (or None)."""
+    given = [t for t in outs if t is not None]
+    if any(t.requires_grad for t in given) and torch.is_grad_enabled():
+        raise ValueError("an output that requires a gradient cannot be written where autograd records")
+    torch.autograd.graph.increment_version(given)
+
+
 def _workspace(workspace: Optional[torch.Tensor], nbytes: int, index: int, stream) -> torch.Tensor:
     if workspace is None:
         return _new(stream, _new_workspace, nbytes, device=torch.device("cuda", index))
@@ -717,6 +725,8 @@ def tsel_rope(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, tab
         if q_out is not None or k_out is not None:
             raise ValueError("q_out and k_out cannot be written where autograd records q or k")
         return _Rotation.apply(q, k, pos, table, flags, workspace, stream)
+    if q_out is not None or k_out is not None:
+        _written(q_out, k_out)
     workspace = _workspace(workspace, 1024, index, stream)
     if q_out is None:
         q_out = _like(q, stream)
@@ -801,6 +811,8 @@ def tsel_cache_read(cache: TselCache, slots: torch.Tensor, *, dtype=torch.bfloat
     shape = (slots.numel(), Hkv, d)
     kos = 0 if k_out is None else _rows(k_out, "k_out", index, dtype, shape)
     vos = 0 if v_out is None else _rows(v_out, "v_out", index, dtype, shape)
+    if k_out is not None or v_out is not None:
+        _written(k_out, v_out)
     workspace = _workspace(workspace, 1024, index, stream)
     if k_out is None:
         k_out = _new(stream, torch.empty, shape, dtype=dtype, device=slots.device)
@@ -839,7 +851,8 @@ def tsel_prefix_attention(q: torch.Tensor, cu_seqlens_q: torch.Tensor, max_seqle
     prefix_len int32 [1] (None with max_prefix_len 0); page_table int32
     [R, pages] and suffix_lens int32 [R] (None with max_suffix_len 0). A
     request's last query rows are its last suffix tokens (causal). Rows past
-    cu_seqlens_q[R] are left as they are in a given out or lse."""
+    cu_seqlens_q[R] are left as they are in a given out or lse. The results carry
+    no gradients."""
     shape, dtype, index = _first(q, "q")
     if dtype is _F32:
         raise TypeError("q must be bf16 or fp16")
@@ -883,6 +896,8 @@ def tsel_prefix_attention(q: torch.Tensor, cu_seqlens_q: torch.Tensor, max_seqle
     os_ = 0 if out is None else _rows(out, "out", index, dtype, shape)
     if lse is not None:
         _vector(lse, _F32, "lse", index, H * tq)
+    if out is not None or lse is not None:
+        _written(out, lse)
     nbytes = 0 if workspace is not None else tsel_prefix_attention_workspace_size(
         R, tq, max_seqlen_q, H, Hkv, d, max_p, max_s)
     workspace = _workspace(workspace, nbytes, index, stream)

@@ -326,3 +326,25 @@ def test_binding_refuses_outputs_where_autograd_records(tsel):
         q, k, qo, ko = (fake((5, h, 64), g) for h, g in zip((4, 2, 4, 2), grads))
         with pytest.raises(ValueError, match="autograd records"):
             tsel.tsel_rope(q, k, pos, table, q_out=qo, k_out=ko)
+
+
+def test_binding_refuses_to_write_outputs_that_require_gradients(tsel):
+    """... as torch refuses them."""
+    bf = torch.bfloat16
+
+    def fake(shape, dtype=bf, grad=False):
+        t = _Fake(shape, dtype)
+        t.requires_grad = grad
+        return t
+
+    i32, cache = torch.int32, _fake_cache(tsel)
+    q, k, leaf_q, leaf_k = fake((5, 4, 64)), fake((5, 2, 64)), fake((5, 4, 64), grad=True), fake((5, 2, 64), grad=True)
+    pos, table, slots = _Fake((5, 3), i32), _Fake((32,), torch.int64), _Fake((5,), i32)
+    attend = (_Fake((3,), i32), 3, cache, _Fake((7,), i32), _Fake((1,), i32), 100, None, None, 0)
+    for call in (lambda: tsel.tsel_rope(q, None, pos, table, q_out=leaf_q),
+                 lambda: tsel.tsel_rope(q, k, pos, table, k_out=leaf_k),
+                 lambda: tsel.tsel_cache_read(cache, slots, v_out=leaf_k),
+                 lambda: tsel.tsel_prefix_attention(q, *attend, out=leaf_q),
+                 lambda: tsel.tsel_prefix_attention(q, *attend, lse=fake((4, 5), torch.float32, True))):
+        with pytest.raises(ValueError, match="autograd records"):
+            call()

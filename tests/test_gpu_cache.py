@@ -1131,3 +1131,35 @@ def test_rope_gradients_in_a_captured_graph(tsel):
         graph.replay()
         want, _ = tsel.tsel_rope(g, None, pos, table, flags=tsel.TSEL_ROPE_INVERSE)
         assert torch.equal(out, want)
+
+
+def test_autograd_notices_what_is_written_in_place(tsel):
+    table, _, _ = _table(tsel, [32], "sectioned")
+    x = torch.randn(3, 2, 64, device="cuda")
+    w = torch.randn(3, 2, 64, device="cuda", requires_grad=True)
+    pos = i32([[1], [2], [3]])
+    for k in (None, x):
+        saved = (w * x).sum()                               # keeps x for w's gradient
+        q = x if k is None else torch.randn(3, 2, 64, device="cuda")
+        tsel.tsel_rope(q, k, pos, table, q_out=q, k_out=k)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            saved.backward()
+    for call in (lambda: tsel.tsel_rope(w, None, pos, table, q_out=w),
+                 lambda: tsel.tsel_rope(w, None, pos, table, q_out=x),
+                 lambda: tsel.tsel_rope(x, w, pos, table, k_out=torch.empty_like(x)),
+                 lambda: tsel.tsel_rope(x, None, pos, table, q_out=w * 1.0)):
+        with pytest.raises(ValueError):
+            call()
+    b = Batch(tsel, 73, [2], [9], 40, 4, 2, 64, 16, BF)
+    for name, shape in (("out", (2, 4, 64)), ("lse", (4, 2))):
+        t = torch.ones(shape, dtype=BF if name == "out" else FP, device="cuda")
+        saved = (torch.ones_like(t).requires_grad_() * t).sum()
+        b.run(**{name: t})
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            saved.backward()
+    with torch.no_grad():
+        tsel.tsel_rope(w, None, pos, table, q_out=w)        # as torch has it
+    with torch.inference_mode():
+        y = torch.randn(3, 2, 64, device="cuda")
+        tsel.tsel_rope(y, None, pos, table, q_out=y)
+    tsel.tsel_rope(y, None, pos, table, q_out=x)            # an inference tensor read outside
