@@ -783,7 +783,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const AttP
   pdl_launch_dependents();
   pdl_wait();
   const int total = __ldg(p.cu_q + p.R);
-  if (total < 0 || total > p.Tq) {
+  // also where no suffix kernel looks at the requests one by one
+  if (total < 0 || total > p.Tq || total > int64_t(p.R) * p.max_q) {
     if (blockIdx.x == 0 && threadIdx.x == 0) set_status(p.status, TSEL_DEV_SEQLENS);
     return;
   }

@@ -587,9 +587,10 @@ TSEL_API size_t tsel_prefix_attention_workspace_size(int num_req, int total_q, i
  *               of the key chunks; nothing in it outlives the call but the
  *               status word.
  *
- * Lengths outside their bounds set TSEL_DEV_SEQLENS, pages outside the cache
- * TSEL_DEV_PAGES; the rows concerned are then unspecified, and nothing out of
- * range is touched. Rows stored as NaN (byte 255) make NaN of the rows that see
+ * Lengths outside their bounds set TSEL_DEV_SEQLENS (without suffixes, where the
+ * requests do not matter one by one, only more rows in all than num_req *
+ * max_seqlen_q), pages outside the cache TSEL_DEV_PAGES; the rows concerned are
+ * then unspecified, and nothing out of range is touched. Rows stored as NaN (byte 255) make NaN of the rows that see
  * them. Keys that a row does not see never reach it, whatever their pages hold,
  * with one exception: E4M3's NaN as a code (0x7F, 0xFF) under another byte, which
  * tsel_cache_write never leaves. In a V row it makes NaN of its column in the

@@ -1163,3 +1163,26 @@ def test_autograd_notices_what_is_written_in_place(tsel):
         y = torch.randn(3, 2, 64, device="cuda")
         tsel.tsel_rope(y, None, pos, table, q_out=y)
     tsel.tsel_rope(y, None, pos, table, q_out=x)            # an inference tensor read outside
+
+
+def test_attention_row_counts_past_their_bound_are_flagged(tsel):
+    """More rows than num_req * max_seqlen_q: flagged also where no suffix kernel
+    runs to look at the requests one by one."""
+    b = Batch(tsel, 72, [2, 1], [30, 7], 140, 4, 2, 64, 16, BF)
+    cu, mq, cache, pp, pl, mp, pt, sl, ms = b.args()
+    ws = torch.zeros(1 << 22, dtype=torch.uint8, device="cuda")
+
+    def status(*a):
+        tsel.tsel_clear_device_status(ws)
+        tsel.tsel_prefix_attention(b.q, *a, workspace=ws)
+        return tsel.tsel_read_device_status(ws)
+
+    S = tsel.TSEL_DEV_SEQLENS
+    assert status(cu, 0, cache, pp, pl, mp, pt, sl, ms) == S          # suffixes, but no rows by the bound
+    assert status(cu, 0, cache, pp, pl, mp, None, None, 0) == S
+    assert status(cu, 1, cache, pp, pl, mp, None, None, 0) == S
+    assert status(cu, 1, cache, None, None, 0, None, None, 0) == S
+    assert status(i32([3]), 2, cache, pp, pl, mp, None, None, 0) == S   # rows of no request
+    assert status(i32([0, 0, 0]), 0, cache, pp, pl, mp, pt, sl, ms) == 0
+    assert status(cu, 2, cache, pp, pl, mp, None, None, 0) == 0
+    assert status(i32([0]), 0, cache, pp, pl, mp, None, None, 0) == 0
