@@ -580,6 +580,13 @@ def _first(t: torch.Tensor, name: str):
     return shape, dtype, index
 
 
+def _sizes(bits: int) -> None:
+    """Refuses sizes (or-ed together) that a C int does not hold: a foreign call
+    takes their low 32 bits."""
+    if bits >> 31:
+        raise ValueError("a size is negative or past 2^31 - 1")
+
+
 def _vector(t: torch.Tensor, dtype, name: str, index: int, numel: Optional[int] = None) -> int:
     """Checks a dense tensor; returns its pointer."""
     if t.dtype is not dtype:
@@ -718,6 +725,7 @@ def tsel_rope(q: torch.Tensor, k: Optional[torch.Tensor], pos: torch.Tensor, tab
     elif k_out is not None:
         raise ValueError("k_out without k")
     pos_p, pos_dim, table_p, pairs = _rope_args(pos, table, total, index)
+    _sizes(total | H | Hkv | d | pos_dim | pairs)
     qos = 0 if q_out is None else _rows(q_out, "q_out", index, dtype, shape)
     if k_out is not None:
         kos = _rows(k_out, "k_out", index, dtype, k_shape)
@@ -790,6 +798,7 @@ def tsel_cache_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, cach
         raise ValueError("k and v do not match the cache's heads and head_dim")
     slots_p = _vector(slots, _I32, "slots", index, total)
     pos_p, pos_dim, table_p, pairs = _rope_args(pos, table, total, index)
+    _sizes(total | Hkv | d | pos_dim | pairs | cache_p[4] | cache_p[5])
     workspace = _workspace(workspace, 1024, index, stream)
     _call(load_library().tsel_cache_write, index, stream, k.data_ptr(), ks, v.data_ptr(), vs, pos_p,
           pos_dim, table_p, pairs, slots_p, total, Hkv, d, _DTYPES[dtype], flags, *cache_p,
@@ -809,6 +818,7 @@ def tsel_cache_read(cache: TselCache, slots: torch.Tensor, *, dtype=torch.bfloat
     if dtype not in _DTYPES:
         raise TypeError("dtype must be bf16, fp16 or fp32")
     shape = (slots.numel(), Hkv, d)
+    _sizes(shape[0] | Hkv | d | cache_p[4] | cache_p[5])
     kos = 0 if k_out is None else _rows(k_out, "k_out", index, dtype, shape)
     vos = 0 if v_out is None else _rows(v_out, "v_out", index, dtype, shape)
     if k_out is not None or v_out is not None:
@@ -831,9 +841,10 @@ def tsel_cache_read(cache: TselCache, slots: torch.Tensor, *, dtype=torch.bfloat
 def tsel_prefix_attention_workspace_size(num_req: int, total_q: int, max_seqlen_q: int,
                                          num_heads: int, num_kv_heads: int, head_dim: int,
                                          max_prefix_len: int, max_suffix_len: int) -> int:
-    return int(load_library().tsel_prefix_attention_workspace_size(
-        int(num_req), int(total_q), int(max_seqlen_q), int(num_heads), int(num_kv_heads),
-        int(head_dim), int(max_prefix_len), int(max_suffix_len)))
+    sizes = [int(n) for n in (num_req, total_q, max_seqlen_q, num_heads, num_kv_heads, head_dim, max_prefix_len, max_suffix_len)]
+    if any(n >> 31 for n in sizes):   # negative, or more than a C int holds
+        return 0
+    return int(load_library().tsel_prefix_attention_workspace_size(*sizes))
 
 
 def tsel_prefix_attention(q: torch.Tensor, cu_seqlens_q: torch.Tensor, max_seqlen_q: int,
@@ -866,7 +877,8 @@ def tsel_prefix_attention(q: torch.Tensor, cu_seqlens_q: torch.Tensor, max_seqle
     R = cu_seqlens_q.numel() - 1
     if R < 0:
         raise ValueError("cu_seqlens_q must have at least one entry")
-    max_p, max_s = int(max_prefix_len), int(max_suffix_len)
+    max_q, max_p, max_s = int(max_seqlen_q), int(max_prefix_len), int(max_suffix_len)
+    _sizes(tq | H | Hkv | d | R | max_q | max_p | max_s | cache_p[4] | page_size)
     prefix_p = len_p = table_p = suffix_p = None
     if max_p > 0:
         if prefix_pages is None or prefix_len is None:
@@ -899,14 +911,14 @@ def tsel_prefix_attention(q: torch.Tensor, cu_seqlens_q: torch.Tensor, max_seqle
     if out is not None or lse is not None:
         _written(out, lse)
     nbytes = 0 if workspace is not None else tsel_prefix_attention_workspace_size(
-        R, tq, max_seqlen_q, H, Hkv, d, max_p, max_s)
+        R, tq, max_q, H, Hkv, d, max_p, max_s)
     workspace = _workspace(workspace, nbytes, index, stream)
     if out is None:
         out = _like(q, stream)
     if lse is None and want_lse:
         lse = _new(stream, torch.empty, (H, tq), dtype=_F32, device=q.device)
     _call(load_library().tsel_prefix_attention, index, stream, q.data_ptr(), qs, cu_p, R, tq,
-          max_seqlen_q, *cache_p, prefix_p, len_p, max_p, table_p, table_stride, suffix_p, max_s, H, Hkv, d,
+          max_q, *cache_p, prefix_p, len_p, max_p, table_p, table_stride, suffix_p, max_s, H, Hkv, d,
           _DTYPES[dtype], softmax_scale, out.data_ptr(), os_, _ptr(lse), workspace.data_ptr(),
           workspace.numel())
     return out, lse

@@ -348,3 +348,34 @@ def test_binding_refuses_to_write_outputs_that_require_gradients(tsel):
                  lambda: tsel.tsel_prefix_attention(q, *attend, lse=fake((4, 5), torch.float32, True))):
         with pytest.raises(ValueError, match="autograd records"):
             call()
+
+
+def test_binding_refuses_sizes_past_32_bits(tsel):
+    """A foreign call would take the low 32 bits of them and work on those rows only."""
+    bf, i32, far = torch.bfloat16, torch.int32, 2 ** 32 + 5
+    table, cache = _Fake((32,), torch.int64), _fake_cache(tsel)
+    q, cu = _Fake((5, 4, 64), bf), _Fake((3,), i32)
+    pp, pl, pt, sl = _Fake((2 ** 29,), i32), _Fake((1,), i32), _Fake((2, 2 ** 29), i32), _Fake((2,), i32)
+    ws = _Fake((1 << 20,), torch.uint8)
+    for call in (lambda: tsel.tsel_rope(_Fake((far, 1, 64), bf), None, _Fake((far, 2), i32), table, workspace=ws),
+                 lambda: tsel.tsel_rope(_Fake((2 ** 31, 1, 64), bf), None, _Fake((2 ** 31, 2), i32), table, workspace=ws),
+                 lambda: tsel.tsel_rope(_Fake((1, far, 64), bf), None, _Fake((1, 2), i32), table, workspace=ws),
+                 lambda: tsel.tsel_rope(q, _Fake((5, far, 64), bf), _Fake((5, 2), i32), table, workspace=ws),
+                 lambda: tsel.tsel_rope(q, None, _Fake((5, far), i32), table, workspace=ws),
+                 lambda: tsel.tsel_rope(q, None, _Fake((5, 2), i32), _Fake((2 ** 32,), torch.int64), workspace=ws),
+                 lambda: tsel.tsel_cache_write(*[_Fake((far, 2, 64), bf)] * 2, _Fake((far,), i32), cache, workspace=ws),
+                 lambda: tsel.tsel_cache_write(*[_Fake((1, 2, 64), bf)] * 2, _Fake((1,), i32), _fake_cache(tsel, pages=far), workspace=ws),
+                 lambda: tsel.tsel_cache_read(cache, _Fake((far,), i32), workspace=ws),
+                 lambda: tsel.tsel_prefix_attention(_Fake((far, 4, 64), bf), cu, 3, cache, pp, pl, 100, pt, sl, 50, workspace=ws),
+                 lambda: tsel.tsel_prefix_attention(q, cu, 2 ** 32, cache, pp, pl, 100, pt, sl, 50, workspace=ws),
+                 lambda: tsel.tsel_prefix_attention(q, cu, 2 ** 32 + 3, cache, pp, pl, 100, pt, sl, 50, workspace=ws),
+                 lambda: tsel.tsel_prefix_attention(q, cu, -1, cache, pp, pl, 100, pt, sl, 50, workspace=ws),
+                 lambda: tsel.tsel_prefix_attention(q, cu, 3, cache, pp, pl, far, pt, sl, 50, workspace=ws),
+                 lambda: tsel.tsel_prefix_attention(q, cu, 3, cache, pp, pl, 100, pt, sl, far, workspace=ws)):
+        with pytest.raises(ValueError, match="past 2"):
+            call()
+    size = tsel.tsel_prefix_attention_workspace_size
+    ok = [1, 4, 4, 4, 2, 64, 10, 10]
+    assert size(*ok) > 0
+    for i in range(8):
+        assert size(*[n + 2 ** 32 if j == i else n for j, n in enumerate(ok)]) == 0
