@@ -644,6 +644,8 @@ def _workspace(workspace: Optional[torch.Tensor], nbytes: int, index: int, strea
         return _new(stream, _new_workspace, nbytes, device=torch.device("cuda", index))
     if workspace.get_device() != index:
         raise ValueError(f"workspace must be on cuda:{index}")
+    if not workspace.is_contiguous():   # its numel() would not be the bytes behind its pointer
+        raise ValueError("workspace must be contiguous")
     return workspace
 
 

@@ -379,3 +379,20 @@ def test_binding_refuses_sizes_past_32_bits(tsel):
     assert size(*ok) > 0
     for i in range(8):
         assert size(*[n + 2 ** 32 if j == i else n for j, n in enumerate(ok)]) == 0
+
+
+def test_binding_refuses_expanded_and_strided_workspaces(tsel):
+    """An expanded workspace has fewer bytes behind its pointer than entries."""
+    bf, i32 = torch.bfloat16, torch.int32
+    q, k, pos, table, slots = _Fake((5, 4, 64), bf), _Fake((5, 2, 64), bf), _Fake((5, 3), i32), _Fake((32,), torch.int64), _Fake((5,), i32)
+    cache = _fake_cache(tsel)
+    q.requires_grad = k.requires_grad = False
+    for stride in (0, 2):
+        ws = _Fake((1 << 20,), torch.uint8, strides=(stride,))
+        for call in (lambda: tsel.tsel_rope(q, k, pos, table, workspace=ws),
+                     lambda: tsel.tsel_cache_write(k, k, slots, cache, workspace=ws),
+                     lambda: tsel.tsel_cache_read(cache, slots, workspace=ws),
+                     lambda: tsel.tsel_prefix_attention(q, _Fake((3,), i32), 3, cache, _Fake((7,), i32), _Fake((1,), i32), 100,
+                                                        None, None, 0, workspace=ws)):
+            with pytest.raises(ValueError, match="workspace must be contiguous"):
+                call()
