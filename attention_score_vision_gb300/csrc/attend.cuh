@@ -92,6 +92,10 @@ inline AttPart att_part(int64_t requests, int tokens, int max_keys, int Hkv, int
   const int tiles = int(ceil_div(max_keys, kTile));
   const int64_t base = requests * Hkv * a.groups;
   if (base < 1 || tiles < 1) return a;
+  if (base > 0x7FFFFFFFll) {   // too large in any number of chunks, and base * chunks could pass 63 bits
+    a.units = base;
+    return a;
+  }
   a.chunks = a.narrow ? att_chunks(base, tiles, a.narrow == 1 ? kAttNarrowCtas1 : kAttNarrowCtas2, true, 1)
                       : att_chunks(base, tiles, kAttWideCtas, false, int(ceil_div(tiles, kAttMaxChunkKeys / kTile)));
   a.keys = int(ceil_div(tiles, a.chunks)) * kTile;

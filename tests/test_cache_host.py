@@ -396,3 +396,13 @@ def test_binding_refuses_expanded_and_strided_workspaces(tsel):
                                                         None, None, 0, workspace=ws)):
             with pytest.raises(ValueError, match="workspace must be contiguous"):
                 call()
+
+
+def test_attention_unit_counts_past_64_bits(tsel, lib):
+    """Sizes whose units, times their chunks, wrap around 64 bits are too large, not small."""
+    size, far = tsel.tsel_prefix_attention_workspace_size, 2 ** 31 - 1
+    for bad in ((far, 1, far, 256, 2, 64, 0, 2 ** 30), (2 ** 30, 1, far, 256, 256, 64, 0, 2 ** 30), (far, 1, far, 256, 256, 64, 0, 1024),
+                (2 ** 30, 4, 2 ** 30, 128, 1, 64, 64, 2 ** 20)):
+        assert size(*bad) == 0
+        R, tq, mq, H, Hkv, d, mp, ms = bad
+        assert _attend(lib, R=R, tq=tq, mq=mq, H=H, Hkv=Hkv, d=d, mp=mp, ms=ms, pts=2 ** 27, wsb=2 ** 40) == 2
