@@ -344,3 +344,46 @@ def test_hist_start_nan_scores(tsel):
     clean = np.where(np.isnan(s), np.float32(-1.0), s).astype(np.float32)
     ref, _ = oracle.select_topk(clean, [0, n], [rest.size])
     assert np.array_equal(rest, ref)
+
+
+@pytest.mark.parametrize("name", ["six_views_1536", "batch_8x16x1024"])
+def test_budgets_written_right_before_the_call_are_the_ones_used(tsel, name):
+    """Budgets that change on the device from call to call, with no pause between:
+    every call selects by its own, eager and from one graph."""
+    w = W.make(name)
+    dev = to_device(w)
+    R = w.keep_per_req.size
+    sizes = np.diff(w.req_tok_offsets)
+    budgets = [i32((sizes * f).astype(np.int32)) for f in (0.25, 0.9, 0.1, 0.6, 1.0, 0.33)]
+    keep = torch.zeros(R, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(tsel.tsel_score_select_workspace_size(w.num_seg, w.total_q, w.total_k, w.num_heads, R),
+                     dtype=torch.uint8, device="cuda")
+    scores = torch.empty(w.total_k, device="cuda")
+    idx = torch.empty((len(budgets), w.total_k), dtype=torch.int32, device="cuda")
+    cu = torch.empty((len(budgets), R + 1), dtype=torch.int32, device="cuda")
+
+    def run():
+        for i, b in enumerate(budgets):
+            keep.copy_(b)
+            tsel.tsel_score_select(dev["q"], dev["k"], dev["cu_q"], dev["cu_k"], w.max_seqlen_q, w.max_seqlen_k, dev["req_off"],
+                                   keep, tsel.TSEL_KEEP_FROM_DEVICE, flags=tsel.TSEL_IMP_TWO_PASS, want_lse=False, scores=scores,
+                                   keep_idx=idx[i], cu_keep=cu[i], workspace=ws)
+
+    def check():
+        torch.cuda.synchronize()
+        assert tsel.tsel_read_device_status(ws) == 0
+        s = scores.cpu().numpy()
+        for i, b in enumerate(budgets):
+            k_ref, cu_ref = oracle.select_topk(s, w.req_tok_offsets, b.cpu().numpy())
+            assert np.array_equal(cu[i].cpu().numpy(), cu_ref)
+            assert np.array_equal(idx[i, :cu_ref[-1]].cpu().numpy(), k_ref)
+
+    run()
+    check()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        run()
+    idx.zero_()
+    cu.zero_()
+    g.replay()
+    check()
