@@ -649,16 +649,21 @@ def _workspace(workspace: Optional[torch.Tensor], nbytes: int, index: int, strea
     return workspace
 
 
+def _int32s(values: list, name: str) -> list:
+    if any(not -2 ** 31 <= x < 2 ** 31 for x in values):   # ctypes keeps the low 32 bits
+        raise ValueError(f"{name} past 32 bits")
+    return values
+
+
 def tsel_rope_frequencies(base: float, sections: Sequence[int],
                           layout: int = TSEL_ROPE_SECTIONED) -> Tuple[list, list]:
     """Frequencies (radians per position step) and axes of the rotated pairs, axis a
     having sections[a] of them; see tsel_rope_frequencies in include/tsel.h."""
-    n = len(sections)
-    pairs = max(sum(max(int(x), 0) for x in sections), 1)
-    sec = (ctypes.c_int32 * max(n, 1))(*[int(x) for x in sections])
-    freq, axis = (ctypes.c_double * pairs)(), (ctypes.c_int32 * pairs)()
+    sections = [int(x) for x in sections]
+    n, total = len(sections), sum(sections)
+    sec = (ctypes.c_int32 * max(n, 1))(*_int32s(sections, "sections"))
+    freq, axis = (ctypes.c_double * 128)(), (ctypes.c_int32 * 128)()   # the library takes no more pairs
     _check(load_library().tsel_rope_frequencies(float(base), sec, n, int(layout), freq, axis))
-    total = sum(int(x) for x in sections)
     return list(freq)[:total], list(axis)[:total]
 
 
@@ -669,7 +674,7 @@ def tsel_rope_table(inv_freq: Sequence[float], axis: Sequence[int], device="cuda
     if len(axis) != n:
         raise ValueError("inv_freq and axis must have the same length")
     freq = (ctypes.c_double * max(n, 1))(*[float(x) for x in inv_freq])
-    ax = (ctypes.c_int32 * max(n, 1))(*[int(x) for x in axis])
+    ax = (ctypes.c_int32 * max(n, 1))(*_int32s([int(x) for x in axis], "axis"))
     table = torch.empty(n, dtype=torch.int64)
     _check(load_library().tsel_rope_table(freq, ax, n, _ptr(table) if n else None))
     return table.to(device)

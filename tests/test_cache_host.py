@@ -406,3 +406,17 @@ def test_attention_unit_counts_past_64_bits(tsel, lib):
         assert size(*bad) == 0
         R, tq, mq, H, Hkv, d, mp, ms = bad
         assert _attend(lib, R=R, tq=tq, mq=mq, H=H, Hkv=Hkv, d=d, mp=mp, ms=ms, pts=2 ** 27, wsb=2 ** 40) == 2
+
+
+def test_rope_host_helpers_refuse_numbers_past_32_bits(tsel):
+    """... whose low 32 bits would be a valid section or axis; and no buffer grows with a refused section."""
+    for sections in ([2 ** 32 + 4, 4], [2 ** 31, 4], [-2 ** 32 + 4]):
+        with pytest.raises(ValueError, match="sections past 32 bits"):
+            tsel.tsel_rope_frequencies(1e4, sections)
+    with pytest.raises(tsel.TselError):
+        tsel.tsel_rope_frequencies(1e4, [2 ** 31 - 1])
+    for axis in (2 ** 32, 2 ** 32 + 1, -2 ** 32):
+        with pytest.raises(ValueError, match="axis past 32 bits"):
+            tsel.tsel_rope_table([1.0], [axis], device="cpu")
+    f, a = tsel.tsel_rope_frequencies(1e4, [128])
+    assert len(f) == len(a) == 128
