@@ -28,7 +28,7 @@
 //     product of one half tile while the softmax is at the other. The whole warp
 //     runs that code and one elected lane issues: with the loop inside a branch
 //     on one lane, an instruction took 70 to 100 clocks, and the issuer, not the
-//     tensor cores, set the pace (483 us for the question prefills below, 413).
+//     tensor cores, set the pace (483 us for the question prefills below, 413 then).
 //   - eight softmax warps per pipeline, two threads to a row, 32 columns each:
 //     P = 2^(S c - m + 6) in fp16 lies over its S in TMEM and is the A operand of
 //     the second product. The reference m may lag the row's maximum by 2^9; past
@@ -44,12 +44,14 @@
 // What bounds it: per 256 x 128 logits the tensor cores need about 2,050 clocks
 // and the instructions (8,000 of the warps, half of them the exponentials and
 // what feeds them) 2,000 of each scheduler; a pass takes about 4,600, the rest
-// is the chain S product, softmax, O product of each pipeline, which TMEM (512
-// columns: S and O of two pipelines) leaves one half tile deep. Schedulers issue
-// in 66% of the cycles, the tensor pipe is busy in 45%. 16 question prefills of
-// up to 142 tokens over 36,831 keys (16 heads on 8 of 128): 362 us of 387 with
-// the join, 0.95 PFLOP/s, 49% of cuBLAS's bf16 rate; 256 rows over the same keys
-// (a step of 64 users): 47 us of 76.
+// is the chain S product, softmax, O product of each pipeline: P lies over its S,
+// so the next S product into those columns waits for the O product that reads
+// them. (P takes half the columns of its S; one S and two compact P would fit and
+// free the S product of that wait. Not built.) Schedulers issue in 66% of the
+// cycles, the tensor pipe is busy in 45%. 16 question prefills of up to 142 tokens
+// over 36,831 keys (16 heads on 8 of 128): 366 us of 390 with the join, 0.94
+// PFLOP/s, 49% of cuBLAS's bf16 rate; 256 rows over the same keys (a step of 64
+// users): 47 us of 79.
 // Tried and slower: one row per thread with more registers (setmaxnreg; 515 us),
 // P in shared memory (472 to 534), one pipeline with two whole S tiles (535: each
 // key tile is then converted for 128 rows instead of 256), whole key tiles

@@ -25,7 +25,9 @@ constexpr int kAttNarrowCtas1 = 4 * 152, kAttNarrowCtas2 = 3 * 152;
 // 32 rows over one prefix of 600 keys 11.8 and 13.3 us, of 2,000 15.8 and 17.8,
 // of 5,000 18.8 and 17.7, of 12,000 25.0 and 25.4, of 36,831 53.5 and 43.2; 64
 // requests of 32 rows with up to 800 keys 42.7 and 59.3, with 3,000 102 and 148;
-// 64 rows over 2,000 keys 19.4 and 21.8, over 36,831 75.9 and 47.8.
+// 64 rows over 2,000 keys 19.4 and 21.8, over 36,831 75.9 and 47.8. The rule goes
+// by rows: past 32 it gives away the 2 us of a short prefix for the 28 of a long
+// one. The rows of a suffix are bounded by the longest request of the batch.
 constexpr int kAttNarrowRows = 32;
 constexpr int kAttNarrowRowsLong = 16;         // past
 constexpr int kAttNarrowKeys = 16384;          // this many keys of few requests
@@ -171,10 +173,12 @@ struct AttUnit {
 };
 
 // `per`: rows of a row group; the keys of a suffix unit end where its last row sees no further.
-// U, the type that the unit number is divided in, only changes what the compiler
-// makes of the rest: uint32_t in the wide kernel (16 question prefills: 387 us,
-// 436 with int64_t), int64_t in the narrow one (four users of a six-view
-// request: 8.6 us, 10.4 with uint32_t).
+// U is the type that the unit number is divided in. Both give the same numbers;
+// what differs is the code that nvcc 13.0 makes of the kernels around them, by no
+// rule known here, so each kernel has the one that measures better with it:
+// uint32_t the wide one (16 question prefills 390 us, 438 with int64_t), int64_t
+// the narrow one (four users of a six-view request 7.9 us, 9.6 with uint32_t;
+// other cases within 1%). To be measured again with another compiler.
 template <typename U>
 __device__ __forceinline__ AttUnit att_unit(const AttParams& p, U u, int per) {
   AttUnit w{};

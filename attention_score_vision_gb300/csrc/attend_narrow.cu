@@ -19,12 +19,14 @@
 //     and converts them in registers: codes go from the cache to the tensor
 //     cores without a transposition or a store. P turns from accumulator to
 //     operand with one movmatrix per eight keys.
-//   - A key's scales multiply S (K) and P (V, relative to the largest exponent
-//     so far, so that P stays inside fp16).
+//   - A key's scales multiply S (K, together with the query's) and P (V, relative
+//     to the largest exponent so far, so that P stays inside fp16: the product is
+//     rounded to fp16, so it keeps eleven bits while probability times relative
+//     scale is at least 2^-20 of the row's reference, and ends at 2^-30 of it).
 // Bound by the latency of each warp's instructions (about 230 for a block of
 // 4 KB) times the 16 warps that fit an SM's registers, before HBM: 64 requests
 // with up to 4,000 keys on 8 KV heads of 128 (253 MB) take 62 us, 4.1 TB/s or
-// 60% of the copy rate, with the schedulers issuing in 39% of the cycles; up to
+// 60% of the copy rate, with the schedulers issuing in 41% of the cycles; up to
 // 1,000 keys 24 us. Five or six CTAs per SM with two stages cost spills (69, 86
 // us); two stages with four CTAs are as fast as three; blocks of 32 keys, two
 // products interleaved and three CTAs, are slower (65.6 against 63.9 us from a

@@ -22,10 +22,11 @@
 // is quantised from the fp32 rotation, without a rounding in between.
 //
 // 36,831 tokens on 8 KV heads of 128, bf16 (227 MB): write 42 us, 5.4 TB/s or 79%
-// of the copy rate, read 40 us, 84%; 131,072 tokens rotated, written and read
-// back (1.6 GB): 303 us, 79% (the rotated write 172: its schedulers issue in 71% of
-// the cycles, for angles, addresses and conversions); 200 tokens written 2.7 us,
-// 142 read 2.4 us.
+// of the copy rate, read 39 us, 85%; 131,072 tokens rotated, written and read
+// back (1.6 GB): 302 us, 79% (the rotated write 175, 4.5 TB/s or 66%: schedulers
+// issue in 70% of the cycles, the ALU pipe is busy in 63%, and the largest stall
+// is the wait for a token's rows, which 30 resident warps with eight rows in
+// flight each do not cover); 200 tokens written 2.3 us, 142 read 2.1 us.
 #include "launch_util.cuh"
 #include "rope.cuh"
 

@@ -15,9 +15,9 @@
 // that go round the lanes, so no lane idles whatever the head dimension, up to
 // three pieces loaded before the first is stored.
 //
-// 61,385 tokens, 16 + 16 heads of 80, bf16 (629 MB): 111 us, 5.7 TB/s, 84% of
+// 61,385 tokens, 16 + 16 heads of 80, bf16 (629 MB): 110 us, 5.7 TB/s, 84% of
 // the copy rate (one row per group of lanes: 227 us); 16,384 tokens, 16 + 8 heads
-// of 128, fp32, turned back (403 MB): 72 us, 82%; 64 tokens: 2.7 us.
+// of 128, fp32, turned back (403 MB): 71 us, 83%; 64 tokens: 2.5 us.
 #include "launch_util.cuh"
 #include "rope.cuh"
 
