@@ -776,6 +776,15 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
 // columns. Chunks without visible keys have lse = -inf and wrote no columns.
 constexpr int kJoinWarps = 8;
 
+// What is left of a partial too far below the row's largest, its weight 0: its
+// NaN, but no number and no infinity (a mean past fp32's range).
+__device__ __forceinline__ void keep_nan(float4& acc, const float4& o) {
+  if (o.x != o.x) acc.x = o.x;
+  if (o.y != o.y) acc.y = o.y;
+  if (o.z != o.z) acc.z = o.z;
+  if (o.w != o.w) acc.w = o.w;
+}
+
 template <int D, int WPR>
 __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const AttParams p) {
   __shared__ float s_acc[WPR > 1 ? kJoinWarps : 1][D];
@@ -825,7 +834,11 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const AttP
                      : make_float4(0.f, 0.f, 0.f, 0.f);
         }
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {   // a weight of 0 (too far below the row's largest) drops numbers, but no NaN
+        for (int x = 0; x < 4; ++x) {
+          if (wv[x] == 0.f) {
+            keep_nan(acc, o[x]);
+            continue;
+          }
           sum += wv[x];
           acc.x += wv[x] * o[x].x;
           acc.y += wv[x] * o[x].y;
@@ -854,6 +867,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const AttP
         // a warp whose partials are all NaN has no maximum, but a NaN sum
         const float f = s_m[warp + x] == kNegInf ? (s_sum[warp + x] == 0.f ? 0.f : 1.f) : exp2f(s_m[warp + x] - m);
         const float4 v = *reinterpret_cast<const float4*>(&s_acc[warp + x][4 * lane]);
+        if (f == 0.f) {
+          keep_nan(acc, v);
+          continue;
+        }
         sum += f * s_sum[warp + x];
         acc.x += f * v.x;
         acc.y += f * v.y;

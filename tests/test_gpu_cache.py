@@ -1186,3 +1186,23 @@ def test_attention_row_counts_past_their_bound_are_flagged(tsel):
     assert status(i32([0, 0, 0]), 0, cache, pp, pl, mp, pt, sl, ms) == 0
     assert status(cu, 2, cache, pp, pl, mp, None, None, 0) == 0
     assert status(i32([0]), 0, cache, pp, pl, mp, None, None, 0) == 0
+
+
+@pytest.mark.parametrize("rows,prefix", [([1], 9000), ([1], 300), ([90], 9000)])
+def test_attention_mean_past_fp32_under_far_larger_logits(tsel, rows, prefix):
+    """V values that E4M3 rounds up to 2^128, in a chunk whose weight is 0: nothing
+    of them is left, where 0 times the chunk's infinite mean would be NaN."""
+    def high(k):
+        k[prefix - 1] = 40.0
+        k[:prefix - 1] = np.minimum(k[:prefix - 1], 1.0)
+
+    def huge(v):
+        v[:20, 0, 7] = float(torch.finfo(BF).max)
+
+    b = Batch(tsel, 74, rows, [n + 5 for n in rows], prefix, 4, 2, 64, 16, BF, spread=0, k_rows=high, v_rows=huge)
+    b.q = b.q.abs() + 0.25
+    assert np.nanmax(b.v) == 2.0 ** 128
+    out, lse = b.run()
+    assert torch.isfinite(out).all()
+    b.v[b.v > 1e30] = 0.0                      # their weight is e^-250: 2^-233 of an ordinary value
+    b.check(out, lse)
