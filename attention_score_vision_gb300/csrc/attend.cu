@@ -867,7 +867,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const AttP
         // a warp whose partials are all NaN has no maximum, but a NaN sum
         const float f = s_m[warp + x] == kNegInf ? (s_sum[warp + x] == 0.f ? 0.f : 1.f) : exp2f(s_m[warp + x] - m);
         const float4 v = *reinterpret_cast<const float4*>(&s_acc[warp + x][4 * lane]);
-        if (f == 0.f) {
+        if (f == 0.f) {   // this warp's NaN partials among lower ones: also in its sum
+          if (s_sum[warp + x] != s_sum[warp + x]) sum = s_sum[warp + x];
           keep_nan(acc, v);
           continue;
         }

@@ -1206,3 +1206,21 @@ def test_attention_mean_past_fp32_under_far_larger_logits(tsel, rows, prefix):
     assert torch.isfinite(out).all()
     b.v[b.v > 1e30] = 0.0                      # their weight is e^-250: 2^-233 of an ordinary value
     b.check(out, lse)
+
+
+@pytest.mark.parametrize("rows,prefix", [([1], 9000), ([2] * 20, 9000), ([90], 9000), ([1], 200)])
+def test_attention_nan_key_among_keys_far_below(tsel, rows, prefix):
+    """A NaN K row makes NaN of the log-sum-exp too, also where the partial results
+    around it are far below others (eight, two and one warps to a row of the join)."""
+    def high(k):
+        k[prefix // 2] = 40.0
+        k[:prefix // 2] = np.minimum(k[:prefix // 2], 1.0)
+        k[prefix // 2 + 1:] = np.minimum(k[prefix // 2 + 1:], 1.0)
+        k[nan_at, 1, 9] = np.nan
+
+    for nan_at in (0, prefix // 3, prefix - 1):
+        b = Batch(tsel, 75, rows, [n + 5 for n in rows], prefix, 4, 2, 64, 16, BF, spread=0, k_rows=high)
+        b.q = b.q.abs() + 0.25
+        out, lse = b.run()
+        assert torch.isnan(out[:, 2:]).all() and torch.isnan(lse[2:]).all()
+        assert torch.isfinite(out[:, :2]).all() and torch.isfinite(lse[:2]).all()
