@@ -30,6 +30,7 @@ __all__ = [
     "tsel_rope_frequencies", "tsel_rope_table", "tsel_rope",
     "TselCache", "tsel_cache_new", "tsel_cache_workspace_size", "tsel_cache_write", "tsel_cache_read",
     "tsel_prefix_attention_workspace_size", "tsel_prefix_attention",
+    "tsel_prompt_attention_workspace_size", "tsel_prompt_attention", "TSEL_ATT_CAUSAL",
     "TSEL_ROPE_ADJACENT", "TSEL_ROPE_INVERSE", "TSEL_ROPE_SECTIONED", "TSEL_ROPE_INTERLEAVED", "TSEL_ROPE_PER_AXIS",
     "TSEL_DEV_SEQLENS", "TSEL_DEV_REQUESTS", "TSEL_DEV_KEEP_IDX", "TSEL_DEV_TIMEOUT", "TSEL_DEV_NAN",
     "TSEL_DEV_PAGES", "TSEL_DEV_POSITIONS",
@@ -70,6 +71,8 @@ TSEL_ROPE_INVERSE = 0x2
 TSEL_ROPE_SECTIONED = 0
 TSEL_ROPE_INTERLEAVED = 1
 TSEL_ROPE_PER_AXIS = 2
+
+TSEL_ATT_CAUSAL = 0x1
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}   # TSEL_BF16, _FP16, _FP32
 
@@ -125,6 +128,10 @@ _SIGNATURES = {
     "tsel_prefix_attention": (_c_int, [_p, _c_i64, _p, _c_int, _c_int, _c_int, _p, _p, _p, _p,
                                        _c_int, _c_int, _p, _p, _c_int, _p, _c_i64, _p, _c_int,
                                        _c_int, _c_int, _c_int, _c_int, _c_float, _p, _c_i64, _p,
+                                       _p, _c_size, _p]),
+    "tsel_prompt_attention_workspace_size": (_c_size, [_c_int] * 7),
+    "tsel_prompt_attention": (_c_int, [_p, _c_i64, _p, _c_i64, _p, _c_i64, _p, _p, _c_int, _c_int, _c_int, _c_int,
+                                       _c_int, _c_int, _c_int, _c_int, _c_int, _c_float, _c_uint, _p, _c_i64, _p,
                                        _p, _c_size, _p]),
 }
 
@@ -928,6 +935,67 @@ def tsel_prefix_attention(q: torch.Tensor, cu_seqlens_q: torch.Tensor, max_seqle
           max_q, *cache_p, prefix_p, len_p, max_p, table_p, table_stride, suffix_p, max_s, H, Hkv, d,
           _DTYPES[dtype], softmax_scale, out.data_ptr(), os_, _ptr(lse), workspace.data_ptr(),
           workspace.numel())
+    return out, lse
+
+
+# ---------------------------------------------------------------------------
+# Attention over whole prompts
+# ---------------------------------------------------------------------------
+
+def tsel_prompt_attention_workspace_size(num_seg: int, total_q: int, max_seqlen_q: int, max_seqlen_k: int,
+                                         num_heads: int, num_kv_heads: int, head_dim: int) -> int:
+    sizes = [int(n) for n in (num_seg, total_q, max_seqlen_q, max_seqlen_k, num_heads, num_kv_heads, head_dim)]
+    if any(n >> 31 for n in sizes):   # negative, or more than a C int holds
+        return 0
+    return int(load_library().tsel_prompt_attention_workspace_size(*sizes))
+
+
+def tsel_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                          cu_seqlens_k: torch.Tensor, max_seqlen_q: int, max_seqlen_k: int, *,
+                          softmax_scale: float = 0.0, flags: int = 0, out: Optional[torch.Tensor] = None,
+                          lse: Optional[torch.Tensor] = None, want_lse: bool = True,
+                          workspace: Optional[torch.Tensor] = None,
+                          stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Attention of packed sequences; returns (out [Tq, H, d], lse fp32 [H, Tq] or None).
+
+    q bf16 or fp16 [Tq, H, d], k and v [Tk, Hkv, d] (rows may be strided, e.g. views
+    of a packed QKV tensor); cu_seqlens_q and cu_seqlens_k int32 [G+1]. With
+    TSEL_ATT_CAUSAL in flags the last row of a segment sees all its keys and every
+    row before it one fewer. lse is what tsel_importance takes with
+    TSEL_IMP_LSE_PROVIDED. Rows past cu_seqlens_q[G] are left as they are in a given
+    out or lse. The results carry no gradients."""
+    shape, dtype, index = _first(q, "q")
+    if dtype is _F32:
+        raise TypeError("q must be bf16 or fp16")
+    qs = _rows(q, "q", index, dtype)
+    tq, H, d = shape
+    ks = _rows(k, "k", index, dtype)
+    k_shape = k.shape
+    if len(k_shape) != 3 or k_shape[2] != d:
+        raise ValueError("k does not match q's head_dim")
+    vs = _rows(v, "v", index, dtype, k_shape)
+    tk, Hkv, _ = k_shape
+    cu_q = _vector(cu_seqlens_q, _I32, "cu_seqlens_q", index)
+    n = cu_seqlens_q.numel()
+    if n < 1:
+        raise ValueError("cu_seqlens_q must have at least one entry")
+    cu_k = _vector(cu_seqlens_k, _I32, "cu_seqlens_k", index, n)
+    max_q, max_k = int(max_seqlen_q), int(max_seqlen_k)
+    _sizes(tq | tk | H | Hkv | d | max_q | max_k)
+    os_ = 0 if out is None else _rows(out, "out", index, dtype, shape)
+    if lse is not None:
+        _vector(lse, _F32, "lse", index, H * tq)
+    if out is not None or lse is not None:
+        _written(out, lse)
+    nbytes = 0 if workspace is not None else tsel_prompt_attention_workspace_size(n - 1, tq, max_q, max_k, H, Hkv, d)
+    workspace = _workspace(workspace, nbytes, index, stream)
+    if out is None:
+        out = _like(q, stream)
+    if lse is None and want_lse:
+        lse = _new(stream, torch.empty, (H, tq), dtype=_F32, device=q.device)
+    _call(load_library().tsel_prompt_attention, index, stream, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+          cu_q, cu_k, n - 1, tq, tk, max_q, max_k, H, Hkv, d, _DTYPES[dtype], softmax_scale, flags, out.data_ptr(),
+          os_, _ptr(lse), workspace.data_ptr(), workspace.numel())
     return out, lse
 
 

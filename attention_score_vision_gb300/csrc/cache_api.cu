@@ -1,7 +1,7 @@
 // Host side of the cache entry points of include/tsel.h (rotary positions,
-// the quantised paged cache, attention over a shared prefix): argument checks,
-// the rope table, workspace carving and kernel launches. Nothing here
-// allocates or synchronises.
+// the quantised paged cache, attention over a shared prefix) and of attention
+// over whole prompts: argument checks, the rope table, workspace carving and
+// kernel launches. Nothing here allocates or synchronises.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -11,12 +11,15 @@
 
 #include "attend.cuh"
 #include "common.cuh"
+#include "prompt.cuh"
 #include "rope.cuh"
 
 namespace tsel {
 void record_error(const char* msg);
 int device_sms(int* out);
 uint64_t device_wait_timeout_ns();
+bool make_rows_map(CUtensorMap* map, const void* base, bool fp16, int head_dim, int heads, int64_t rows,
+                   int64_t row_stride_bytes, int box_heads, int box_rows);
 }  // namespace tsel
 
 using namespace tsel;
@@ -411,6 +414,120 @@ tsel_status tsel_prefix_attention(
     if (e != cudaSuccess) return cuda_fail(e, "attention launch");
   }
   e = launch_attend_join(head_dim, p, stream);
+  return e == cudaSuccess ? TSEL_OK : cuda_fail(e, "join launch");
+}
+
+size_t tsel_prompt_attention_workspace_size(int num_seg, int total_q, int max_seqlen_q, int max_seqlen_k,
+                                            int num_heads, int num_kv_heads, int head_dim) {
+  if (num_seg < 0 || total_q < 0 || max_seqlen_q < 0 || max_seqlen_k < 0 || num_kv_heads < 1 ||
+      num_heads < num_kv_heads || num_heads > 256 || num_heads % num_kv_heads != 0 ||
+      num_heads / num_kv_heads > kTile || !cache_head_dim(head_dim) || total_q > kAttMaxKeys ||
+      max_seqlen_k > kAttMaxKeys)
+    return 0;
+  const PromptPlan a = prompt_plan(num_seg, total_q, max_seqlen_k, num_heads, num_kv_heads, head_dim);
+  return a.too_large ? 0 : size_t(a.total);
+}
+
+tsel_status tsel_prompt_attention(const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride,
+                                  const void* v, int64_t v_row_stride, const int32_t* cu_seqlens_q,
+                                  const int32_t* cu_seqlens_k, int num_seg, int total_q, int total_k,
+                                  int max_seqlen_q, int max_seqlen_k, int num_heads, int num_kv_heads,
+                                  int head_dim, int dtype, float softmax_scale, unsigned flags, void* out,
+                                  int64_t out_row_stride, float* lse, void* workspace,
+                                  size_t workspace_bytes, void* stream_) {
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (dtype != TSEL_BF16 && dtype != TSEL_FP16)
+    return fail(TSEL_ERR_UNSUPPORTED, "dtype=%d (bf16 or fp16)", dtype);
+  if (num_seg < 0 || total_q < 0 || total_k < 0 || max_seqlen_q < 0 || max_seqlen_k < 0)
+    return fail(TSEL_ERR_INVALID_VALUE, "negative size");
+  if (num_heads < 1 || num_heads > 256 || num_kv_heads < 1 || num_heads % num_kv_heads != 0)
+    return fail(TSEL_ERR_INVALID_VALUE, "num_heads=%d num_kv_heads=%d", num_heads, num_kv_heads);
+  if (num_heads / num_kv_heads > kTile)
+    return fail(TSEL_ERR_UNSUPPORTED, "%d query heads per KV head (at most %d)",
+                num_heads / num_kv_heads, kTile);
+  if (!cache_head_dim(head_dim))
+    return fail(TSEL_ERR_UNSUPPORTED, "head_dim=%d (supported: 64, 80, 96, 112, 128)", head_dim);
+  if (total_q > kAttMaxKeys || total_k > kAttMaxKeys || max_seqlen_k > kAttMaxKeys)
+    return fail(TSEL_ERR_UNSUPPORTED, "more than %d rows or keys", kAttMaxKeys);
+  if (flags & ~TSEL_ATT_CAUSAL) return fail(TSEL_ERR_UNSUPPORTED, "flags=0x%x", flags);
+  if (!(softmax_scale == softmax_scale) || std::isinf(softmax_scale))
+    return fail(TSEL_ERR_INVALID_VALUE, "softmax_scale");
+  if (cu_seqlens_q == nullptr || cu_seqlens_k == nullptr || !aligned(cu_seqlens_q, 4) || !aligned(cu_seqlens_k, 4))
+    return fail(TSEL_ERR_INVALID_VALUE, "cu_seqlens_q or cu_seqlens_k");
+  if (lse != nullptr && !aligned(lse, 4)) return fail(TSEL_ERR_INVALID_VALUE, "lse misaligned");
+  TSEL_TRY(check_header(workspace, workspace_bytes));
+  const PromptPlan a = prompt_plan(num_seg, total_q, max_seqlen_k, num_heads, num_kv_heads, head_dim);
+  if (a.too_large) return fail(TSEL_ERR_UNSUPPORTED, "too many units of work");
+  if (workspace_bytes < size_t(a.total))
+    return fail(TSEL_ERR_WORKSPACE, "workspace %zu < %lld bytes", workspace_bytes, (long long)a.total);
+  if (total_q == 0) return TSEL_OK;
+  PromptParams p{};
+  int64_t q_stride = q_row_stride, k_stride = k_row_stride;
+  p.v_stride = v_row_stride;
+  p.out_stride = out_row_stride;
+  const int64_t width = int64_t(num_heads) * head_dim, kv_width = int64_t(num_kv_heads) * head_dim;
+  TSEL_TRY(check_rows("q", q, &q_stride, width, 2));
+  TSEL_TRY(check_rows("out", out, &p.out_stride, width, 2));
+  if (total_k > 0) {
+    TSEL_TRY(check_rows("k", k, &k_stride, kv_width, 2));
+    TSEL_TRY(check_rows("v", v, &p.v_stride, kv_width, 2));
+  }
+  const bool fp16 = dtype == TSEL_FP16;
+  CUtensorMap mq, mk, mv;
+  // without keys nothing is loaded through their maps: those of q will do
+  if (!make_rows_map(&mq, q, fp16, head_dim, num_heads, total_q, q_stride * 2, a.G, a.tt) ||
+      !make_rows_map(&mk, total_k > 0 ? k : q, fp16, head_dim, total_k > 0 ? num_kv_heads : num_heads,
+                     total_k > 0 ? total_k : total_q, (total_k > 0 ? k_stride : q_stride) * 2, 1, kPromptStep) ||
+      !make_rows_map(&mv, total_k > 0 ? v : q, fp16, head_dim, total_k > 0 ? num_kv_heads : num_heads,
+                     total_k > 0 ? total_k : total_q, (total_k > 0 ? p.v_stride : q_stride) * 2, 1, kPromptStep))
+    return fail(TSEL_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+  int sms = 0;
+  if (device_sms(&sms) != 0) return fail(TSEL_ERR_CUDA, "cannot query the SM count");
+  p.v = v;
+  p.cu_q = cu_seqlens_q;
+  p.cu_k = cu_seqlens_k;
+  p.seg = num_seg;
+  p.Tq = total_q;
+  p.Tk = total_k;
+  p.max_q = max_seqlen_q;
+  p.max_k = max_seqlen_k;
+  p.H = num_heads;
+  p.Hkv = num_kv_heads;
+  p.G = a.G;
+  p.tt = a.tt;
+  p.causal = (flags & TSEL_ATT_CAUSAL) ? 1 : 0;
+  p.chunks = a.chunks;
+  p.keys = a.keys;
+  const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt(float(head_dim));
+  p.c = std::fmax(scale * 1.4426950408889634f, 1e-38f);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (a.slots > 0) {
+    p.part_lse = reinterpret_cast<float*>(ws + a.lse_off);
+    p.part_o = reinterpret_cast<float*>(ws + a.o_off);
+  }
+  p.out = out;
+  p.lse = lse;
+  p.status = &reinterpret_cast<WsHeader*>(ws)->status;
+  p.timeout_ns = device_wait_timeout_ns();
+  const int ctas = int(a.units < sms ? a.units : sms);
+  cudaError_t e = launch_prompt(head_dim, fp16, mq, mk, mv, p, ctas, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "prompt attention launch");
+  if (a.slots == 0) return TSEL_OK;
+  AttParams j{};
+  j.cu_q = cu_seqlens_q;
+  j.R = num_seg;
+  j.Tq = total_q;
+  j.max_q = max_seqlen_q;
+  j.H = num_heads;
+  j.slots = a.slots;
+  j.part_lse = p.part_lse;
+  j.part_o = p.part_o;
+  j.out = out;
+  j.out_stride = p.out_stride;
+  j.fp16 = fp16 ? 1 : 0;
+  j.lse = lse;
+  j.status = p.status;
+  e = launch_attend_join(head_dim, j, stream);
   return e == cudaSuccess ? TSEL_OK : cuda_fail(e, "join launch");
 }
 

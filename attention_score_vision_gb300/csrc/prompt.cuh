@@ -1,0 +1,70 @@
+// Attention over whole prompts: sizes of the launch and parameters of its
+// kernel (prompt.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "attend.cuh"
+
+namespace tsel {
+
+constexpr int kPromptStep = 64;       // keys of a step
+constexpr int kPromptSorted = 256;    // segments up to which units go longest first
+
+struct PromptPlan {
+  int G, tt;           // query heads per KV head, tokens per 128-row tile
+  int chunks, keys;    // key chunks of a segment, keys of one (a multiple of 128)
+  int64_t units;       // upper bound
+  int slots;           // partial results of a row, 0: written at once
+  int64_t lse_off, o_off, total;   // workspace
+  bool too_large;
+};
+
+// Keys are cut into chunks only while the (segment, KV head, row block) units
+// leave SMs idle. `base` is a lower estimate of the units that have rows.
+inline PromptPlan prompt_plan(int seg, int Tq, int max_k, int H, int Hkv, int d) {
+  PromptPlan a{};
+  a.G = H / Hkv;
+  a.tt = kTile / a.G;
+  const int64_t blocks = ceil_div(Tq, 2 * a.tt);
+  const int64_t base = Hkv * (blocks > seg ? blocks : seg);
+  const int tiles = int(ceil_div(max_k, kTile));
+  a.chunks = 1;
+  if (base > 0 && base < kAttWideCtas && tiles > 1) a.chunks = att_chunks(base, tiles, kAttWideCtas, false, 1);
+  a.keys = a.chunks > 1 ? int(ceil_div(tiles, a.chunks)) * kTile : 0x7FFFFF80;
+  a.units = Hkv * (blocks + seg) * a.chunks;
+  a.slots = a.chunks > 1 ? a.chunks : 0;
+  a.too_large = double(a.slots) * Tq * H * d > 1e15 || a.units > (1ll << 40);
+  if (a.too_large) return a;
+  a.lse_off = kWsHeaderBytes;
+  a.o_off = align_up(a.lse_off + 4 * int64_t(a.slots) * Tq * H, 256);
+  a.total = align_up(a.o_off + 4 * int64_t(a.slots) * Tq * H * d, 256);
+  return a;
+}
+
+struct PromptParams {
+  const void* v;               // also read by threads where V holds infinities or NaN
+  int64_t v_stride;            // elements
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  int seg, Tq, Tk, max_q, max_k;
+  int H, Hkv, G, tt;
+  int causal;
+  int chunks, keys;
+  float c;                     // softmax_scale * log2(e)
+  float* part_lse;             // [chunks][Tq][H], base 2; null: results are written at once
+  float* part_o;               // [chunks][Tq][H][d]
+  void* out;
+  int64_t out_stride;
+  float* lse;                  // [H][Tq] natural log, or null
+  uint32_t* status;
+  uint64_t timeout_ns;
+};
+
+cudaError_t launch_prompt(int head_dim, bool fp16, const CUtensorMap& mq, const CUtensorMap& mk,
+                          const CUtensorMap& mv, const PromptParams& p, int ctas, cudaStream_t stream);
+
+}  // namespace tsel

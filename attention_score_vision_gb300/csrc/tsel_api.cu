@@ -166,6 +166,20 @@ void record_error(const char* msg) { g_last_error = msg; }
 // ... and size its launches and bound its waits as this one does.
 int device_sms(int* out) { return sm_count(out); }
 uint64_t device_wait_timeout_ns() { return wait_timeout_ns(); }
+// 3-D map over rows [rows, heads, head_dim] of 16-bit elements: boxes of 64
+// columns (past head_dim they read zeros) x box_heads x box_rows, 128-byte swizzle.
+bool make_rows_map(CUtensorMap* map, const void* base, bool fp16, int head_dim, int heads, int64_t rows,
+                   int64_t row_stride_bytes, int box_heads, int box_rows) {
+  auto enc = encode_fn();
+  if (enc == nullptr) return false;
+  cuuint64_t dims[3] = {cuuint64_t(head_dim), cuuint64_t(heads), cuuint64_t(rows)};
+  cuuint64_t strides[2] = {cuuint64_t(head_dim) * 2, cuuint64_t(row_stride_bytes)};
+  cuuint32_t box[3] = {64u, cuuint32_t(box_heads), cuuint32_t(box_rows)};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 }  // namespace tsel
 
 extern "C" {

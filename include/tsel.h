@@ -614,6 +614,65 @@ TSEL_API tsel_status tsel_prefix_attention(
     int64_t out_row_stride, float* lse, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Attention over whole prompts                                             */
+/* ------------------------------------------------------------------------ */
+
+/* tsel_prompt_attention flags */
+#define TSEL_ATT_CAUSAL 0x1u /* a row sees the keys up to its own place, counted from the ends */
+
+/* Bytes of workspace tsel_prompt_attention needs for these sizes (0 for sizes
+ * it does not take). */
+TSEL_API size_t tsel_prompt_attention_workspace_size(int num_seg, int total_q, int max_seqlen_q,
+                                                     int max_seqlen_k, int num_heads, int num_kv_heads,
+                                                     int head_dim);
+
+/*
+ * Attention of packed sequences, as a vision encoder (no mask) and a language
+ * model's prefill (causal) compute it ([LiteVLM] core formulas, softmax(Q K^T /
+ * sqrt d) V). Queries of segment g attend to the keys of segment g; with
+ * TSEL_ATT_CAUSAL query row i (of n) sees the first m - n + i + 1 of its m keys
+ * (none if that is not positive), so the last rows of a sequence may come after
+ * keys that are there already. With kvh(h) = h / (H / Hkv):
+ *   P[h,i,j] = exp(s * q_{i,h} . k_{j,kvh(h)} - lse[h,i]),
+ *   out[i,h] = sum_j P[h,i,j] v_{j,kvh(h)},   lse natural log,
+ * the LSE as tsel_importance takes it with TSEL_IMP_LSE_PROVIDED ([VTC] section
+ * 3.2: the LSE that the attention kernel produced). A row that sees no key
+ * gives out = 0 and lse = -inf.
+ *
+ * q             [total_q, num_heads, head_dim] of dtype (TSEL_BF16 or
+ *               TSEL_FP16); rows as in tsel_rope, e.g. views of a packed QKV
+ *               tensor. num_heads in [1, 256], num_kv_heads divides it, at most
+ *               128 query heads per KV head. head_dim 64, 80, 96, 112 or 128.
+ * k, v          [total_k, num_kv_heads, head_dim], the same.
+ * cu_seqlens_q, cu_seqlens_k  int32 [num_seg + 1] device: 0, monotone, lengths
+ *               at most max_seqlen_q / max_seqlen_k, the last at most total_q /
+ *               total_k. Rows from cu_seqlens_q[num_seg] on (padding of a captured
+ *               batch) are neither read for others nor written.
+ * total_q, total_k  at most 2^30.
+ * softmax_scale <= 0 selects 1/sqrt(head_dim).
+ * out           as q; may be q itself with the same stride. lse fp32
+ *               [num_heads, total_q] or NULL.
+ * workspace     >= tsel_prompt_attention_workspace_size(...): partial results of
+ *               the key chunks that few rows over many keys are cut into;
+ *               nothing in it outlives the call but the status word.
+ *
+ * Segments that break these bounds set TSEL_DEV_SEQLENS and their rows are left
+ * unspecified; nothing out of range is touched. Keys that a row does not see
+ * never reach it, infinities and NaN among them. An infinity or NaN in V makes
+ * the same of its column in the rows that see the key.
+ * Results are deterministic. Precision: products of the inputs as they are,
+ * probabilities rounded to dtype (relative to a reference at most 2^9 below the
+ * row's largest; fp16 below 2^-20 of it on a grid of 2^-30), sums and statistics
+ * in fp32.
+ */
+TSEL_API tsel_status tsel_prompt_attention(
+    const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride, const void* v,
+    int64_t v_row_stride, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k, int num_seg,
+    int total_q, int total_k, int max_seqlen_q, int max_seqlen_k, int num_heads, int num_kv_heads,
+    int head_dim, int dtype, float softmax_scale, unsigned flags, void* out, int64_t out_row_stride,
+    float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Host helpers                                                             */
 /* ------------------------------------------------------------------------ */
 
