@@ -89,7 +89,7 @@ struct AttTileMeta {
   uint32_t v_nan[4];   // keys whose V row is NaN, a bit each
 };
 
-template <int D>
+template <int D, bool TREE>
 struct AttCfg {
   static constexpr int DC = D > 64 ? 2 : 1;                 // 64-element chunks of a row
   static constexpr int TILE_BYTES = DC * kTile * 128;       // one 128-row fp16 operand
@@ -106,7 +106,8 @@ struct AttCfg {
   static constexpr int OFF_FAC = OFF_V + KS * TILE_BYTES;   // uint32 [K, V][tile parity][128]
   static constexpr int OFF_PAGES = OFF_FAC + 2 * 2 * kTile * 4;
   static constexpr int OFF_ROW = OFF_PAGES + kAttMaxPages * 4;   // fp32 [row tile][parity][half][128]
-  static constexpr int OFF_META = OFF_ROW + 2 * 2 * 2 * kTile * 4;
+  static constexpr int OFF_TREE = OFF_ROW + 2 * 2 * 2 * kTile * 4;   // uint64 [row tile][128]: ancestors
+  static constexpr int OFF_META = OFF_TREE + (TREE ? 2 * kTile * 8 : 0);
   static constexpr int NUM_BARS = 4 * KS + 3 * 4;
   static constexpr int OFF_BAR = OFF_META + kAttMetaRing * int(sizeof(AttTileMeta));
   static constexpr int OFF_MISC = OFF_BAR + 8 * NUM_BARS;
@@ -174,9 +175,18 @@ __device__ __forceinline__ void att_poison32(uint32_t (&h)[16], uint32_t nan, in
   }
 }
 
-template <int D>
-__global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const AttParams p) {
-  using C = AttCfg<D>;
+// The columns of 32 that a row sees where the tree's keys begin at column -s:
+// all of those before it, then its ancestors.
+__device__ __forceinline__ uint32_t att_seen32(uint64_t tree, int s) {
+  if (s >= 64) return 0u;
+  if (s >= 0) return uint32_t(tree >> s);
+  return s <= -32 ? 0xFFFFFFFFu : uint32_t(tree << -s) | ((1u << -s) - 1u);
+}
+
+// TREE: rows of a suffix are nodes of trees.
+template <int D, bool TREE>
+__global__ void __launch_bounds__(AttCfg<D, TREE>::THREADS, 1) attend_kernel(const AttParams p) {
+  using C = AttCfg<D, TREE>;
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = smem_dyn + ((1024u - (smem_u32(smem_dyn) & 1023u)) & 1023u);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
@@ -326,6 +336,11 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
             make_uint4(h[0], h[1], h[2], h[3]);
     }
     qc = p.c * __uint_as_float(uint32_t(row_exp(row) - 13) << 23);   // 2^(E - 140)
+    if (TREE && w.causal) {
+      const AttAncestors a = att_ancestors(p.parents + w.tok_first, w.tok_last - w.tok_first, p.status);
+      const uint64_t bits = att_bits(a, row_ok ? tok - w.tok_first : 0);
+      if (half == 0) reinterpret_cast<uint64_t*>(smem + C::OFF_TREE)[x * kTile + row] = row_ok ? bits : 0;
+    }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   if (threadIdx.x == 0) {
@@ -352,11 +367,14 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
       const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
       const uint32_t s_at = tmem + lanes + uint32_t(x * 256);   // O: 128 columns on
       const bool any_row = __any_sync(0xffffffffu, row_ok);
-      const int lim = w.causal ? w.lim0 + (tok - w.tok_first) : w.lim0;
+      // in a tree: where its keys begin
+      const int lim = TREE ? w.lim0 - w.causal : (w.causal ? w.lim0 + (tok - w.tok_first) : w.lim0);
       int end = (row_ok ? min(lim, w.k1) : 0) - w.k0;
       int min_end = int(__reduce_min_sync(0xffffffffu, row_ok ? max(end, 0) : 0x7FFFFFFF));   // of the warp's rows
       // What the loop needs of the row is computed here, once: left alone, the
       // compiler saves registers by dividing rows into tokens again for every tile.
+      int keys = w.k1 - w.k0;
+      if (TREE) opaque(keys);
       opaque(end);
       opaque(min_end);
       // the two warps of the same 32 rows meet at a barrier of their own
@@ -389,15 +407,25 @@ __global__ void __launch_bounds__(AttCfg<D>::THREADS, 1) attend_kernel(const Att
           tc_fence_after();
           const AttTileMeta& meta = s_meta[t & (kAttMetaRing - 1)];
           const int col = 64 * hh + 32 * half;        // first of this thread's columns of the tile
-          const int vis = end - t * kTile - col;      // visible ones: [0, vis)
+          int vis = end - t * kTile - col;            // visible ones: [0, vis)
           const bool full = t * kTile + col + 32 <= min_end;
           uint32_t r[32];
           tmem_ld32_async(s_at + col, r);
           const float ct = fmaxf(qc * meta.k_scale, 1e-38f);
           const int vnew = meta.v_ref;
-          const uint32_t nan_v = meta.v_nan[2 * hh + half];
+          uint32_t nan_v = meta.v_nan[2 * hh + half];
           tmem_wait_ld(r);
-          if (!full) mask_cols(r, vis);
+          if (TREE && !full && w.causal) {
+            const int last = keys - t * kTile - col;   // columns of the chunk
+            const uint32_t seen = att_seen32(reinterpret_cast<const uint64_t*>(smem + C::OFF_TREE)[x * kTile + row], -vis) &
+                                  (last >= 32 ? 0xFFFFFFFFu : last <= 0 ? 0u : (1u << last) - 1u);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) r[k] = (seen >> k) & 1u ? r[k] : __float_as_uint(kNegInf);
+            nan_v &= seen;
+            vis = 32;
+          } else if (!full) {
+            mask_cols(r, vis);
+          }
           float top = cols_max(r) * ct;
           // the two warps of the same rows go the same way
           if (meet_any(top > m + kAttSlack || vnew != vref)) {
@@ -818,10 +846,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const AttP
     p.lse[int64_t(head) * p.Tq + tok] = sum == 0.f ? kNegInf : (ref + log2f(sum)) * 0.69314718055994531f;
 }
 
-template <int D>
+template <int D, bool TREE>
 cudaError_t launch_attend_t(const AttParams& p, int64_t units, cudaStream_t stream) {
-  using C = AttCfg<D>;
-  auto kern = attend_kernel<D>;
+  using C = AttCfg<D, TREE>;
+  auto kern = attend_kernel<D, TREE>;
   static bool attr_set[128] = {};   // per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -837,14 +865,20 @@ cudaError_t launch_attend_t(const AttParams& p, int64_t units, cudaStream_t stre
 }  // namespace
 
 cudaError_t launch_attend(int head_dim, const AttParams& p, int64_t units, cudaStream_t stream) {
+  const bool tree = p.parents != nullptr && units > p.pre_units;
+#define TSEL_ATT_CASE(DD) \
+  case DD:                \
+    return tree ? launch_attend_t<DD, true>(p, units, stream) : launch_attend_t<DD, false>(p, units, stream);
   switch (head_dim) {
-    case 64: return launch_attend_t<64>(p, units, stream);
-    case 80: return launch_attend_t<80>(p, units, stream);
-    case 96: return launch_attend_t<96>(p, units, stream);
-    case 112: return launch_attend_t<112>(p, units, stream);
-    case 128: return launch_attend_t<128>(p, units, stream);
-    default: return cudaErrorInvalidValue;
+    TSEL_ATT_CASE(64)
+    TSEL_ATT_CASE(80)
+    TSEL_ATT_CASE(96)
+    TSEL_ATT_CASE(112)
+    TSEL_ATT_CASE(128)
+    default:
+      return cudaErrorInvalidValue;
   }
+#undef TSEL_ATT_CASE
 }
 
 namespace {

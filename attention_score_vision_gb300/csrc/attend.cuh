@@ -32,6 +32,7 @@ constexpr int kAttNarrowRows = 32;
 constexpr int kAttNarrowRowsLong = 16;         // past
 constexpr int kAttNarrowKeys = 16384;          // this many keys of few requests
 
+constexpr int kAttTreeNodes = 64;              // of a request: a row's ancestors are bits of one word
 constexpr int kAttJoinedTiles = 1024;          // 128-key tiles of suffixes that a prefix's narrow launch takes along
 
 // How the prefix, or the suffixes, are cut into units: (key chunk, KV head, row
@@ -145,6 +146,7 @@ struct AttParams {
   int64_t table_stride;
   const int32_t* suffix_lens;
   int max_suffix;
+  const int32_t* parents;      // [Tq] of the drafted tokens' trees, or null: one after another
   int H, Hkv;
   float c;                     // softmax_scale * log2(e)
   int G, tt, slots;
@@ -161,7 +163,8 @@ struct AttParams {
 
 // Keys [k0, k1) of a page list and the rows that see them: row i of a suffix
 // sees the first lim0 + i keys (of the suffix's tokens tok_first ...), rows of
-// the prefix the first lim0.
+// the prefix the first lim0. In a tree of drafted tokens row i sees, of its
+// request's last keys, only its ancestors' and its own: key lim0 - 1 + a is that of node a.
 struct AttUnit {
   int kvh, slot, group;
   int tok_first, tok_last;   // tokens [tok_first, tok_last) of the request (prefix: of the batch)
@@ -207,7 +210,7 @@ __device__ __forceinline__ AttUnit att_unit(const AttParams& p, U u, int per) {
     const int a = __ldg(p.cu_q + r), b = __ldg(p.cu_q + r + 1);
     const int n = __ldg(p.suffix_lens + r);
     w.bad = a < 0 || b < a || b > p.Tq || b - a > p.max_q || n < 0 || n > p.max_suffix ||
-            (r == 0 && a != 0);
+            (r == 0 && a != 0) || (p.parents != nullptr && n < b - a);
     if (w.bad) return w;
     w.tok_first = a;
     w.tok_last = b;
@@ -220,6 +223,57 @@ __device__ __forceinline__ AttUnit att_unit(const AttParams& p, U u, int per) {
     w.pages = p.page_table + r * p.table_stride;
   }
   return w;
+}
+
+// Ancestors of the up to 64 nodes of a tree, a node itself among them: a bit each,
+// node `lane` in the .x of both words, node 32 + lane in .y. Every lane of a warp
+// calls it. `parents`: of node 0 on, each before its child or -1 (a root).
+struct AttAncestors {
+  uint2 lo, hi;
+};
+__device__ __forceinline__ AttAncestors att_ancestors(const int32_t* parents, int nodes, uint32_t* status) {
+  const int lane = threadIdx.x & 31;
+  // up[x]: the next ancestor that is not in the node's bits yet
+  int up[2];
+  uint32_t b[2][2] = {{1u << lane, 0u}, {0u, 1u << lane}};
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int i = 32 * x + lane;
+    up[x] = i < nodes ? __ldg(parents + i) : -1;
+    if (up[x] < -1 || up[x] >= i) {
+      set_status(status, TSEL_DEV_PARENTS);
+      up[x] = -1;
+    }
+  }
+  // the way doubles with every round, so six rounds reach past 63 ancestors
+  for (int reach = 1; reach < nodes; reach <<= 1) {
+    int next[2];
+    uint32_t more[2][2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int src = up[x] & 31;
+      const bool high = up[x] >= 32, any = up[x] >= 0;
+      const int n0 = __shfl_sync(0xffffffffu, up[0], src), n1 = __shfl_sync(0xffffffffu, up[1], src);
+      const uint32_t l0 = __shfl_sync(0xffffffffu, b[0][0], src), l1 = __shfl_sync(0xffffffffu, b[1][0], src);
+      const uint32_t h1 = __shfl_sync(0xffffffffu, b[1][1], src);
+      next[x] = any ? (high ? n1 : n0) : -1;
+      more[x][0] = any ? (high ? l1 : l0) : 0u;
+      more[x][1] = any && high ? h1 : 0u;
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      up[x] = next[x];
+      b[x][0] |= more[x][0];
+      b[x][1] |= more[x][1];
+    }
+  }
+  return {make_uint2(b[0][0], b[1][0]), make_uint2(b[0][1], b[1][1])};
+}
+// Node i's bits out of the warp's.
+__device__ __forceinline__ uint64_t att_bits(const AttAncestors& a, int i) {
+  const uint32_t l0 = __shfl_sync(0xffffffffu, a.lo.x, i & 31), l1 = __shfl_sync(0xffffffffu, a.lo.y, i & 31);
+  const uint32_t h1 = __shfl_sync(0xffffffffu, a.hi.y, i & 31);
+  return i < 32 ? uint64_t(l0) : uint64_t(h1) << 32 | l1;
 }
 
 cudaError_t launch_attend(int head_dim, const AttParams& p, int64_t units, cudaStream_t stream);

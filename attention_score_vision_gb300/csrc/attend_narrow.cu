@@ -49,7 +49,7 @@ constexpr float kNarLift = 6.f;      // P = 2^6 at the row's reference
 constexpr float kNarSlack = 9.f;     // the reference may lag the row maximum by 2^9
 
 // NB: groups of eight rows.
-template <int D, int NB>
+template <int D, int NB, bool TREE>
 struct NarCfg {
   static constexpr int H64 = D / 64;               // whole 64-element parts of a row
   static constexpr int TAIL = (D % 64) / 16;       // 4-byte words per lane of the rest
@@ -61,7 +61,8 @@ struct NarCfg {
   static constexpr int WARP_BYTES = kNarStages * STAGE_BYTES;
   static constexpr int ROWS = 8 * NB;
   static constexpr int OFF_ROWS = kNarWarps * WARP_BYTES;   // fp32 m, l [warp][ROWS], int vref [warp]
-  static constexpr int SMEM_BYTES = OFF_ROWS + kNarWarps * (2 * ROWS + 4) * 4;
+  static constexpr int OFF_TREE = OFF_ROWS + kNarWarps * (2 * ROWS + 4) * 4;   // uint64 [warp][ROWS]: ancestors
+  static constexpr int SMEM_BYTES = OFF_TREE + (TREE ? kNarWarps * ROWS * 8 : 0);
   static constexpr int CTAS = NB == 1 ? 4 : 3;     // per SM
   static_assert(kNarWarps * ROWS * D * 4 <= OFF_ROWS, "the outputs fit the ring");
   static_assert(CTAS * (SMEM_BYTES + 1024) <= 228 * 1024, "resident CTAs");
@@ -108,9 +109,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return r;
 }
 
-template <int D, int NB>
-__global__ void __launch_bounds__(kNarThreads, NarCfg<D, NB>::CTAS) attend_narrow_kernel(const AttParams p) {
-  using C = NarCfg<D, NB>;
+// TREE: rows of a suffix are nodes of trees.
+template <int D, int NB, bool TREE>
+__global__ void __launch_bounds__(kNarThreads, NarCfg<D, NB, TREE>::CTAS) attend_narrow_kernel(const AttParams p) {
+  using C = NarCfg<D, NB, TREE>;
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;   // fragment group and place in it
@@ -137,6 +139,7 @@ __global__ void __launch_bounds__(kNarThreads, NarCfg<D, NB>::CTAS) attend_narro
   const uint8_t* ring_ptr = smem + warp * C::WARP_BYTES;
   const int64_t head_row = int64_t(w.kvh) << p.page_shift;
   const int mask = (1 << p.page_shift) - 1;
+  uint64_t* tree = reinterpret_cast<uint64_t*>(smem + C::OFF_TREE) + warp * C::ROWS;
   const bool v_in = C::CB * g < D;   // this lane has V columns
   const int k_at = g * D + 16 * c;                                  // key g, elements 16 c ..
   const int t_at = g * D + 64 * C::H64 + 4 * C::TAIL * c;           // ... of the rest of the row
@@ -256,12 +259,18 @@ __global__ void __launch_bounds__(kNarThreads, NarCfg<D, NB>::CTAS) attend_narro
           for (int x = 0; x < 2; ++x) {
             const int r2 = 8 * n + 2 * c + x;
             qc[n][x] = __shfl_sync(0xffffffffu, mine_c, 4 * (2 * c + x));
-            const int lim = w.causal ? w.lim0 + (row0 + r2) / p.G : w.lim0;
+            const int lim = TREE ? w.lim0 - w.causal : (w.causal ? w.lim0 + (row0 + r2) / p.G : w.lim0);
             end[n][x] = r2 < rows ? min(lim, w.k1) - w.k0 : 0;
             if (r2 < rows) min_end = min(min_end, end[n][x]);
           }
         }
         min_end = __reduce_min_sync(0xffffffffu, min_end);
+        if (TREE && w.causal) {   // `end` is where the tree's keys begin
+          const AttAncestors a = att_ancestors(p.parents + w.tok_first, w.tok_last - w.tok_first, p.status);
+          const uint64_t bits = att_bits(a, lane < rows ? (row0 + lane) / p.G : 0);
+          if (lane < C::ROWS) tree[lane] = bits;
+          __syncwarp();
+        }
       }
       continue;
     }
@@ -307,14 +316,27 @@ __global__ void __launch_bounds__(kNarThreads, NarCfg<D, NB>::CTAS) attend_narro
       for (int x = 0; x < 4; ++x) s[n][x] = (s[n][x] + s1[n][x]) * (kf[x >> 1] * qc[n][x & 1]);
     }
     const bool full = key0 + kNarKeys <= min_end;
+    uint32_t out = 0;   // keys that rows do not see: bit 4 n + 2 x + y
     if (!full) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int key = key0 + 8 * x + g;
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
-          if (key >= end[n][0]) s[n][2 * x] = kNegInf;
-          if (key >= end[n][1]) s[n][2 * x + 1] = kNegInf;
+          if (TREE) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const int node = key - end[n][y];   // below 64 up to the last key of the chunk
+              const bool sees = node < 0 || (w.causal && key < keys && 8 * n + 2 * c + y < rows && ((tree[8 * n + 2 * c + y] >> (node & 63)) & 1u));
+              if (!sees) {
+                out |= 1u << (4 * n + 2 * x + y);
+                s[n][2 * x + y] = kNegInf;
+              }
+            }
+          } else {
+            if (key >= end[n][0]) s[n][2 * x] = kNegInf;
+            if (key >= end[n][1]) s[n][2 * x + 1] = kNegInf;
+          }
         }
         if (key >= keys) vf[x] = 0.f;   // whatever the page holds there
       }
@@ -383,7 +405,7 @@ __global__ void __launch_bounds__(kNarThreads, NarCfg<D, NB>::CTAS) attend_narro
           const float pr = ex2(s[n][2 * x + y] + shift[n][y]);
           l[n][y] += pr;
           e[y] = pr * vr[x];
-          if (!full && key0 + 8 * x + g >= end[n][y]) e[y] = 0.f;   // not 0 * NaN
+          if (TREE ? (out >> (4 * n + 2 * x + y)) & 1u : !full && key0 + 8 * x + g >= end[n][y]) e[y] = 0.f;   // not 0 * NaN
         }
         pb[n][x] = transpose8(f16x2(e[0], e[1]));
       }
@@ -488,10 +510,10 @@ __global__ void __launch_bounds__(kNarThreads, NarCfg<D, NB>::CTAS) attend_narro
   }
 }
 
-template <int D, int NB>
+template <int D, int NB, bool TREE>
 cudaError_t launch_narrow_t(const AttParams& p, int64_t units, cudaStream_t stream) {
-  using C = NarCfg<D, NB>;
-  auto kern = attend_narrow_kernel<D, NB>;
+  using C = NarCfg<D, NB, TREE>;
+  auto kern = attend_narrow_kernel<D, NB, TREE>;
   static bool attr_set[128] = {};   // per device
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -508,10 +530,13 @@ cudaError_t launch_narrow_t(const AttParams& p, int64_t units, cudaStream_t stre
 
 cudaError_t launch_attend_narrow(int head_dim, int row_groups, const AttParams& p, int64_t units,
                                  cudaStream_t stream) {
-#define TSEL_NAR_CASE(DD)                                                \
-  case DD:                                                               \
-    return row_groups == 1 ? launch_narrow_t<DD, 1>(p, units, stream)    \
-                           : launch_narrow_t<DD, 2>(p, units, stream);
+  const bool tree = p.parents != nullptr && units > p.pre_units;
+#define TSEL_NAR_CASE(DD)                                                              \
+  case DD:                                                                             \
+    return row_groups == 1 ? (tree ? launch_narrow_t<DD, 1, true>(p, units, stream)    \
+                                   : launch_narrow_t<DD, 1, false>(p, units, stream))  \
+                           : (tree ? launch_narrow_t<DD, 2, true>(p, units, stream)    \
+                                   : launch_narrow_t<DD, 2, false>(p, units, stream));
   switch (head_dim) {
     TSEL_NAR_CASE(64)
     TSEL_NAR_CASE(80)
