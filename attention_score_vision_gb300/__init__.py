@@ -29,7 +29,9 @@ __all__ = [
     "tsel_status_string", "tsel_last_error", "tsel_probe_ex2",
     "tsel_rope_frequencies", "tsel_rope_table", "tsel_rope",
     "TselCache", "tsel_cache_new", "tsel_cache_workspace_size", "tsel_cache_write", "tsel_cache_read",
+    "tsel_cache_compact", "tsel_cache_resize_workspace_size", "tsel_cache_resize", "tsel_cache_fork",
     "tsel_prefix_attention_workspace_size", "tsel_prefix_attention",
+    "tsel_tree_attention_workspace_size", "tsel_tree_attention", "TSEL_DEV_PARENTS",
     "tsel_prompt_attention_workspace_size", "tsel_prompt_attention", "TSEL_ATT_CAUSAL",
     "TSEL_ROPE_ADJACENT", "TSEL_ROPE_INVERSE", "TSEL_ROPE_SECTIONED", "TSEL_ROPE_INTERLEAVED", "TSEL_ROPE_PER_AXIS",
     "TSEL_DEV_SEQLENS", "TSEL_DEV_REQUESTS", "TSEL_DEV_KEEP_IDX", "TSEL_DEV_TIMEOUT", "TSEL_DEV_NAN",
@@ -51,6 +53,7 @@ TSEL_DEV_TIMEOUT = 0x8
 TSEL_DEV_NAN = 0x10
 TSEL_DEV_PAGES = 0x20
 TSEL_DEV_POSITIONS = 0x40
+TSEL_DEV_PARENTS = 0x80
 
 TSEL_KEEP_FROM_DEVICE = -1
 
@@ -124,11 +127,22 @@ _SIGNATURES = {
                                   _p, _c_size, _p]),
     "tsel_cache_read": (_c_int, [_p, _p, _p, _p, _c_int, _c_int, _p, _c_int, _c_int, _c_int,
                                  _c_int, _p, _c_i64, _p, _c_i64, _p, _c_size, _p]),
+    "tsel_cache_compact": (_c_int, [_p, _p, _p, _p, _c_int, _c_int, _p, _c_i64, _c_int, _p, _c_i64, _c_int, _p, _p, _p, _p,
+                                    _c_int, _c_int, _c_int, _c_int, _c_int, _p, _p, _c_size, _p]),
+    "tsel_cache_resize_workspace_size": (_c_size, [_c_int] * 2),
+    "tsel_cache_resize": (_c_int, [_p, _c_int, _c_int, _p, _c_i64, _c_int, _c_int, _p, _p, _p, _c_size, _p]),
+    "tsel_cache_fork": (_c_int, [_p, _p, _p, _p, _c_int, _c_int, _c_int, _c_int, _p, _p, _c_i64, _c_int, _c_int, _p, _p, _p,
+                                 _c_int, _p, _c_size, _p]),
     "tsel_prefix_attention_workspace_size": (_c_size, [_c_int] * 8),
     "tsel_prefix_attention": (_c_int, [_p, _c_i64, _p, _c_int, _c_int, _c_int, _p, _p, _p, _p,
                                        _c_int, _c_int, _p, _p, _c_int, _p, _c_i64, _p, _c_int,
                                        _c_int, _c_int, _c_int, _c_int, _c_float, _p, _c_i64, _p,
                                        _p, _c_size, _p]),
+    "tsel_tree_attention_workspace_size": (_c_size, [_c_int] * 8),
+    "tsel_tree_attention": (_c_int, [_p, _c_i64, _p, _c_int, _c_int, _c_int, _p, _p, _p, _p, _p,
+                                     _c_int, _c_int, _p, _p, _c_int, _p, _c_i64, _p, _c_int,
+                                     _c_int, _c_int, _c_int, _c_int, _c_float, _p, _c_i64, _p,
+                                     _p, _c_size, _p]),
     "tsel_prompt_attention_workspace_size": (_c_size, [_c_int] * 7),
     "tsel_prompt_attention": (_c_int, [_p, _c_i64, _p, _c_i64, _p, _c_i64, _p, _p, _c_int, _c_int, _c_int, _c_int,
                                        _c_int, _c_int, _c_int, _c_int, _c_int, _c_float, _c_uint, _p, _c_i64, _p,
@@ -849,6 +863,122 @@ def tsel_cache_read(cache: TselCache, slots: torch.Tensor, *, dtype=torch.bfloat
 
 
 # ---------------------------------------------------------------------------
+# Pages of the cache
+# ---------------------------------------------------------------------------
+
+def _table(t: torch.Tensor, name: str, index: int, rows: Optional[int] = None):
+    """Checks a page table, int32 [rows, pages] with contiguous rows; returns
+    (pointer, row stride, rows, pages)."""
+    if t.dtype is not _I32:
+        raise TypeError(f"{name} must be a CUDA torch.int32 tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}")
+    shape = t.shape
+    if len(shape) != 2 or (rows is not None and shape[0] != rows) or (shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be an int32 [requests, pages] tensor with contiguous rows")
+    stride = t.stride(0) if shape[0] > 1 else shape[1]
+    if stride < shape[1]:
+        raise ValueError(f"{name} rows must not overlap")
+    return t.data_ptr(), stride, shape[0], shape[1]
+
+
+def tsel_cache_compact(cache: TselCache, page_table: torch.Tensor, keep_idx: torch.Tensor, cu_keep: torch.Tensor,
+                       max_keep: int, *, starts: Optional[torch.Tensor] = None, bases: Optional[torch.Tensor] = None,
+                       dst_table: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Moves the cached rows of kept tokens together; returns the new lengths int32 [R].
+
+    Token k of request r's kept ones goes from position starts[r] + keep_idx[cu_keep[r] + k]
+    - bases[r] of its pages (page_table int32 [R, pages]) to position starts[r] + k of
+    the pages of dst_table, or of its own (None: in place). keep_idx ascends in each
+    request, e.g. accepted nodes of a drafted tree with starts = the length before it, or
+    tsel_select_topk's tokens with bases = its request offsets."""
+    index = cache.k_pages.get_device()
+    if index < 0:
+        raise TypeError("the cache must be on a CUDA device")
+    cache_p, Hkv, d = _cache_args(cache, index)
+    R = cu_keep.numel() - 1
+    if R < 0:
+        raise ValueError("cu_keep must have at least one entry")
+    table_p, table_s, _, pages = _table(page_table, "page_table", index, R)
+    to_p, to_s, to_pages = None, 0, 0
+    if dst_table is not None:
+        to_p, to_s, _, to_pages = _table(dst_table, "dst_table", index, R)
+        if to_p == table_p:
+            raise ValueError("dst_table is page_table: give None to move in place")
+    keep_p = _vector(keep_idx, _I32, "keep_idx", index)
+    cu_p = _vector(cu_keep, _I32, "cu_keep", index)
+    starts_p = None if starts is None else _vector(starts, _I32, "starts", index, R)
+    bases_p = None if bases is None else _vector(bases, _I32, "bases", index, R)
+    total, most = keep_idx.numel(), int(max_keep)
+    _sizes(R | total | most | pages | to_pages | Hkv | d | cache_p[4] | cache_p[5])
+    if new_lens is not None:
+        if _vector(new_lens, _I32, "new_lens", index, R) == starts_p and R:
+            raise ValueError("new_lens must not be starts")
+        _written(new_lens)
+    workspace = _workspace(workspace, 1024, index, stream)
+    if new_lens is None:
+        new_lens = _new(stream, torch.empty, R, dtype=_I32, device=cu_keep.device)
+    _call(load_library().tsel_cache_compact, index, stream, *cache_p, table_p, table_s, pages, to_p, to_s, to_pages,
+          starts_p, bases_p, keep_p, cu_p, R, total, most, Hkv, d, new_lens.data_ptr(), workspace.data_ptr(),
+          workspace.numel())
+    return new_lens
+
+
+def tsel_cache_resize_workspace_size(num_rows: int, pages_per_row: int) -> int:
+    """Bytes of workspace of tsel_cache_resize and tsel_cache_fork."""
+    sizes = [int(num_rows), int(pages_per_row)]
+    if any(n >> 31 for n in sizes):   # negative, or more than a C int holds
+        return 0
+    return int(load_library().tsel_cache_resize_workspace_size(*sizes))
+
+
+def tsel_cache_resize(refs: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor, new_lens: torch.Tensor,
+                      page_size: int, *, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gives pages to the rows of page_table (int32 [rows, pages]) that grow from lens to
+    new_lens (int32 [rows], negative: left alone) and takes them back from those that
+    shrink. refs int32 [num_pages] counts the rows that hold a page; the lowest free
+    pages go to rows in order. page_table, refs and lens are written."""
+    index = refs.get_device()
+    if index < 0:
+        raise TypeError("refs must be a CUDA torch.int32 tensor")
+    refs_p = _vector(refs, _I32, "refs", index)
+    table_p, stride, rows, pages = _table(page_table, "page_table", index)
+    lens_p = _vector(lens, _I32, "lens", index, rows)
+    new_p = _vector(new_lens, _I32, "new_lens", index, rows)
+    num_pages, page_size = refs.numel(), int(page_size)
+    _sizes(num_pages | rows | pages | page_size)
+    nbytes = 0 if workspace is not None else tsel_cache_resize_workspace_size(rows, pages)
+    workspace = _workspace(workspace, nbytes, index, stream)
+    _call(load_library().tsel_cache_resize, index, stream, refs_p, num_pages, page_size, table_p, stride, rows, pages,
+          lens_p, new_p, workspace.data_ptr(), workspace.numel())
+
+
+def tsel_cache_fork(cache: TselCache, refs: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
+                    parents: torch.Tensor, children: torch.Tensor, *, workspace: Optional[torch.Tensor] = None,
+                    stream=None) -> None:
+    """Rows children[i] of page_table start from the cached tokens of rows parents[i]
+    (int32 [n], children ascending and of length 0): whole pages are shared, the
+    rows of a last page that is not full are copied into a free one. cache, refs (int32
+    [num_pages]), page_table and lens are written."""
+    index = cache.k_pages.get_device()
+    if index < 0:
+        raise TypeError("the cache must be on a CUDA device")
+    cache_p, Hkv, d = _cache_args(cache, index)
+    refs_p = _vector(refs, _I32, "refs", index, cache_p[4])
+    table_p, stride, rows, pages = _table(page_table, "page_table", index)
+    lens_p = _vector(lens, _I32, "lens", index, rows)
+    parents_p = _vector(parents, _I32, "parents", index)
+    n = parents.numel()
+    children_p = _vector(children, _I32, "children", index, n)
+    _sizes(n | rows | pages | Hkv | d | cache_p[4] | cache_p[5])
+    nbytes = 0 if workspace is not None else tsel_cache_resize_workspace_size(rows, pages)
+    workspace = _workspace(workspace, nbytes, index, stream)
+    _call(load_library().tsel_cache_fork, index, stream, *cache_p, Hkv, d, refs_p, table_p, stride, rows, pages, lens_p,
+          parents_p, children_p, n, workspace.data_ptr(), workspace.numel())
+
+
+# ---------------------------------------------------------------------------
 # Attention over a shared prefix
 # ---------------------------------------------------------------------------
 
@@ -878,6 +1008,13 @@ def tsel_prefix_attention(q: torch.Tensor, cu_seqlens_q: torch.Tensor, max_seqle
     request's last query rows are its last suffix tokens (causal). Rows past
     cu_seqlens_q[R] are left as they are in a given out or lse. The results carry
     no gradients."""
+    return _attend_cache(q, cu_seqlens_q, max_seqlen_q, None, cache, prefix_pages, prefix_len, max_prefix_len, page_table,
+                         suffix_lens, max_suffix_len, softmax_scale, out, lse, want_lse, workspace, stream)
+
+
+def _attend_cache(q, cu_seqlens_q, max_seqlen_q, parents, cache, prefix_pages, prefix_len, max_prefix_len, page_table,
+                  suffix_lens, max_suffix_len, softmax_scale, out, lse, want_lse, workspace, stream):
+    """Both attentions over the cache: of trees where parents are given."""
     shape, dtype, index = _first(q, "q")
     if dtype is _F32:
         raise TypeError("q must be bf16 or fp16")
@@ -892,6 +1029,7 @@ def tsel_prefix_attention(q: torch.Tensor, cu_seqlens_q: torch.Tensor, max_seqle
     if R < 0:
         raise ValueError("cu_seqlens_q must have at least one entry")
     max_q, max_p, max_s = int(max_seqlen_q), int(max_prefix_len), int(max_suffix_len)
+    parents_p = None if parents is None else _vector(parents, _I32, "parents", index, tq)
     _sizes(tq | H | Hkv | d | R | max_q | max_p | max_s | cache_p[4] | page_size)
     prefix_p = len_p = table_p = suffix_p = None
     if max_p > 0:
@@ -924,18 +1062,46 @@ def tsel_prefix_attention(q: torch.Tensor, cu_seqlens_q: torch.Tensor, max_seqle
         _vector(lse, _F32, "lse", index, H * tq)
     if out is not None or lse is not None:
         _written(out, lse)
-    nbytes = 0 if workspace is not None else tsel_prefix_attention_workspace_size(
-        R, tq, max_q, H, Hkv, d, max_p, max_s)
+    nbytes = 0 if workspace is not None else tsel_prefix_attention_workspace_size(R, tq, max_q, H, Hkv, d, max_p, max_s)
     workspace = _workspace(workspace, nbytes, index, stream)
     if out is None:
         out = _like(q, stream)
     if lse is None and want_lse:
         lse = _new(stream, torch.empty, (H, tq), dtype=_F32, device=q.device)
-    _call(load_library().tsel_prefix_attention, index, stream, q.data_ptr(), qs, cu_p, R, tq,
-          max_q, *cache_p, prefix_p, len_p, max_p, table_p, table_stride, suffix_p, max_s, H, Hkv, d,
+    tree = () if parents is None else (parents_p,)
+    _call(load_library().tsel_prefix_attention if parents is None else load_library().tsel_tree_attention, index, stream,
+          q.data_ptr(), qs, cu_p, R, tq, max_q, *tree, *cache_p, prefix_p, len_p, max_p, table_p, table_stride, suffix_p, max_s, H, Hkv, d,
           _DTYPES[dtype], softmax_scale, out.data_ptr(), os_, _ptr(lse), workspace.data_ptr(),
           workspace.numel())
     return out, lse
+
+
+def tsel_tree_attention_workspace_size(num_req: int, total_q: int, max_nodes: int, num_heads: int, num_kv_heads: int,
+                                       head_dim: int, max_prefix_len: int, max_suffix_len: int) -> int:
+    sizes = [int(n) for n in (num_req, total_q, max_nodes, num_heads, num_kv_heads, head_dim, max_prefix_len, max_suffix_len)]
+    if any(n >> 31 for n in sizes):   # negative, or more than a C int holds
+        return 0
+    return int(load_library().tsel_tree_attention_workspace_size(*sizes))
+
+
+def tsel_tree_attention(q: torch.Tensor, cu_seqlens_q: torch.Tensor, max_nodes: int, parents: torch.Tensor,
+                        cache: TselCache, prefix_pages: Optional[torch.Tensor], prefix_len: Optional[torch.Tensor],
+                        max_prefix_len: int, page_table: Optional[torch.Tensor], suffix_lens: Optional[torch.Tensor],
+                        max_suffix_len: int, *, softmax_scale: float = 0.0, out: Optional[torch.Tensor] = None,
+                        lse: Optional[torch.Tensor] = None, want_lse: bool = True,
+                        workspace: Optional[torch.Tensor] = None,
+                        stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """tsel_prefix_attention of drafted tokens that form a tree in each request; returns
+    (out [Tq, H, d], lse fp32 [H, Tq] or None).
+
+    parents int32 [Tq]: each node's parent as an index into its request's nodes, or -1
+    for a root. A request's last suffix keys are those of its nodes (at most 64), in
+    order; a node sees the prefix, the suffix before the tree, its ancestors and itself.
+    The results carry no gradients."""
+    if parents is None:
+        raise ValueError("parents must be an int32 [tokens] tensor")
+    return _attend_cache(q, cu_seqlens_q, max_nodes, parents, cache, prefix_pages, prefix_len, max_prefix_len, page_table,
+                         suffix_lens, max_suffix_len, softmax_scale, out, lse, want_lse, workspace, stream)
 
 
 # ---------------------------------------------------------------------------

@@ -11,6 +11,7 @@
 
 #include "attend.cuh"
 #include "common.cuh"
+#include "pages.cuh"
 #include "prompt.cuh"
 #include "rope.cuh"
 
@@ -321,9 +322,10 @@ size_t tsel_prefix_attention_workspace_size(int num_req, int total_q, int max_se
   return a.too_large ? 0 : size_t(a.total);
 }
 
-tsel_status tsel_prefix_attention(
+// Both attentions over the cache; `parents` (and `tree`) are the tree's.
+static tsel_status attend_cache(
     const void* q, int64_t q_row_stride, const int32_t* cu_seqlens_q, int num_req, int total_q,
-    int max_seqlen_q, const uint8_t* k_pages, const uint8_t* v_pages, const uint8_t* k_exps,
+    int max_seqlen_q, bool tree, const int32_t* parents, const uint8_t* k_pages, const uint8_t* v_pages, const uint8_t* k_exps,
     const uint8_t* v_exps, int num_pages, int page_size, const int32_t* prefix_pages,
     const int32_t* prefix_len, int max_prefix_len, const int32_t* page_table,
     int64_t page_table_stride, const int32_t* suffix_lens, int max_suffix_len, int num_heads,
@@ -346,6 +348,10 @@ tsel_status tsel_prefix_attention(
   if (!(softmax_scale == softmax_scale) || std::isinf(softmax_scale))
     return fail(TSEL_ERR_INVALID_VALUE, "softmax_scale");
   if (cu_seqlens_q == nullptr) return fail(TSEL_ERR_INVALID_VALUE, "null cu_seqlens_q");
+  if (tree && max_seqlen_q > kAttTreeNodes)
+    return fail(TSEL_ERR_UNSUPPORTED, "trees of up to %d nodes (at most %d)", max_seqlen_q, kAttTreeNodes);
+  if (tree && total_q > 0 && (parents == nullptr || !aligned(parents, 4)))
+    return fail(TSEL_ERR_INVALID_VALUE, "parents");
   if (max_prefix_len > 0 && (prefix_pages == nullptr || prefix_len == nullptr))
     return fail(TSEL_ERR_INVALID_VALUE, "null prefix_pages or prefix_len");
   if (max_suffix_len > 0 && num_req > 0 && (page_table == nullptr || suffix_lens == nullptr))
@@ -385,6 +391,7 @@ tsel_status tsel_prefix_attention(
   p.table_stride = page_table_stride;
   p.suffix_lens = suffix_lens;
   p.max_suffix = max_suffix_len;
+  p.parents = parents;
   p.H = num_heads;
   p.Hkv = num_kv_heads;
   const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt(float(head_dim));
@@ -415,6 +422,41 @@ tsel_status tsel_prefix_attention(
   }
   e = launch_attend_join(head_dim, p, stream);
   return e == cudaSuccess ? TSEL_OK : cuda_fail(e, "join launch");
+}
+
+tsel_status tsel_prefix_attention(
+    const void* q, int64_t q_row_stride, const int32_t* cu_seqlens_q, int num_req, int total_q,
+    int max_seqlen_q, const uint8_t* k_pages, const uint8_t* v_pages, const uint8_t* k_exps,
+    const uint8_t* v_exps, int num_pages, int page_size, const int32_t* prefix_pages,
+    const int32_t* prefix_len, int max_prefix_len, const int32_t* page_table,
+    int64_t page_table_stride, const int32_t* suffix_lens, int max_suffix_len, int num_heads,
+    int num_kv_heads, int head_dim, int dtype, float softmax_scale, void* out,
+    int64_t out_row_stride, float* lse, void* workspace, size_t workspace_bytes, void* stream_) {
+  return attend_cache(q, q_row_stride, cu_seqlens_q, num_req, total_q, max_seqlen_q, false, nullptr, k_pages, v_pages, k_exps,
+                      v_exps, num_pages, page_size, prefix_pages, prefix_len, max_prefix_len, page_table,
+                      page_table_stride, suffix_lens, max_suffix_len, num_heads, num_kv_heads, head_dim, dtype,
+                      softmax_scale, out, out_row_stride, lse, workspace, workspace_bytes, stream_);
+}
+
+size_t tsel_tree_attention_workspace_size(int num_req, int total_q, int max_nodes, int num_heads, int num_kv_heads,
+                                          int head_dim, int max_prefix_len, int max_suffix_len) {
+  return max_nodes > kAttTreeNodes ? 0
+                                   : tsel_prefix_attention_workspace_size(num_req, total_q, max_nodes, num_heads, num_kv_heads,
+                                                                          head_dim, max_prefix_len, max_suffix_len);
+}
+
+tsel_status tsel_tree_attention(
+    const void* q, int64_t q_row_stride, const int32_t* cu_seqlens_q, int num_req, int total_q,
+    int max_nodes, const int32_t* parents, const uint8_t* k_pages, const uint8_t* v_pages, const uint8_t* k_exps,
+    const uint8_t* v_exps, int num_pages, int page_size, const int32_t* prefix_pages,
+    const int32_t* prefix_len, int max_prefix_len, const int32_t* page_table,
+    int64_t page_table_stride, const int32_t* suffix_lens, int max_suffix_len, int num_heads,
+    int num_kv_heads, int head_dim, int dtype, float softmax_scale, void* out,
+    int64_t out_row_stride, float* lse, void* workspace, size_t workspace_bytes, void* stream_) {
+  return attend_cache(q, q_row_stride, cu_seqlens_q, num_req, total_q, max_nodes, true, parents, k_pages, v_pages, k_exps,
+                      v_exps, num_pages, page_size, prefix_pages, prefix_len, max_prefix_len, page_table,
+                      page_table_stride, suffix_lens, max_suffix_len, num_heads, num_kv_heads, head_dim, dtype,
+                      softmax_scale, out, out_row_stride, lse, workspace, workspace_bytes, stream_);
 }
 
 size_t tsel_prompt_attention_workspace_size(int num_seg, int total_q, int max_seqlen_q, int max_seqlen_k,
@@ -529,6 +571,142 @@ tsel_status tsel_prompt_attention(const void* q, int64_t q_row_stride, const voi
   j.status = p.status;
   e = launch_attend_join(head_dim, j, stream);
   return e == cudaSuccess ? TSEL_OK : cuda_fail(e, "join launch");
+}
+
+tsel_status tsel_cache_compact(uint8_t* k_pages, uint8_t* v_pages, uint8_t* k_exps, uint8_t* v_exps, int num_pages,
+                               int page_size, const int32_t* page_table, int64_t page_table_stride, int pages_per_req,
+                               const int32_t* dst_table, int64_t dst_table_stride, int dst_pages_per_req,
+                               const int32_t* starts, const int32_t* bases, const int32_t* keep_idx,
+                               const int32_t* cu_keep, int num_req, int total_keep, int max_keep, int num_kv_heads,
+                               int head_dim, int32_t* new_lens, void* workspace, size_t workspace_bytes,
+                               void* stream_) {
+  if (num_req < 0 || total_keep < 0 || max_keep < 0 || pages_per_req < 0 || (dst_table != nullptr && dst_pages_per_req < 0))
+    return fail(TSEL_ERR_INVALID_VALUE, "negative size");
+  TSEL_TRY(check_cache(k_pages, v_pages, k_exps, v_exps, num_pages, page_size, num_kv_heads, head_dim));
+  TSEL_TRY(check_header(workspace, workspace_bytes));
+  if (num_req == 0) return TSEL_OK;
+  if (cu_keep == nullptr || !aligned(cu_keep, 4) || !aligned(starts, 4) || !aligned(bases, 4) || !aligned(new_lens, 4))
+    return fail(TSEL_ERR_INVALID_VALUE, "cu_keep, starts, bases or new_lens");
+  if (total_keep > 0 && (keep_idx == nullptr || !aligned(keep_idx, 4))) return fail(TSEL_ERR_INVALID_VALUE, "keep_idx");
+  if (max_keep > 0 && pages_per_req > 0 && (page_table == nullptr || !aligned(page_table, 4)))
+    return fail(TSEL_ERR_INVALID_VALUE, "page_table");
+  if (page_table_stride < pages_per_req || (dst_table != nullptr && dst_table_stride < dst_pages_per_req))
+    return fail(TSEL_ERR_INVALID_VALUE, "table strides %lld, %lld", (long long)page_table_stride, (long long)dst_table_stride);
+  if (!aligned(dst_table, 4)) return fail(TSEL_ERR_INVALID_VALUE, "dst_table");
+  MoveParams p{};
+  p.k_pages = k_pages;
+  p.v_pages = v_pages;
+  p.k_exps = k_exps;
+  p.v_exps = v_exps;
+  p.num_pages = num_pages;
+  p.page_shift = page_shift_of(page_size);
+  p.Hkv = num_kv_heads;
+  p.d = head_dim;
+  p.table = page_table;
+  p.table_stride = page_table_stride;
+  p.width = pages_per_req;
+  p.dst_table = dst_table;
+  p.dst_stride = dst_table_stride;
+  p.dst_width = dst_pages_per_req;
+  p.starts = starts;
+  p.bases = bases;
+  p.keep = keep_idx;
+  p.cu_keep = cu_keep;
+  p.total = total_keep;
+  p.max_keep = max_keep > 0 ? max_keep : 1;   // the lengths are written without kept tokens too
+  p.R = num_req;
+  p.new_lens = new_lens;
+  p.status = &static_cast<WsHeader*>(workspace)->status;
+  int sms = 0;
+  if (device_sms(&sms) != 0) return fail(TSEL_ERR_CUDA, "cannot query the SM count");
+  move_plan(p, sms);
+  p.max_keep = max_keep;
+  if (int64_t(p.R) * p.chunks * p.head_parts * p.slices > 0x7FFFFFFFll)
+    return fail(TSEL_ERR_UNSUPPORTED, "too many units of work");
+  const cudaError_t e = launch_move(p, static_cast<cudaStream_t>(stream_));
+  return e == cudaSuccess ? TSEL_OK : cuda_fail(e, "cache compaction launch");
+}
+
+size_t tsel_cache_resize_workspace_size(int num_rows, int pages_per_row) {
+  if (num_rows < 0 || pages_per_row < 0 || int64_t(num_rows) * pages_per_row > 0x7FFFFFFFll) return 0;
+  const int64_t found = align_up(kWsHeaderBytes + 4 * (int64_t(num_rows) + 1), 256);
+  return size_t(found + 4 * align_up(int64_t(num_rows) * (pages_per_row > 0 ? pages_per_row : 1), 64));
+}
+
+// What resizing and forking have in common.
+static tsel_status pages_params(PagesParams* p, int32_t* refs, int num_pages, int page_size, int32_t* page_table,
+                                int64_t page_table_stride, int num_rows, int pages_per_row, int32_t* lens,
+                                void* workspace, size_t workspace_bytes) {
+  if (page_shift_of(page_size) < 0)
+    return fail(TSEL_ERR_UNSUPPORTED, "page_size=%d (supported: 16, 32, 64, 128)", page_size);
+  if (num_pages < 0 || int64_t(num_pages) * page_size > 0x7FFFFFFFll)
+    return fail(TSEL_ERR_INVALID_VALUE, "num_pages=%d of %d", num_pages, page_size);
+  if (num_rows < 0 || pages_per_row < 0 || int64_t(num_rows) * pages_per_row > 0x7FFFFFFFll)
+    return fail(TSEL_ERR_INVALID_VALUE, "%d rows of %d pages", num_rows, pages_per_row);
+  TSEL_TRY(check_header(workspace, workspace_bytes));
+  const size_t need = tsel_cache_resize_workspace_size(num_rows, pages_per_row);
+  if (workspace_bytes < need) return fail(TSEL_ERR_WORKSPACE, "workspace %zu < %zu bytes", workspace_bytes, need);
+  if (num_rows > 0 && (lens == nullptr || !aligned(lens, 4))) return fail(TSEL_ERR_INVALID_VALUE, "lens");
+  if (num_rows > 0 && pages_per_row > 0 && (page_table == nullptr || !aligned(page_table, 4)))
+    return fail(TSEL_ERR_INVALID_VALUE, "page_table");
+  if (page_table_stride < pages_per_row)
+    return fail(TSEL_ERR_INVALID_VALUE, "page_table_stride %lld", (long long)page_table_stride);
+  if (num_pages > 0 && (refs == nullptr || !aligned(refs, 4))) return fail(TSEL_ERR_INVALID_VALUE, "refs");
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p->refs = refs;
+  p->num_pages = num_pages;
+  p->page_shift = page_shift_of(page_size);
+  p->table = page_table;
+  p->table_stride = page_table_stride;
+  p->rows = num_rows;
+  p->width = pages_per_row;
+  p->lens = lens;
+  p->plan = reinterpret_cast<int32_t*>(ws + kWsHeaderBytes);
+  p->found = reinterpret_cast<int32_t*>(ws + align_up(kWsHeaderBytes + 4 * (int64_t(num_rows) + 1), 256));
+  p->status = &reinterpret_cast<WsHeader*>(ws)->status;
+  return TSEL_OK;
+}
+
+tsel_status tsel_cache_resize(int32_t* refs, int num_pages, int page_size, int32_t* page_table,
+                              int64_t page_table_stride, int num_rows, int pages_per_row, int32_t* lens,
+                              const int32_t* new_lens, void* workspace, size_t workspace_bytes, void* stream_) {
+  PagesParams p{};
+  TSEL_TRY(pages_params(&p, refs, num_pages, page_size, page_table, page_table_stride, num_rows, pages_per_row, lens,
+                        workspace, workspace_bytes));
+  if (num_rows == 0) return TSEL_OK;
+  if (new_lens == nullptr || !aligned(new_lens, 4)) return fail(TSEL_ERR_INVALID_VALUE, "new_lens");
+  p.new_lens = new_lens;
+  const cudaError_t e = launch_resize(p, static_cast<cudaStream_t>(stream_));
+  return e == cudaSuccess ? TSEL_OK : cuda_fail(e, "cache resize launch");
+}
+
+tsel_status tsel_cache_fork(uint8_t* k_pages, uint8_t* v_pages, uint8_t* k_exps, uint8_t* v_exps, int num_pages,
+                            int page_size, int num_kv_heads, int head_dim, int32_t* refs, int32_t* page_table,
+                            int64_t page_table_stride, int num_rows, int pages_per_row, int32_t* lens,
+                            const int32_t* parents, const int32_t* children, int num_forks, void* workspace,
+                            size_t workspace_bytes, void* stream_) {
+  TSEL_TRY(check_cache(k_pages, v_pages, k_exps, v_exps, num_pages, page_size, num_kv_heads, head_dim));
+  PagesParams p{};
+  TSEL_TRY(pages_params(&p, refs, num_pages, page_size, page_table, page_table_stride, num_rows, pages_per_row, lens,
+                        workspace, workspace_bytes));
+  if (num_forks < 0 || num_forks > num_rows)
+    return fail(TSEL_ERR_INVALID_VALUE, "num_forks=%d of %d rows", num_forks, num_rows);
+  if (num_forks == 0) return TSEL_OK;
+  if (parents == nullptr || children == nullptr || !aligned(parents, 4) || !aligned(children, 4))
+    return fail(TSEL_ERR_INVALID_VALUE, "parents or children");
+  p.parents = parents;
+  p.children = children;
+  p.n = num_forks;
+  p.k_pages = k_pages;
+  p.v_pages = v_pages;
+  p.k_exps = k_exps;
+  p.v_exps = v_exps;
+  p.Hkv = num_kv_heads;
+  p.d = head_dim;
+  p.parts = kForkParts;
+  if (int64_t(num_forks) * p.parts > 0x7FFFFFFFll) return fail(TSEL_ERR_UNSUPPORTED, "too many units of work");
+  const cudaError_t e = launch_fork(p, static_cast<cudaStream_t>(stream_));
+  return e == cudaSuccess ? TSEL_OK : cuda_fail(e, "cache fork launch");
 }
 
 }  // extern "C"

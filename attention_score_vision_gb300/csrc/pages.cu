@@ -1,0 +1,393 @@
+// Pages of the quantised cache: the rows of kept tokens moved together (accepted
+// drafts, a pruned prompt), pages shared by requests that start from another one,
+// and pages given out and back. Dynamic vision-token compression article, section
+// 3.2: after pruning the KV cache holds the kept tokens.
+//
+// cache_move_kernel. Token k of a request's kept list goes from position
+// start + keep[k] - base to start + k: cached bytes move unchanged. A thread owns
+// one 16-byte piece of rows and has eight of them in flight. A CTA covers some of
+// the K and V heads (and, where requests are few, some pieces of their rows) for
+// one chunk of tokens; a chunk's row numbers are worked out once in shared memory.
+//   In place the destination of one token may be the source of another. Kept
+// indices ascend, so a token's source is at or behind its destination and a
+// destination is the source of this chunk's tokens or earlier ones', never of
+// later ones'. So a CTA takes all the chunks of a request in order and every load
+// of a chunk comes before its stores (one barrier); CTAs of other heads or pieces
+// touch other bytes.
+//
+// cache_resize_kernel, fork_plan_kernel. Reference counts are whole numbers added
+// with atomics, so their order does not matter; free pages (count 0) are found by
+// one CTA that walks the counts 8,192 at a time until it has enough, and go, lowest
+// first, to rows in order: results are deterministic.
+#include "launch_util.cuh"
+#include "pages.cuh"
+
+namespace tsel {
+
+namespace {
+
+__device__ __forceinline__ int ceil_pages(int n, int shift) { return int((int64_t(n) + (1 << shift) - 1) >> shift); }
+
+template <bool IN_PLACE>
+__global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(const MoveParams p) {
+  extern __shared__ int64_t s_rows[];   // [chunk mod 3][source, destination][tokens]: rows of head 0, -1 none
+  pdl_wait();
+  pdl_launch_dependents();
+  unsigned b = blockIdx.x;
+  const int slice = int(b % unsigned(p.slices));
+  b /= unsigned(p.slices);
+  const int part = int(b % unsigned(p.head_parts));
+  b /= unsigned(p.head_parts);
+  const int first_chunk = int(b % unsigned(p.chunks)), r = int(b / unsigned(p.chunks));
+  const int a = __ldg(p.cu_keep + r), e = __ldg(p.cu_keep + r + 1);
+  const int start = p.starts != nullptr ? __ldg(p.starts + r) : 0, base = p.bases != nullptr ? __ldg(p.bases + r) : 0;
+  const bool lead = threadIdx.x == 0 && part == 0 && slice == 0 && first_chunk == 0;
+  const int64_t room = int64_t(IN_PLACE ? p.width : p.dst_width) << p.page_shift;
+  if (a < 0 || e < a || e > p.total || e - a > p.max_keep || (r == 0 && a != 0) || start < 0 || int64_t(start) + (e - a) > room) {
+    if (lead) set_status(p.status, TSEL_DEV_REQUESTS);
+    return;
+  }
+  const int n = e - a;
+  if (lead && p.new_lens != nullptr) p.new_lens[r] = start + n;
+  const int chunks = int(ceil_div(n, p.tokens));
+  if (first_chunk >= chunks) return;
+
+  const int32_t* table = p.table + r * p.table_stride;
+  const int32_t* to = IN_PLACE ? table : p.dst_table + r * p.dst_stride;
+  const int mask = (1 << p.page_shift) - 1;
+  // rows of a chunk's tokens: [(page * Hkv) << shift] + place
+  auto find = [&](int c, int64_t* rows) {
+    for (int i = threadIdx.x; i < p.tokens; i += kMoveThreads) {
+      const int k = c * p.tokens + i;
+      int64_t src = -1, dst = -1;
+      if (k < n) {
+        const int64_t rel = int64_t(__ldg(p.keep + a + k)) - base;
+        const int64_t at = start + rel;
+        if (rel < k || at >= int64_t(p.width) << p.page_shift || (k > 0 && rel <= int64_t(__ldg(p.keep + a + k - 1)) - base)) {
+          set_status(p.status, TSEL_DEV_KEEP_IDX);
+        } else if (!IN_PLACE || rel != k) {
+          const int put = start + k;
+          const int pg = __ldg(table + (at >> p.page_shift)), pd = __ldg(to + (put >> p.page_shift));
+          if (pg < 0 || pg >= p.num_pages || pd < 0 || pd >= p.num_pages) {
+            set_status(p.status, TSEL_DEV_PAGES);
+          } else {
+            src = ((int64_t(pg) * p.Hkv) << p.page_shift) + (at & mask);
+            dst = ((int64_t(pd) * p.Hkv) << p.page_shift) + (put & mask);
+          }
+        }
+      }
+      rows[i] = src;
+      rows[p.tokens + i] = dst;
+    }
+  };
+
+  const int head0 = part * p.heads, heads = min(p.heads, 2 * p.Hkv - head0);
+  const int piece0 = slice * p.pieces, pieces = min(p.pieces, p.d / 16 - piece0);
+  const int groups = kMoveThreads / p.pieces;
+  const int group = int(threadIdx.x) / p.pieces, piece = int(threadIdx.x) - group * p.pieces;
+  const bool works = group < groups && piece < pieces;
+  const bool scales = works && piece == 0 && slice == 0;   // also moves the row's scale byte
+  // item i of this thread: (token, head), head fastest, `groups` apart
+  const int tok_step = groups / heads, head_step = groups - tok_step * heads;
+  int buf = 0;
+  find(first_chunk, s_rows);
+  __syncthreads();
+  for (int c = first_chunk; c < chunks; ++c) {
+    const int64_t* rows = s_rows + buf * 2 * p.tokens;
+    const int left = min(n - c * p.tokens, p.tokens);
+    uint4 data[kMoveItems];
+    uint8_t exps[kMoveItems];
+    auto each = [&](auto&& f) {
+      int tok = group / heads, h = group - tok * heads;
+#pragma unroll
+      for (int i = 0; i < kMoveItems; ++i) {
+        if (works && tok < left) f(i, tok, head0 + h);
+        tok += tok_step;
+        h += head_step;
+        if (h >= heads) {
+          h -= heads;
+          ++tok;
+        }
+      }
+    };
+    each([&](int i, int tok, int h) {
+      const int64_t row = rows[tok];
+      if (row < 0) return;
+      const bool v = h >= p.Hkv;
+      const int64_t at = row + (int64_t(v ? h - p.Hkv : h) << p.page_shift);
+      data[i] = __ldcg(reinterpret_cast<const uint4*>((v ? p.v_pages : p.k_pages) + at * p.d) + piece0 + piece);
+      if (scales) exps[i] = __ldcg((v ? p.v_exps : p.k_exps) + at);
+    });
+    // every load of the chunk before its stores; and the next chunk's rows, in a
+    // place that no thread can still read for its stores of the chunk before
+    buf = buf == 2 ? 0 : buf + 1;
+    if (IN_PLACE && c + 1 < chunks) find(c + 1, s_rows + buf * 2 * p.tokens);
+    if (IN_PLACE) __syncthreads();
+    each([&](int i, int tok, int h) {
+      if (rows[tok] < 0) return;
+      const bool v = h >= p.Hkv;
+      const int64_t at = rows[p.tokens + tok] + (int64_t(v ? h - p.Hkv : h) << p.page_shift);
+      reinterpret_cast<uint4*>((v ? p.v_pages : p.k_pages) + at * p.d)[piece0 + piece] = data[i];
+      if (scales) ((v ? p.v_exps : p.k_exps) + at)[0] = exps[i];
+    });
+    if (!IN_PLACE) break;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Counts
+// ---------------------------------------------------------------------------
+
+constexpr int kPagesThreads = 1024;
+constexpr int kPagesWarps = kPagesThreads / 32;
+constexpr int kPagesPerLane = 8;
+
+// Inclusive sums over the block's threads; the total in *total.
+__device__ __forceinline__ int block_sum(int mine, int* s_warps, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int v = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += y;
+  }
+  __syncthreads();   // the sums of the call before have been read
+  if (lane == 31) s_warps[warp] = v;
+  __syncthreads();
+  int before = s_warps[lane];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += y;
+  }
+  *total = __shfl_sync(0xffffffffu, before, 31);
+  const int up_to = __shfl_sync(0xffffffffu, before, max(warp - 1, 0));   // of the warps before
+  return v + (warp > 0 ? up_to : 0);
+}
+
+// Writes the lowest `want` free pages into list; returns how many there are (at
+// most `want`).
+__device__ int free_pages(const int32_t* refs, int num_pages, int want, int32_t* list, int* s_warps) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int got = 0;
+  for (int64_t base = 0; base < num_pages && got < want; base += kPagesThreads * kPagesPerLane) {
+    const int64_t first = base + warp * (32 * kPagesPerLane) + lane;
+    unsigned free_[kPagesPerLane];
+    int count = 0;
+#pragma unroll
+    for (int i = 0; i < kPagesPerLane; ++i) {
+      const int64_t page = first + 32 * i;
+      free_[i] = __ballot_sync(0xffffffffu, page < num_pages && __ldcg(refs + page) == 0);
+      count += __popc(free_[i]);
+    }
+    int total;
+    int at = got + block_sum(lane == 31 ? count : 0, s_warps, &total);   // lane 31 has the warp's last place
+    at = __shfl_sync(0xffffffffu, at, 31) - count;
+#pragma unroll
+    for (int i = 0; i < kPagesPerLane; ++i) {
+      const int place = at + __popc(free_[i] & ((1u << lane) - 1u));
+      if (((free_[i] >> lane) & 1u) && place < want) list[place] = int32_t(first + 32 * i);
+      at += __popc(free_[i]);
+    }
+    got = min(got + total, want);
+  }
+  return got;
+}
+
+__global__ void __launch_bounds__(kPagesThreads) cache_resize_kernel(const PagesParams p) {
+  __shared__ int s_warps[kPagesWarps];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t room = int64_t(p.width) << p.page_shift;
+  // 0: left alone or bad, else pages held and needed
+  auto row_of = [&](int r, int* have, int* need) -> bool {
+    const int now = p.lens[r], then = __ldg(p.new_lens + r);
+    if (then < 0) return false;
+    if (now < 0 || now > room || then > room) {
+      set_status(p.status, TSEL_DEV_REQUESTS);
+      return false;
+    }
+    *have = ceil_pages(now, p.page_shift);
+    *need = ceil_pages(then, p.page_shift);
+    return true;
+  };
+  int want = 0;   // pages for the rows so far
+  for (int base = 0; base < p.rows; base += kPagesThreads) {
+    const int r = base + int(threadIdx.x);
+    int have = 0, need = 0;
+    const int more = r < p.rows && row_of(r, &have, &need) ? max(need - have, 0) : 0;
+    int total;
+    const int up_to = want + block_sum(more, s_warps, &total);
+    if (r < p.rows) p.plan[r] = up_to - more;
+    want += total;
+  }
+  const int found = free_pages(p.refs, p.num_pages, want, p.found, s_warps);
+  __syncthreads();   // plan, found
+  for (int r = warp; r < p.rows; r += kPagesWarps) {
+    int have = 0, need = 0;
+    if (!row_of(r, &have, &need)) continue;
+    int32_t* row = p.table + r * p.table_stride;
+    const int first = p.plan[r];
+    if (need > have && first + (need - have) > found) {   // not enough: the row stays as it is
+      if (lane == 0) set_status(p.status, TSEL_DEV_PAGES);
+      continue;
+    }
+    for (int i = have + lane; i < need; i += 32) {
+      const int page = p.found[first + i - have];
+      row[i] = page;
+      p.refs[page] = 1;
+    }
+    for (int i = need + lane; i < have; i += 32) {
+      const int page = row[i];
+      if (page < 0 || page >= p.num_pages) {
+        set_status(p.status, TSEL_DEV_PAGES);
+      } else if (atomicSub(p.refs + page, 1) <= 0) {
+        atomicAdd(p.refs + page, 1);
+        set_status(p.status, TSEL_DEV_PAGES);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) p.lens[r] = __ldg(p.new_lens + r);
+  }
+}
+
+// Fresh pages for the children whose parent's last page is not full. plan[i]: that
+// page, -1 none needed, -2 no child.
+__global__ void __launch_bounds__(kPagesThreads) fork_plan_kernel(const PagesParams p) {
+  __shared__ int s_warps[kPagesWarps];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t room = int64_t(p.width) << p.page_shift;
+  const int mask = (1 << p.page_shift) - 1;
+  int want = 0;
+  for (int base = 0; base < p.n; base += kPagesThreads) {
+    const int i = base + int(threadIdx.x);
+    int state = -2;   // no child, no page, a page
+    if (i < p.n) {
+      const int src = __ldg(p.parents + i), dst = __ldg(p.children + i);
+      bool ok = src >= 0 && src < p.rows && dst >= 0 && dst < p.rows && (i == 0 || dst > __ldg(p.children + i - 1));
+      if (ok) {   // no child is a parent
+        int lo = 0, hi = p.n;
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (__ldg(p.children + mid) < src) lo = mid + 1;
+          else hi = mid;
+        }
+        ok = lo >= p.n || __ldg(p.children + lo) != src;
+      }
+      const int len = ok ? __ldcg(p.lens + src) : 0;
+      ok = ok && len >= 0 && len <= room && __ldcg(p.lens + dst) == 0;
+      if (!ok) {
+        set_status(p.status, TSEL_DEV_REQUESTS);
+      } else if ((len & mask) == 0) {
+        state = -1;
+      } else {
+        const int last = __ldcg(p.table + src * p.table_stride + (len >> p.page_shift));
+        if (last < 0 || last >= p.num_pages) set_status(p.status, TSEL_DEV_PAGES);
+        else state = 0;
+      }
+    }
+    int total;
+    const int up_to = want + block_sum(state == 0 ? 1 : 0, s_warps, &total);
+    if (i < p.n) p.plan[i] = state == 0 ? up_to - 1 : state;
+    want += total;
+  }
+  const int found = free_pages(p.refs, p.num_pages, want, p.found, s_warps);
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.n; i += kPagesThreads) {
+    int at = p.plan[i];
+    if (at >= found) {
+      set_status(p.status, TSEL_DEV_PAGES);
+      at = -2;
+    } else if (at >= 0) {
+      at = p.found[at];
+      p.refs[at] = 1;
+    }
+    p.plan[i] = at;
+  }
+  // lengths last: a child's own is read above as the sign that it holds nothing
+  __syncthreads();
+  for (int i = threadIdx.x; i < p.n; i += kPagesThreads)
+    if (p.plan[i] != -2) p.lens[__ldg(p.children + i)] = __ldcg(p.lens + __ldg(p.parents + i));
+}
+
+// A child's list of pages, their counts, and the rows of its last page.
+__global__ void __launch_bounds__(kMoveThreads) fork_copy_kernel(const PagesParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int i = int(blockIdx.x / unsigned(p.parts)), part = int(blockIdx.x - unsigned(i) * unsigned(p.parts));
+  const int fresh = __ldcg(p.plan + i);
+  if (fresh == -2) return;
+  const int32_t* from = p.table + __ldg(p.parents + i) * p.table_stride;
+  const int dst = __ldg(p.children + i);
+  int32_t* to = p.table + dst * p.table_stride;
+  const int len = __ldcg(p.lens + dst), whole = len >> p.page_shift, rest = len & ((1 << p.page_shift) - 1);
+  for (int x = part * kMoveThreads + int(threadIdx.x); x < whole; x += p.parts * kMoveThreads) {
+    const int page = __ldcg(from + x);
+    to[x] = page;
+    if (page < 0 || page >= p.num_pages) set_status(p.status, TSEL_DEV_PAGES);
+    else atomicAdd(p.refs + page, 1);
+  }
+  if (fresh < 0 || rest == 0) return;
+  if (part == 0 && threadIdx.x == 0) to[whole] = fresh;
+  const int old = __ldcg(from + whole);
+  if (old < 0 || old >= p.num_pages) return;
+  const int bytes = rest * p.d;
+  for (int h = part; h < 2 * p.Hkv; h += p.parts) {   // the rows in use of a head are one piece
+    const bool v = h >= p.Hkv;
+    const int hh = v ? h - p.Hkv : h;
+    uint8_t* pages = v ? p.v_pages : p.k_pages;
+    uint8_t* exps = v ? p.v_exps : p.k_exps;
+    const int64_t a = (int64_t(old) * p.Hkv + hh) << p.page_shift, b = (int64_t(fresh) * p.Hkv + hh) << p.page_shift;
+    const uint4* src = reinterpret_cast<const uint4*>(pages + a * p.d);
+    uint4* out = reinterpret_cast<uint4*>(pages + b * p.d);
+#pragma unroll 4
+    for (int x = threadIdx.x; x < bytes / 16; x += kMoveThreads) out[x] = __ldcg(src + x);
+    if (int(threadIdx.x) < rest) exps[b + threadIdx.x] = __ldcg(exps + a + threadIdx.x);
+  }
+}
+
+}  // namespace
+
+void move_plan(MoveParams& p, int want) {
+  const int all = 2 * p.Hkv, row = p.d / 16;
+  p.heads = all < kMoveHeads ? all : kMoveHeads;
+  p.pieces = row;
+  // CTAs of a request: first by heads, then by pieces of 32 bytes or more (a sector)
+  auto parts = [&]() { return int64_t(p.R) * ceil_div(all, p.heads) * ceil_div(row, p.pieces); };
+  auto size = [&]() {
+    const int groups = kMoveThreads / p.pieces;
+    p.tokens = groups * kMoveItems / p.heads;
+    p.chunks = p.dst_table == nullptr ? 1 : int(ceil_div(p.max_keep, p.tokens));
+  };
+  size();
+  if (p.dst_table == nullptr) {
+    while (p.heads > 1 && parts() < want) p.heads = (p.heads + 1) / 2;
+    while (p.pieces > 2 && parts() < want && p.max_keep > 64) p.pieces = (p.pieces + 1) / 2;
+    size();
+  }
+  p.head_parts = int(ceil_div(all, p.heads));
+  p.slices = int(ceil_div(row, p.pieces));
+}
+
+cudaError_t launch_move(const MoveParams& p, cudaStream_t stream) {
+  const int64_t grid = int64_t(p.R) * p.chunks * p.head_parts * p.slices;
+  if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  const bool in_place = p.dst_table == nullptr;
+  const size_t smem = size_t(p.tokens) * 16 * (in_place ? 3 : 1);   // 48 KB at most
+  return in_place ? launch_kernel(cache_move_kernel<true>, dim3(unsigned(grid)), kMoveThreads, smem, stream, 1, p)
+                  : launch_kernel(cache_move_kernel<false>, dim3(unsigned(grid)), kMoveThreads, smem, stream, 1, p);
+}
+
+cudaError_t launch_resize(const PagesParams& p, cudaStream_t stream) {
+  return launch_kernel(cache_resize_kernel, dim3(1), kPagesThreads, 0, stream, 1, p);
+}
+
+cudaError_t launch_fork(const PagesParams& p, cudaStream_t stream) {
+  const cudaError_t e = launch_kernel(fork_plan_kernel, dim3(1), kPagesThreads, 0, stream, 1, p);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(fork_copy_kernel, dim3(unsigned(p.n) * unsigned(p.parts)), kMoveThreads, 0, stream, 1, p);
+}
+
+}  // namespace tsel

@@ -1,0 +1,72 @@
+// Pages of the quantised cache: parameters of the kernels that move cached
+// tokens together, share pages and give them out (pages.cu).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "common.cuh"
+
+namespace tsel {
+
+constexpr int kMoveThreads = 256;
+constexpr int kMoveItems = 8;         // 16-byte pieces of a thread in flight
+constexpr int kMoveHeads = 64;        // K and V heads of a CTA, at most
+constexpr int kForkParts = 8;         // CTAs of a child
+
+struct MoveParams {
+  uint8_t* k_pages;
+  uint8_t* v_pages;
+  uint8_t* k_exps;
+  uint8_t* v_exps;
+  int num_pages, page_shift, Hkv, d;
+  const int32_t* table;
+  int64_t table_stride;
+  int width;                   // pages of a row of it
+  const int32_t* dst_table;    // null: in place
+  int64_t dst_stride;
+  int dst_width;
+  const int32_t* starts;       // [R] or null
+  const int32_t* bases;        // [R] or null
+  const int32_t* keep;
+  const int32_t* cu_keep;      // [R + 1]
+  int total, max_keep, R;
+  int32_t* new_lens;           // [R] or null
+  uint32_t* status;
+  int heads;                   // K and V heads of a CTA (of 2 Hkv)
+  int head_parts;              // CTAs that share the heads
+  int pieces, slices;          // 16-byte pieces of a CTA's rows, CTAs that share a row
+  int tokens;                  // of a chunk
+  int chunks;                  // of a request; 1 in place, where a CTA walks them itself
+};
+
+struct PagesParams {
+  int32_t* refs;
+  int num_pages, page_shift;
+  int32_t* table;
+  int64_t table_stride;
+  int rows, width;
+  int32_t* lens;
+  const int32_t* new_lens;     // resize
+  const int32_t* parents;      // fork
+  const int32_t* children;
+  int n;
+  uint8_t* k_pages;
+  uint8_t* v_pages;
+  uint8_t* k_exps;
+  uint8_t* v_exps;
+  int Hkv, d;
+  int parts;                   // CTAs of a child
+  int32_t* plan;               // [rows + 1]
+  int32_t* found;              // [rows * width]
+  uint32_t* status;
+};
+
+// Sizes of a compaction's launch; CTAs enough for `want` where there is work.
+void move_plan(MoveParams& p, int want);
+cudaError_t launch_move(const MoveParams& p, cudaStream_t stream);
+cudaError_t launch_resize(const PagesParams& p, cudaStream_t stream);
+cudaError_t launch_fork(const PagesParams& p, cudaStream_t stream);
+
+}  // namespace tsel

@@ -77,6 +77,7 @@ typedef enum tsel_status {
                                     infinity written to the cache */
 #define TSEL_DEV_PAGES     0x20u /* page index or cache slot out of range */
 #define TSEL_DEV_POSITIONS 0x40u /* rope table names an axis the positions do not have */
+#define TSEL_DEV_PARENTS   0x80u /* a tree's node does not come after its parent */
 
 /* total_keep value of tsel_select_topk when the budgets were computed on the
  * device (tsel_dynamic_budget): keep_idx then has room for total_tokens. */
@@ -543,6 +544,104 @@ TSEL_API tsel_status tsel_cache_read(const uint8_t* k_pages, const uint8_t* v_pa
                                      void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Pages of the cache: kept tokens together, sharing, giving out             */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Moves the cached rows of kept tokens together ([VTC] section 3.2: after pruning
+ * the cache holds the kept tokens): accepted drafts, or a cached prompt pruned by
+ * the selection. For request r and k below n = cu_keep[r+1] - cu_keep[r], the row
+ * at position
+ *   starts[r] + keep_idx[cu_keep[r] + k] - bases[r]   of its pages goes to
+ *   starts[r] + k                                     of the pages of dst_table,
+ * codes and scale bytes unchanged, and new_lens[r] = starts[r] + n.
+ *
+ * page_table    int32 device, row r at page_table + r * page_table_stride,
+ *               pages_per_req pages in order. The pages of a request must differ.
+ * dst_table     the same for the destinations, which must be no page that the
+ *               call reads; NULL: in place, the pages of page_table. In place
+ *               those pages must be the request's own (tsel_cache_fork shares them).
+ * starts, bases int32 [num_req] device, NULL for zeros. E.g. starts = the length
+ *               without the drafted tokens and keep_idx = the accepted nodes; or
+ *               bases = req_tok_offsets with the outputs of tsel_select_topk.
+ * keep_idx      int32 [total_keep] device: ascending in each request, none below
+ *               bases[r]; others set TSEL_DEV_KEEP_IDX and are skipped (so are
+ *               positions past the request's pages).
+ * cu_keep       int32 [num_req + 1] device: 0, monotone, at most max_keep each,
+ *               the last at most total_keep. A request that breaks these, or whose
+ *               kept tokens do not fit its destination's pages, sets
+ *               TSEL_DEV_REQUESTS and is left as it is.
+ * new_lens      int32 [num_req] device or NULL; not starts itself.
+ * workspace     >= tsel_cache_workspace_size() bytes (status).
+ * Pages outside the cache set TSEL_DEV_PAGES; their tokens are skipped. Rows that
+ * are no destination keep what they hold.
+ */
+TSEL_API tsel_status tsel_cache_compact(uint8_t* k_pages, uint8_t* v_pages, uint8_t* k_exps, uint8_t* v_exps,
+                                        int num_pages, int page_size, const int32_t* page_table,
+                                        int64_t page_table_stride, int pages_per_req, const int32_t* dst_table,
+                                        int64_t dst_table_stride, int dst_pages_per_req, const int32_t* starts,
+                                        const int32_t* bases, const int32_t* keep_idx, const int32_t* cu_keep,
+                                        int num_req, int total_keep, int max_keep, int num_kv_heads, int head_dim,
+                                        int32_t* new_lens, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace tsel_cache_resize and tsel_cache_fork need for a table of
+ * these sizes (0 for sizes they do not take). */
+TSEL_API size_t tsel_cache_resize_workspace_size(int num_rows, int pages_per_row);
+
+/*
+ * Gives pages to requests that grow and takes them back from requests that
+ * shrink or end. refs[page] counts the requests that hold a page; 0: free. Row r
+ * of page_table holds ceil(lens[r] / page_size) pages; afterwards it holds
+ * ceil(new_lens[r] / page_size), and lens[r] = new_lens[r]. A negative new_lens[r]
+ * leaves its row alone.
+ *   Growing rows get the free pages of the lowest numbers, in the order of the
+ * rows, each with count 1; pages given back by this call are not among them. Where
+ * they run out, that row and the growing ones after it stay as they are and
+ * TSEL_DEV_PAGES is set.
+ *   Shrinking rows lower the counts of the pages past their new length; the
+ * entries stay in the table. A page outside the cache, or one whose count is 0
+ * already, sets TSEL_DEV_PAGES and is passed over.
+ *
+ * refs        int32 [num_pages] device.
+ * page_table  int32 device, row r at page_table + r * page_table_stride,
+ *             pages_per_row entries; num_rows * pages_per_row at most 2^31 - 1.
+ * lens        int32 [num_rows] device, in and out; new_lens int32 [num_rows]
+ *             device. Lengths past the row's pages set TSEL_DEV_REQUESTS; the row
+ *             stays as it is.
+ * workspace   >= tsel_cache_resize_workspace_size(num_rows, pages_per_row).
+ * Deterministic; one CTA, for the pages that change hands between steps.
+ */
+TSEL_API tsel_status tsel_cache_resize(int32_t* refs, int num_pages, int page_size, int32_t* page_table,
+                                       int64_t page_table_stride, int num_rows, int pages_per_row, int32_t* lens,
+                                       const int32_t* new_lens, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
+/*
+ * Lets requests start from others' cached tokens (several answers to one prompt):
+ * row children[i] gets the pages of row parents[i]. Whole pages are shared
+ * (refs + 1); where the parent's last page is not full the child gets a free one
+ * (the lowest numbers, in the order of i, count 1) and the rows in use are copied
+ * into it, so that both can be written behind them. lens[children[i]] becomes
+ * lens[parents[i]]. Pages of tsel_cache_new; refs, page_table, lens as in
+ * tsel_cache_resize.
+ *
+ * parents, children  int32 [num_forks] device, rows of page_table: children
+ *             ascending, of length 0, none of them a parent in the same call
+ *             (else TSEL_DEV_REQUESTS, and that child is left as it is).
+ *             num_forks at most num_rows.
+ * A child for which no page is free is left as it is (TSEL_DEV_PAGES); so is one
+ * whose parent's last page is outside the cache. Other pages outside the cache are
+ * noted in the child's row and flagged.
+ * workspace   >= tsel_cache_resize_workspace_size(num_rows, pages_per_row).
+ */
+TSEL_API tsel_status tsel_cache_fork(uint8_t* k_pages, uint8_t* v_pages, uint8_t* k_exps, uint8_t* v_exps,
+                                     int num_pages, int page_size, int num_kv_heads, int head_dim, int32_t* refs,
+                                     int32_t* page_table, int64_t page_table_stride, int num_rows,
+                                     int pages_per_row, int32_t* lens, const int32_t* parents,
+                                     const int32_t* children, int num_forks, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Attention over a shared prefix                                           */
 /* ------------------------------------------------------------------------ */
 
@@ -607,6 +706,43 @@ TSEL_API size_t tsel_prefix_attention_workspace_size(int num_req, int total_q, i
 TSEL_API tsel_status tsel_prefix_attention(
     const void* q, int64_t q_row_stride, const int32_t* cu_seqlens_q, int num_req, int total_q,
     int max_seqlen_q, const uint8_t* k_pages, const uint8_t* v_pages, const uint8_t* k_exps,
+    const uint8_t* v_exps, int num_pages, int page_size, const int32_t* prefix_pages,
+    const int32_t* prefix_len, int max_prefix_len, const int32_t* page_table,
+    int64_t page_table_stride, const int32_t* suffix_lens, int max_suffix_len, int num_heads,
+    int num_kv_heads, int head_dim, int dtype, float softmax_scale, void* out,
+    int64_t out_row_stride, float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Attention of drafted trees                                               */
+/* ------------------------------------------------------------------------ */
+
+/* Bytes of workspace tsel_tree_attention needs for these sizes (0 for sizes it
+ * does not take). */
+TSEL_API size_t tsel_tree_attention_workspace_size(int num_req, int total_q, int max_nodes,
+                                                   int num_heads, int num_kv_heads, int head_dim,
+                                                   int max_prefix_len, int max_suffix_len);
+
+/*
+ * tsel_prefix_attention for drafted tokens that form a tree in each request, so
+ * that one pass checks several continuations: query row i of request r is node
+ * i of its tree, and the request's last n suffix keys are those of its n nodes,
+ * in order. Node i sees the prefix, the suffix keys before the tree, its ancestors
+ * and itself.
+ *
+ * parents   int32 [total_q] device: a node's parent as an index into the same
+ *           request's nodes, or -1 for a root; a parent comes before its
+ *           children. Anything else sets TSEL_DEV_PARENTS; the node is then a root.
+ * max_nodes at most 64; the rows cu_seqlens_q[r] .. of a request are its nodes,
+ *           at most max_nodes and at most suffix_lens[r] of them (else
+ *           TSEL_DEV_SEQLENS).
+ * All else as in tsel_prefix_attention (a tree whose node i hangs on i - 1 gives
+ * its results). Keys that a node does not see never reach it, with that call's
+ * one exception; the tokens that are accepted can be moved together by
+ * tsel_cache_compact.
+ */
+TSEL_API tsel_status tsel_tree_attention(
+    const void* q, int64_t q_row_stride, const int32_t* cu_seqlens_q, int num_req, int total_q,
+    int max_nodes, const int32_t* parents, const uint8_t* k_pages, const uint8_t* v_pages, const uint8_t* k_exps,
     const uint8_t* v_exps, int num_pages, int page_size, const int32_t* prefix_pages,
     const int32_t* prefix_len, int max_prefix_len, const int32_t* page_table,
     int64_t page_table_stride, const int32_t* suffix_lens, int max_suffix_len, int num_heads,

@@ -1,0 +1,72 @@
+"""Plain simulation of the cache's pages (numpy; test infrastructure). Every
+function changes its arrays in place; the cache is a list of arrays [pages, Hkv,
+page_size, ...]."""
+from __future__ import annotations
+
+import numpy as np
+
+
+def _pages(n, page_size):
+    return -(-n // page_size)
+
+
+def compact(cache, table, starts, bases, keep, cu, dst_table=None):
+    """Returns the new lengths."""
+    page = cache[0].shape[2]
+    to = table if dst_table is None else dst_table
+    lens = np.zeros(len(cu) - 1, np.int64)
+    for r in range(len(cu) - 1):
+        rows = [[a[table[r, p // page], :, p % page].copy() for a in cache]
+                for p in (starts[r] + keep[j] - bases[r] for j in range(cu[r], cu[r + 1]))]
+        for k, row in enumerate(rows):
+            at = starts[r] + k
+            for a, x in zip(cache, row):
+                a[to[r, at // page], :, at % page] = x
+        lens[r] = starts[r] + len(rows)
+    return lens
+
+
+def resize(refs, table, lens, new_lens, page_size):
+    """False where pages ran out."""
+    free = iter(np.flatnonzero(refs == 0).tolist())
+    left, ok = int((refs == 0).sum()), True
+    refs0 = refs.copy()
+    for r in range(len(lens)):
+        if new_lens[r] < 0:
+            continue
+        have, need = _pages(lens[r], page_size), _pages(new_lens[r], page_size)
+        if need > have:
+            ok = ok and need - have <= left
+            if not ok:
+                continue
+            left -= need - have
+            for i in range(have, need):
+                page = next(free)
+                assert refs0[page] == 0
+                table[r, i] = page
+                refs[page] = 1
+        for i in range(need, have):
+            refs[table[r, i]] -= 1
+        lens[r] = new_lens[r]
+    return ok
+
+
+def fork(cache, refs, table, lens, parents, children):
+    """Children without a page stay as they are."""
+    page = cache[0].shape[2]
+    free = iter(np.flatnonzero(refs == 0).tolist())
+    for p, c in zip(parents, children):
+        n, whole = lens[p], lens[p] // page
+        if n % page:
+            fresh = next(free, None)
+            if fresh is None:
+                continue
+            for a in cache:
+                a[fresh, :, :n % page] = a[table[p, whole], :, :n % page]
+            refs[fresh] = 1
+        table[c, :whole] = table[p, :whole]
+        if n % page:
+            table[c, whole] = fresh
+        for i in range(whole):
+            refs[table[p, i]] += 1
+        lens[c] = n

@@ -1,0 +1,264 @@
+"""GPU: cached tokens moved together, pages shared, given out and back, against a
+plain simulation. Everything here is moved or counted, so results are exact."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import i32
+from oracle import pages_oracle as O
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def tsel():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import attention_score_vision_gb300 as t
+    t.build()
+    t.load_library()
+    return t
+
+
+def _cache(tsel, rng, pages, page, Hkv, d):
+    """A cache of random bytes and its host copy."""
+    host = [rng.integers(0, 256, (pages, Hkv, page, d), dtype=np.uint8) for _ in range(2)]
+    host += [rng.integers(0, 256, (pages, Hkv, page), dtype=np.uint8) for _ in range(2)]
+    return tsel.TselCache(*[torch.from_numpy(a.copy()).cuda() for a in host]), host
+
+
+def _same(cache, host):
+    for a, b in zip(cache, host):
+        assert np.array_equal(a.cpu().numpy(), b)
+
+
+def _ws(tsel, n=1024):
+    return torch.zeros(n, dtype=torch.uint8, device="cuda")
+
+
+COMPACT = [
+    # kept counts, page, Hkv, d, start, span of positions, in place
+    ([1], 16, 1, 64, 0, 1, True),
+    ([0, 3, 0], 16, 2, 80, 7, 20, True),
+    ([6, 1, 4, 6], 64, 8, 128, 100, 32, True),
+    ([400], 16, 8, 128, 0, 700, True),              # one request: few CTAs, many chunks
+    ([900, 2, 333], 32, 1, 96, 5, 1100, True),
+    ([57] * 40, 128, 3, 112, 130, 64, True),
+    ([700, 1, 0, 250], 16, 4, 128, 3, 900, False),
+    ([1500], 64, 1, 64, 0, 1501, False),
+    ([5], 32, 40, 128, 0, 8, False),                # more heads than a CTA takes
+    ([33, 33], 32, 40, 128, 1, 40, True),
+    ([1300], 16, 1, 64, 0, 5000, True),
+    ([2500], 128, 2, 80, 11, 2500, True),           # nothing moves
+]
+
+
+@pytest.mark.parametrize("case", COMPACT, ids=[str(i) for i in range(len(COMPACT))])
+def test_compact(tsel, case):
+    counts, page, Hkv, d, start, span, in_place = case
+    rng = np.random.default_rng(len(counts) * 1000 + page + d)
+    R = len(counts)
+    starts = np.asarray([start + r for r in range(R)], np.int32)
+    bases = np.asarray([1000 * r for r in range(R)], np.int32)
+    keep = np.concatenate([np.sort(rng.permutation(span)[:n]) + b for n, b in zip(counts, bases)]).astype(np.int32)
+    cu = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    width = -(-(start + R + span) // page)
+    order = rng.permutation(2 * R * width + 2).astype(np.int32)
+    table = order[:R * width].reshape(R, width)
+    to = None if in_place else order[R * width:2 * R * width].reshape(R, width)
+    cache, host = _cache(tsel, rng, len(order), page, Hkv, d)
+    ws = _ws(tsel)
+    lens = tsel.tsel_cache_compact(cache, i32(table), i32(keep), i32(cu), max(counts), starts=i32(starts), bases=i32(bases),
+                                   dst_table=None if to is None else i32(to), workspace=ws)
+    assert tsel.tsel_read_device_status(ws) == 0
+    want = O.compact(host, table, starts, bases, keep, cu, to)
+    assert np.array_equal(lens.cpu().numpy(), want)
+    _same(cache, host)
+
+
+def test_compact_chains_of_moves_in_place(tsel):
+    """Every token's destination is the next one's source: the hardest order."""
+    rng = np.random.default_rng(5)
+    n, page = 3000, 16
+    width = -(-(n + 1) // page)
+    table = rng.permutation(width).astype(np.int32)[None]
+    for Hkv, d in ((1, 64), (8, 128)):
+        cache, host = _cache(tsel, rng, width, page, Hkv, d)
+        keep = np.arange(1, n + 1, dtype=np.int32)
+        tsel.tsel_cache_compact(cache, i32(table), i32(keep), i32([0, n]), n)
+        O.compact(host, table, [0], [0], keep, [0, n])
+        _same(cache, host)
+
+
+def test_compact_flags_and_skips(tsel):
+    rng = np.random.default_rng(6)
+    page, width = 16, 4
+    table = np.arange(12, dtype=np.int32).reshape(3, 4)
+    cache, host = _cache(tsel, rng, 12, page, 2, 64)
+    ws = _ws(tsel)
+    bits = lambda: (tsel.tsel_read_device_status(ws), tsel.tsel_clear_device_status(ws))[0]
+
+    def call(keep, cu, most=8, starts=None, table=table):
+        return tsel.tsel_cache_compact(cache, i32(table), i32(keep), i32(cu), most, starts=None if starts is None else i32(starts), workspace=ws)
+    # not ascending: the second of the equal two is skipped, the others move
+    call([1, 3, 3, 9], [0, 0, 4, 4])
+    assert bits() == tsel.TSEL_DEV_KEEP_IDX
+    for p, k in ((1, 0), (3, 1), (9, 3)):
+        for a in host:
+            a[4, :, k] = a[4, :, p]
+    _same(cache, host)
+    # past the pages, and below its own place
+    call([63, 64], [0, 0, 0, 2])
+    assert bits() == tsel.TSEL_DEV_KEEP_IDX
+    for a in host:
+        a[8, :, 0] = a[11, :, 15]
+    _same(cache, host)
+    call([-1], [0, 1, 1, 1])
+    assert bits() == tsel.TSEL_DEV_KEEP_IDX
+    # counts that are no counts
+    for cu, most in (([0, 2, 1, 1], 8), ([1, 1, 1, 1], 8), ([0, 5, 5, 5], 4), ([0, 0, 0, 3], 8)):
+        call([1, 2], cu, most)
+        assert bits() & tsel.TSEL_DEV_REQUESTS
+    call([0], [0, 1, 1, 1], starts=[-1, 0, 0])
+    assert bits() & tsel.TSEL_DEV_REQUESTS
+    call([0], [0, 1, 1, 1], starts=[64, 0, 0])
+    assert bits() & tsel.TSEL_DEV_REQUESTS
+    torch.cuda.synchronize()
+    # pages that are none
+    bad = table.copy()
+    bad[0, 1], bad[1, 2] = -3, 12
+    before = [a.clone() for a in cache]
+    call([20, 40], [0, 1, 2, 2], table=bad)
+    assert bits() == tsel.TSEL_DEV_PAGES
+    for a, b in zip(cache, before):
+        assert torch.equal(a, b)
+
+
+def test_compact_of_nothing(tsel):
+    rng = np.random.default_rng(7)
+    cache, host = _cache(tsel, rng, 2, 16, 1, 64)
+    lens = tsel.tsel_cache_compact(cache, i32([[0], [1]]), i32([]), i32([0, 0, 0]), 0, starts=i32([3, 9]))
+    assert lens.tolist() == [3, 9]
+    assert tsel.tsel_cache_compact(cache, i32(np.zeros((0, 1))), i32([]), i32([0]), 0).numel() == 0
+    _same(cache, host)
+
+
+# ------------------------------------------------------------------ pages
+
+def _state(rng, rows, width, pages, page, lens):
+    """Rows that hold pages of their own."""
+    order = rng.permutation(pages).astype(np.int32)
+    table = np.full((rows, width), -1, np.int32)
+    refs, at = np.zeros(pages, np.int32), 0
+    for r, n in enumerate(lens):
+        k = -(-n // page)
+        table[r, :k] = order[at:at + k]
+        refs[order[at:at + k]] = 1
+        at += k
+    return table, refs, np.asarray(lens, np.int32)
+
+
+@pytest.mark.parametrize("rows,width,pages,page", [(1, 3, 5, 16), (7, 20, 150, 32), (300, 9, 20000, 128), (1500, 4, 3000, 16), (3, 5000, 40000, 16)])
+def test_resize(tsel, rows, width, pages, page):
+    rng = np.random.default_rng(rows + pages)
+    some = min(width, pages // (2 * rows))
+    table, refs, lens = _state(rng, rows, width, pages, page, rng.integers(0, some * page + 1, rows).tolist())
+    dev = [i32(x) for x in (refs, table, lens)]
+    ws = _ws(tsel, tsel.tsel_cache_resize_workspace_size(rows, width))
+    for step in range(6):
+        new = rng.integers(-1 if step else 0, width * page + 1 if step % 2 else some * page + 1, rows).astype(np.int32)
+        new[rng.random(rows) < 0.3] = -1
+        tsel.tsel_cache_resize(dev[0], dev[1], dev[2], i32(new), page, workspace=ws)
+        ok = O.resize(refs, table, lens, new, page)
+        assert tsel.tsel_read_device_status(ws) == (0 if ok else tsel.TSEL_DEV_PAGES)
+        tsel.tsel_clear_device_status(ws)
+        for a, b in zip(dev, (refs, table, lens)):
+            assert np.array_equal(a.cpu().numpy(), b)
+    tsel.tsel_cache_resize(dev[0], dev[1], dev[2], i32(np.zeros(rows)), page, workspace=ws)
+    assert not dev[0].any() and not dev[2].any()
+
+
+def test_resize_flags(tsel):
+    refs, table, lens = i32([1, 0, 0, 1]), i32([[0, -1], [3, 9]]), i32([16, 32])
+    ws = _ws(tsel, tsel.tsel_cache_resize_workspace_size(2, 2))
+    tsel.tsel_cache_resize(refs, table, lens, i32([33, -1]), 16, workspace=ws)   # past the row
+    assert tsel.tsel_read_device_status(ws) == tsel.TSEL_DEV_REQUESTS
+    tsel.tsel_clear_device_status(ws)
+    assert lens.tolist() == [16, 32] and refs.tolist() == [1, 0, 0, 1]
+    tsel.tsel_cache_resize(refs, table, lens, i32([-1, 0]), 16, workspace=ws)    # page 9 is none
+    assert tsel.tsel_read_device_status(ws) == tsel.TSEL_DEV_PAGES
+    tsel.tsel_clear_device_status(ws)
+    assert lens.tolist() == [16, 0] and refs.tolist() == [1, 0, 0, 0]
+    lens.fill_(16)
+    tsel.tsel_cache_resize(refs, table, lens, i32([-1, 0]), 16, workspace=ws)    # page 3 is free already
+    assert tsel.tsel_read_device_status(ws) == tsel.TSEL_DEV_PAGES
+    assert refs.tolist() == [1, 0, 0, 0]
+
+
+@pytest.mark.parametrize("lens,children,page,Hkv,d", [([1], 1, 16, 1, 64), ([48, 17, 0, 160], 3, 16, 2, 80), ([1370] * 5, 9, 64, 8, 128), ([127, 129, 128], 40, 128, 3, 96)])
+def test_fork_grow_and_end(tsel, lens, children, page, Hkv, d):
+    rng = np.random.default_rng(len(lens) + children + page)
+    P = len(lens)
+    kids = P * children
+    width = -(-(max(lens) + 2 * page) // page)
+    pages = sum(-(-n // page) for n in lens) + 4 * kids
+    table, refs, lens = _state(rng, P + kids, width, pages, page, lens + [0] * kids)
+    cache, host = _cache(tsel, rng, pages, page, Hkv, d)
+    parents = np.asarray([i % P for i in range(kids)], np.int32)
+    kid = np.arange(P, P + kids, dtype=np.int32)
+    dev = [i32(x) for x in (refs, table, lens)]
+    ws = _ws(tsel, tsel.tsel_cache_resize_workspace_size(P + kids, width))
+
+    def check():
+        assert tsel.tsel_read_device_status(ws) == 0
+        _same(cache, host)
+        for a, b in zip(dev, (refs, table, lens)):
+            assert np.array_equal(a.cpu().numpy(), b)
+    tsel.tsel_cache_fork(cache, *dev, i32(parents), i32(kid), workspace=ws)
+    O.fork(host, refs, table, lens, parents, kid)
+    check()
+    new = np.where(np.arange(P + kids) < P, -1, lens + rng.integers(0, 2 * page, P + kids)).astype(np.int32)
+    tsel.tsel_cache_resize(*dev, i32(new), page, workspace=ws)
+    assert O.resize(refs, table, lens, new, page)
+    check()
+    new = np.where(np.arange(P + kids) % 2 == 0, 0, -1).astype(np.int32)     # some parents end before their children
+    tsel.tsel_cache_resize(*dev, i32(new), page, workspace=ws)
+    O.resize(refs, table, lens, new, page)
+    check()
+    tsel.tsel_cache_resize(*dev, i32(np.zeros(P + kids)), page, workspace=ws)
+    assert not dev[0].any()
+
+
+def test_fork_refuses_and_runs_out(tsel):
+    rng = np.random.default_rng(9)
+    table, refs, lens = _state(rng, 5, 3, 6, 16, [20, 32, 0, 0, 0])      # two free pages
+    cache, host = _cache(tsel, rng, 6, 16, 1, 64)
+    dev = [i32(x) for x in (refs, table, lens)]
+    ws = _ws(tsel, tsel.tsel_cache_resize_workspace_size(5, 3))
+    bits = lambda: (tsel.tsel_read_device_status(ws), tsel.tsel_clear_device_status(ws))[0]
+
+    def unchanged():
+        _same(cache, host)
+        for a, b in zip(dev, (refs, table, lens)):
+            assert np.array_equal(a.cpu().numpy(), b)
+    for parents, children in (([5], [2]), ([-1], [2]), ([0], [5]), ([0], [1]), ([0], [0]), ([2], [2])):
+        tsel.tsel_cache_fork(cache, *dev, i32(parents), i32(children), workspace=ws)
+        assert bits() == tsel.TSEL_DEV_REQUESTS
+        unchanged()
+    # the same child twice: the second is refused; a child that is a parent too: refused
+    tsel.tsel_cache_fork(cache, *dev, i32([1, 0]), i32([2, 2]), workspace=ws)
+    assert bits() == tsel.TSEL_DEV_REQUESTS
+    O.fork(host, refs, table, lens, [1], [2])
+    unchanged()
+    tsel.tsel_cache_fork(cache, *dev, i32([3, 1]), i32([3, 4]), workspace=ws)
+    assert bits() == tsel.TSEL_DEV_REQUESTS
+    O.fork(host, refs, table, lens, [1], [4])
+    unchanged()
+    # three children, two pages
+    table, refs, lens = _state(rng, 5, 3, 6, 16, [20, 32, 0, 0, 0])
+    dev = [i32(x) for x in (refs, table, lens)]
+    tsel.tsel_cache_fork(cache, *dev, i32([0, 0, 0]), i32([2, 3, 4]), workspace=ws)
+    assert bits() == tsel.TSEL_DEV_PAGES
+    O.fork(host, refs, table, lens, [0, 0, 0], [2, 3, 4])
+    assert lens.tolist() == [20, 32, 20, 20, 0]
+    unchanged()
