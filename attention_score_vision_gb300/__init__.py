@@ -1062,7 +1062,8 @@ def _attend_cache(q, cu_seqlens_q, max_seqlen_q, parents, cache, prefix_pages, p
         _vector(lse, _F32, "lse", index, H * tq)
     if out is not None or lse is not None:
         _written(out, lse)
-    nbytes = 0 if workspace is not None else tsel_prefix_attention_workspace_size(R, tq, max_q, H, Hkv, d, max_p, max_s)
+    size = tsel_prefix_attention_workspace_size if parents is None else tsel_tree_attention_workspace_size
+    nbytes = 0 if workspace is not None else size(R, tq, max_q, H, Hkv, d, max_p, max_s)
     workspace = _workspace(workspace, nbytes, index, stream)
     if out is None:
         out = _like(q, stream)

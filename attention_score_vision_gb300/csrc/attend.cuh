@@ -85,11 +85,12 @@ inline int att_chunks(int64_t base, int tiles, int ctas, bool narrow, int least)
 }
 
 // `two`: units of 16 rows even where 8 would do.
-inline AttPart att_part(int64_t requests, int tokens, int max_keys, int Hkv, int G, int tt, bool two, int* slots) {
+inline AttPart att_part(int64_t requests, int tokens, int max_keys, int Hkv, int G, int tt, bool two, int* slots,
+                        int narrow_rows = kAttNarrowRows) {
   AttPart a{};
   const int64_t rows = int64_t(tokens) * G;
   const bool few = max_keys > kAttNarrowKeys && requests * Hkv < kAttWideCtas;
-  a.narrow = rows > (few ? kAttNarrowRowsLong : kAttNarrowRows) ? 0 : (rows > 8 || two ? 2 : 1);
+  a.narrow = rows > (few ? kAttNarrowRowsLong : narrow_rows) ? 0 : (rows > 8 || two ? 2 : 1);
   a.groups = int(a.narrow ? ceil_div(rows, 8 * a.narrow) : ceil_div(tokens, 2 * tt));
   a.slot0 = *slots;
   const int tiles = int(ceil_div(max_keys, kTile));
@@ -101,14 +102,20 @@ inline AttPart att_part(int64_t requests, int tokens, int max_keys, int Hkv, int
   }
   a.chunks = a.narrow ? att_chunks(base, tiles, a.narrow == 1 ? kAttNarrowCtas1 : kAttNarrowCtas2, true, 1)
                       : att_chunks(base, tiles, kAttWideCtas, false, int(ceil_div(tiles, kAttMaxChunkKeys / kTile)));
+#ifdef TREE_CHUNKS
+  if (narrow_rows != kAttNarrowRows && !a.narrow && tiles > TREE_CHUNKS) a.chunks = TREE_CHUNKS;
+#endif
   a.keys = int(ceil_div(tiles, a.chunks)) * kTile;
   a.units = base * a.chunks;
   *slots += a.chunks * (a.narrow ? 1 : 2);
   return a;
 }
 
+#ifndef TREE_ROWS
+#define TREE_ROWS 31
+#endif
 inline AttPlan att_plan(int R, int Tq, int max_q, int H, int Hkv, int d, int max_prefix,
-                        int max_suffix) {
+                        int max_suffix, bool tree = false) {
   AttPlan a{};
   a.G = H / Hkv;
   a.tt = kTile / a.G;
@@ -119,7 +126,7 @@ inline AttPlan att_plan(int R, int Tq, int max_q, int H, int Hkv, int d, int max
   // (called, not replayed: 24.5, 25.0, 24.4 and 25.9, 26.5, 26.5).
   const bool two = a.pre.narrow == 2 && a.pre.units > 0 &&
                    int64_t(R) * Hkv * ceil_div(max_suffix, kTile) <= kAttJoinedTiles;
-  a.suf = att_part(Tq > 0 ? R : 0, max_q, max_suffix, Hkv, a.G, a.tt, two, &a.slots);
+  a.suf = att_part(Tq > 0 ? R : 0, max_q, max_suffix, Hkv, a.G, a.tt, two, &a.slots, tree ? TREE_ROWS : kAttNarrowRows);
   a.too_large = a.pre.units + a.suf.units > 0x7FFFFFFFll || double(a.slots) * Tq * H * d > 1e15;
   if (a.too_large) return a;
   a.lse_off = kWsHeaderBytes;

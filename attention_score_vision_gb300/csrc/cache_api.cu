@@ -309,17 +309,24 @@ tsel_status tsel_cache_read(const uint8_t* k_pages, const uint8_t* v_pages, cons
   return e == cudaSuccess ? TSEL_OK : cuda_fail(e, "cache read launch");
 }
 
-size_t tsel_prefix_attention_workspace_size(int num_req, int total_q, int max_seqlen_q,
-                                            int num_heads, int num_kv_heads, int head_dim,
-                                            int max_prefix_len, int max_suffix_len) {
+static size_t attend_workspace(bool tree, int num_req, int total_q, int max_seqlen_q, int num_heads, int num_kv_heads,
+                               int head_dim, int max_prefix_len, int max_suffix_len) {
   if (num_req < 0 || total_q < 0 || max_seqlen_q < 0 || num_kv_heads < 1 ||
       num_heads < num_kv_heads || num_heads > 256 || num_heads % num_kv_heads != 0 ||
       num_heads / num_kv_heads > kTile || !cache_head_dim(head_dim) || max_prefix_len < 0 ||
-      max_suffix_len < 0 || max_prefix_len > kAttMaxKeys || max_suffix_len > kAttMaxKeys)
+      max_suffix_len < 0 || max_prefix_len > kAttMaxKeys || max_suffix_len > kAttMaxKeys ||
+      (tree && max_seqlen_q > kAttTreeNodes))
     return 0;
   const AttPlan a = att_plan(num_req, total_q, max_seqlen_q, num_heads, num_kv_heads, head_dim,
-                             max_prefix_len, max_suffix_len);
+                             max_prefix_len, max_suffix_len, tree);
   return a.too_large ? 0 : size_t(a.total);
+}
+
+size_t tsel_prefix_attention_workspace_size(int num_req, int total_q, int max_seqlen_q,
+                                            int num_heads, int num_kv_heads, int head_dim,
+                                            int max_prefix_len, int max_suffix_len) {
+  return attend_workspace(false, num_req, total_q, max_seqlen_q, num_heads, num_kv_heads, head_dim,
+                          max_prefix_len, max_suffix_len);
 }
 
 // Both attentions over the cache; `parents` (and `tree`) are the tree's.
@@ -361,7 +368,7 @@ static tsel_status attend_cache(
                 (long long)page_table_stride, max_suffix_len);
   TSEL_TRY(check_header(workspace, workspace_bytes));
   const AttPlan a = att_plan(num_req, total_q, max_seqlen_q, num_heads, num_kv_heads, head_dim,
-                             max_prefix_len, max_suffix_len);
+                             max_prefix_len, max_suffix_len, tree);
   if (a.too_large) return fail(TSEL_ERR_UNSUPPORTED, "too many units of work");
   if (workspace_bytes < size_t(a.total))
     return fail(TSEL_ERR_WORKSPACE, "workspace %zu < %lld bytes", workspace_bytes, (long long)a.total);
@@ -440,9 +447,8 @@ tsel_status tsel_prefix_attention(
 
 size_t tsel_tree_attention_workspace_size(int num_req, int total_q, int max_nodes, int num_heads, int num_kv_heads,
                                           int head_dim, int max_prefix_len, int max_suffix_len) {
-  return max_nodes > kAttTreeNodes ? 0
-                                   : tsel_prefix_attention_workspace_size(num_req, total_q, max_nodes, num_heads, num_kv_heads,
-                                                                          head_dim, max_prefix_len, max_suffix_len);
+  return attend_workspace(true, num_req, total_q, max_nodes, num_heads, num_kv_heads, head_dim, max_prefix_len,
+                          max_suffix_len);
 }
 
 tsel_status tsel_tree_attention(

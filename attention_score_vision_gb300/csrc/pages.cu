@@ -18,7 +18,10 @@
 // cache_resize_kernel, fork_plan_kernel. Reference counts are whole numbers added
 // with atomics, so their order does not matter; free pages (count 0) are found by
 // one CTA that walks the counts 8,192 at a time until it has enough, and go, lowest
-// first, to rows in order: results are deterministic.
+// first, to rows in order: results are deterministic. Pages given back are a launch
+// of their own, a CTA for each row: one SM adds about one scattered count a clock
+// (256 rows of up to 289 pages freed in the first launch's CTA: 50 us, in CTAs of
+// their own 17).
 #include "launch_util.cuh"
 #include "pages.cuh"
 
@@ -29,7 +32,7 @@ namespace {
 __device__ __forceinline__ int ceil_pages(int n, int shift) { return int((int64_t(n) + (1 << shift) - 1) >> shift); }
 
 template <bool IN_PLACE>
-__global__ void __launch_bounds__(kMoveThreads) cache_move_kernel(const MoveParams p) {
+__global__ void __launch_bounds__(kMoveThreads, MC) cache_move_kernel(const MoveParams p) {
   extern __shared__ int64_t s_rows[];   // [chunk mod 3][source, destination][tokens]: rows of head 0, -1 none
   pdl_wait();
   pdl_launch_dependents();
@@ -194,29 +197,30 @@ __device__ int free_pages(const int32_t* refs, int num_pages, int want, int32_t*
   return got;
 }
 
+// Pages that row r holds and needs; false where it is left alone or bad.
+__device__ __forceinline__ bool resized_row(const PagesParams& p, int r, int* have, int* need) {
+  const int64_t room = int64_t(p.width) << p.page_shift;
+  const int now = p.lens[r], then = __ldg(p.new_lens + r);
+  if (then < 0) return false;
+  if (now < 0 || now > room || then > room) {
+    set_status(p.status, TSEL_DEV_REQUESTS);
+    return false;
+  }
+  *have = ceil_pages(now, p.page_shift);
+  *need = ceil_pages(then, p.page_shift);
+  return true;
+}
+
 __global__ void __launch_bounds__(kPagesThreads) cache_resize_kernel(const PagesParams p) {
   __shared__ int s_warps[kPagesWarps];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t room = int64_t(p.width) << p.page_shift;
-  // 0: left alone or bad, else pages held and needed
-  auto row_of = [&](int r, int* have, int* need) -> bool {
-    const int now = p.lens[r], then = __ldg(p.new_lens + r);
-    if (then < 0) return false;
-    if (now < 0 || now > room || then > room) {
-      set_status(p.status, TSEL_DEV_REQUESTS);
-      return false;
-    }
-    *have = ceil_pages(now, p.page_shift);
-    *need = ceil_pages(then, p.page_shift);
-    return true;
-  };
   int want = 0;   // pages for the rows so far
   for (int base = 0; base < p.rows; base += kPagesThreads) {
     const int r = base + int(threadIdx.x);
     int have = 0, need = 0;
-    const int more = r < p.rows && row_of(r, &have, &need) ? max(need - have, 0) : 0;
+    const int more = r < p.rows && resized_row(p, r, &have, &need) ? max(need - have, 0) : 0;
     int total;
     const int up_to = want + block_sum(more, s_warps, &total);
     if (r < p.rows) p.plan[r] = up_to - more;
@@ -226,7 +230,7 @@ __global__ void __launch_bounds__(kPagesThreads) cache_resize_kernel(const Pages
   __syncthreads();   // plan, found
   for (int r = warp; r < p.rows; r += kPagesWarps) {
     int have = 0, need = 0;
-    if (!row_of(r, &have, &need)) continue;
+    if (!resized_row(p, r, &have, &need) || need < have) continue;
     int32_t* row = p.table + r * p.table_stride;
     const int first = p.plan[r];
     if (need > have && first + (need - have) > found) {   // not enough: the row stays as it is
@@ -238,18 +242,31 @@ __global__ void __launch_bounds__(kPagesThreads) cache_resize_kernel(const Pages
       row[i] = page;
       p.refs[page] = 1;
     }
-    for (int i = need + lane; i < have; i += 32) {
-      const int page = row[i];
-      if (page < 0 || page >= p.num_pages) {
-        set_status(p.status, TSEL_DEV_PAGES);
-      } else if (atomicSub(p.refs + page, 1) <= 0) {
-        atomicAdd(p.refs + page, 1);
-        set_status(p.status, TSEL_DEV_PAGES);
-      }
-    }
     __syncwarp();
     if (lane == 0) p.lens[r] = __ldg(p.new_lens + r);
   }
+}
+
+// The rows that shrink, a CTA each.
+__global__ void __launch_bounds__(kMoveThreads) cache_shrink_kernel(const PagesParams p) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int r = int(blockIdx.x);
+  int have = 0, need = 0;
+  const bool shrinks = resized_row(p, r, &have, &need) && need < have;
+  __syncthreads();   // every thread has read the length
+  if (!shrinks) return;
+  const int32_t* row = p.table + r * p.table_stride;
+  for (int i = need + int(threadIdx.x); i < have; i += kMoveThreads) {
+    const int page = row[i];
+    if (page < 0 || page >= p.num_pages) {
+      set_status(p.status, TSEL_DEV_PAGES);
+    } else if (atomicSub(p.refs + page, 1) <= 0) {
+      atomicAdd(p.refs + page, 1);
+      set_status(p.status, TSEL_DEV_PAGES);
+    }
+  }
+  if (threadIdx.x == 0) p.lens[r] = __ldg(p.new_lens + r);
 }
 
 // Fresh pages for the children whose parent's last page is not full. plan[i]: that
@@ -381,7 +398,9 @@ cudaError_t launch_move(const MoveParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_resize(const PagesParams& p, cudaStream_t stream) {
-  return launch_kernel(cache_resize_kernel, dim3(1), kPagesThreads, 0, stream, 1, p);
+  const cudaError_t e = launch_kernel(cache_resize_kernel, dim3(1), kPagesThreads, 0, stream, 1, p);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(cache_shrink_kernel, dim3(unsigned(p.rows)), kMoveThreads, 0, stream, 1, p);
 }
 
 cudaError_t launch_fork(const PagesParams& p, cudaStream_t stream) {

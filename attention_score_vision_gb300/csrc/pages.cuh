@@ -11,7 +11,13 @@
 namespace tsel {
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveItems = 8;         // 16-byte pieces of a thread in flight
+#ifndef MI
+#define MI 4
+#endif
+#ifndef MC
+#define MC 6
+#endif
+constexpr int kMoveItems = MI;         // 16-byte pieces of a thread in flight
 constexpr int kMoveHeads = 64;        // K and V heads of a CTA, at most
 constexpr int kForkParts = 8;         // CTAs of a child
 

@@ -14,14 +14,15 @@
 // are cut into chunks only where units are few; attend.cu's join then adds the
 // chunks up.
 //
-// Roles of a CTA (12 warps):
+// Roles of a CTA (14 warps):
 //   - producer: decodes units into a ring and loads Q tiles and steps of 64 keys
 //     of K and V by TMA (128-byte swizzle; columns past the head dimension and
 //     rows past the tensor read as zeros);
-//   - two issuers, one for each row tile: S = Q K^T (64 columns) and O += P V, both
-//     tcgen05 with fp32 accumulators in TMEM. A row tile has 256 columns: O 128,
-//     S 64, and two places of 32 for P, so that the next S product waits only until
-//     the softmax has S in registers, never for the O product that reads P;
+//   - four issuers, one for each product of a row tile: S = Q K^T (64 columns) and
+//     O += P V, both tcgen05 with fp32 accumulators in TMEM. A row tile has 256
+//     columns: O, S 64 (twice up to heads of 96), and P 32 beside S (twice but for heads
+//     of 80 and 96), so that the next S product waits only until the softmax has S in
+//     registers, never for the O product that reads P;
 //   - four softmax warps for each row tile, a thread to a row: P = 2^(S c - m) goes
 //     to TMEM as the A operand of the second product. The reference m may lag the
 //     row's maximum by 2^9; past that O is rescaled in TMEM;
@@ -43,7 +44,10 @@ namespace tsel {
 
 namespace {
 
-constexpr float kPromptSlack = 9.f;   // the reference may lag the row maximum by 2^9
+// A row's reference moves when its P of a step add up to more than this: none of
+// them is then past fp16's range, and the reference lags the row's maximum by
+// less than 2^15 (bf16; 2^9 in fp16, whose P are 2^6 at the reference).
+constexpr float kPromptMost = 32768.f;
 constexpr int kPromptRing = 3;        // units in flight
 
 struct PromptUnit {
@@ -63,16 +67,21 @@ struct PromptCfg {
   static constexpr int Q_BYTES = DC * kTile * 128;
   static constexpr int ST_BYTES = DC * kPromptStep * 128;       // one step of K or V
   static constexpr int KS = 8 / DC;                             // stages of each
+  // TMEM columns of a row tile: two places for S where O leaves room, else two for P
+  static constexpr int NS = D <= 64 ? 2 : 1, NP = 2;
+  static constexpr int COL_P = 64 * NS, COL_O = COL_P + 32 * NP;
+  static_assert(COL_O + D <= 256, "half of TMEM");
   static constexpr int SOFT_WARPS = 8;
-  static constexpr int MMA_WARP = SOFT_WARPS;                   // two
-  static constexpr int LOAD_WARP = MMA_WARP + 2;
+  static constexpr int MMA_WARP = SOFT_WARPS;                   // [product][row tile]
+  static constexpr int LOAD_WARP = MMA_WARP + 4;
   static constexpr int FIX_WARP = LOAD_WARP + 1;
   static constexpr int THREADS = 32 * (FIX_WARP + 1);
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = 2 * Q_BYTES;
   static constexpr int OFF_V = OFF_K + KS * ST_BYTES;
-  static constexpr int OFF_BAR = OFF_V + KS * ST_BYTES;
-  static constexpr int NUM_BARS = 4 + 5 * KS + 4 + 8 + 2 + 2 + 2 * kPromptRing;
+  static constexpr int OFF_OUT = OFF_V + KS * ST_BYTES;         // 64 bytes of each row of the softmax warps
+  static constexpr int OFF_BAR = OFF_OUT + SOFT_WARPS * 32 * 64;
+  static constexpr int NUM_BARS = 4 + 5 * KS + 4 * NS + 4 * NP + 2 + 4 + 2 * kPromptRing;
   static constexpr int OFF_UNITS = OFF_BAR + 8 * NUM_BARS;
   static constexpr int OFF_BAD = OFF_UNITS + kPromptRing * int(sizeof(PromptUnit));   // int [ring]
   static constexpr int OFF_ORDER = OFF_BAD + 4 * kPromptRing;   // int [sorted], then int [sorted]
@@ -103,16 +112,66 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "memory");
 }
 
+// exp2 of both halves of x, added to acc with one packed add and packed in the type
+// of V: in one piece, so that the two results need no moves to become a pair.
+template <bool FP16>
+__device__ __forceinline__ uint32_t exp_add_pack(float2 x, float2& acc) {
+  uint32_t h;
+  float2 r;
+#define TSEL_EXP_ADD_PACK(CVT)                                \
+  asm("{\n\t.reg .f32 e0, e1;\n\t.reg .b64 t, s, d;\n\t"     \
+      "ex2.approx.ftz.f32 e0, %3;\n\t"                        \
+      "ex2.approx.ftz.f32 e1, %4;\n\t"                        \
+      "mov.b64 t, {e0, e1};\n\t"                              \
+      "mov.b64 s, {%5, %6};\n\t"                              \
+      "add.rn.f32x2 d, s, t;\n\t"                             \
+      "mov.b64 {%0, %1}, d;\n\t" CVT " %2, e1, e0;\n\t}"      \
+      : "=f"(r.x), "=f"(r.y), "=r"(h)                         \
+      : "f"(x.x), "f"(x.y), "f"(acc.x), "f"(acc.y))
+  if (FP16) TSEL_EXP_ADD_PACK("cvt.rn.f16x2.f32");
+  else TSEL_EXP_ADD_PACK("cvt.rn.bf16x2.f32");
+#undef TSEL_EXP_ADD_PACK
+  acc = r;
+  return h;
+}
+
 // 2^(S c + shift) of 32 columns, added up in acc and packed.
 template <bool FP16>
 __device__ __forceinline__ void prompt_exp32(const uint32_t (&r)[32], float2 c2, float2 s2, float2& acc, uint32_t (&h)[16]) {
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const float2 a = __ffma2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), c2, s2);
-    const float2 e = make_float2(ex2(a.x), ex2(a.y));
-    acc = __fadd2_rn(acc, e);
-    h[j] = pack16<FP16>(e.x, e.y);
-  }
+  for (int j = 0; j < 16; ++j)
+    h[j] = exp_add_pack<FP16>(__ffma2_rn(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), c2, s2), acc);
+}
+
+// warp_wait() of barriers that have usually come: one test, with the vote taken on
+// its predicate, before the bounded waits. (warp_wait alone costs 200 clocks where
+// the barrier has come, and a step has several on its way.)
+__device__ __forceinline__ bool prompt_wait(uint64_t* bar, uint32_t parity, const volatile int* abort_flag, uint64_t timeout_ns) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "vote.sync.all.pred p, p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0 || warp_wait(bar, parity, abort_flag, timeout_ns);
+}
+__device__ __forceinline__ bool prompt_wait2(uint64_t* bar, uint32_t parity, uint64_t* bar2, uint32_t parity2,
+                                             const volatile int* abort_flag, uint64_t timeout_ns) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "and.pred p, p, q;\n\t"
+      "vote.sync.all.pred p, p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(smem_u32(bar2)), "r"(parity2)
+      : "memory");
+  return done != 0 || (warp_wait(bar, parity, abort_flag, timeout_ns) && warp_wait(bar2, parity2, abort_flag, timeout_ns));
 }
 
 // Two values of V of which one is an infinity or NaN: a mask of those halves.
@@ -132,7 +191,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     prompt_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                   const __grid_constant__ CUtensorMap mv, const PromptParams p) {
   using C = PromptCfg<D>;
-  constexpr int KS = C::KS;
+  constexpr int KS = C::KS, NS = C::NS, NP = C::NP;
   constexpr float kLift = FP16 ? 6.f : 0.f;   // P at the row's reference: fp16's range goes further down from there
   extern __shared__ uint8_t smem_dyn[];
   uint8_t* smem = smem_dyn + ((1024u - (smem_u32(smem_dyn) & 1023u)) & 1023u);
@@ -144,13 +203,13 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
   uint64_t* v_in = k_free + KS;         // loaded
   uint64_t* v_full = v_in + KS;         // looked through
   uint64_t* v_free = v_full + KS;
-  uint64_t* s_full = v_free + KS;       // [row tile] S in TMEM
-  uint64_t* s_free = s_full + 2;        // S in registers
-  uint64_t* p_full = s_free + 2;        // [row tile][place] P in TMEM
-  uint64_t* o_done = p_full + 4;        // [row tile][place] O product done
-  uint64_t* o_free = o_done + 4;        // [row tile] O of the unit in registers
-  uint64_t* drained = o_free + 2;       // [row tile] every product done
-  uint64_t* u_full = drained + 2;       // [ring]
+  uint64_t* s_full = v_free + KS;       // [row tile][place] S in TMEM
+  uint64_t* s_free = s_full + 2 * NS;   // S in registers
+  uint64_t* p_full = s_free + 2 * NS;   // [row tile][place] P in TMEM
+  uint64_t* o_done = p_full + 2 * NP;   // O product done
+  uint64_t* o_free = o_done + 2 * NP;   // [row tile] O of the unit in registers
+  uint64_t* drained = o_free + 2;       // [issuer] every product done
+  uint64_t* u_full = drained + 4;       // [ring]
   uint64_t* u_free = u_full + kPromptRing;
   PromptUnit* s_units = reinterpret_cast<PromptUnit*>(smem + C::OFF_UNITS);
   volatile int* s_bad = reinterpret_cast<volatile int*>(smem + C::OFF_BAD);   // the unit's V had infinities or NaN taken out
@@ -173,18 +232,20 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       for (int i = 0; i < 2; ++i) {
         mbar_init(&q_full[i], 1);
         mbar_init(&q_free[i], 1);
+        mbar_init(&o_free[i], 4);
+      }
+      for (int i = 0; i < 2 * NS; ++i) {
         mbar_init(&s_full[i], 1);
         mbar_init(&s_free[i], 4);
-        mbar_init(&o_free[i], 4);
-        mbar_init(&drained[i], 1);
       }
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2 * NP; ++i) {
         mbar_init(&p_full[i], 4);
         mbar_init(&o_done[i], 1);
       }
+      for (int i = 0; i < 4; ++i) mbar_init(&drained[i], 1);
       for (int i = 0; i < kPromptRing; ++i) {
         mbar_init(&u_full[i], 1);
-        mbar_init(&u_free[i], C::SOFT_WARPS + 2 + 1);   // softmax, issuers, V warp
+        mbar_init(&u_free[i], C::SOFT_WARPS + 4 + 1);   // softmax, issuers, V warp
       }
       *abort_flag = 0;
       fence_barrier_init();
@@ -221,9 +282,12 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     // ------------------------------------------------------------ softmax
     const int x = warp >> 2;
     const int row = int(threadIdx.x) & (kTile - 1);
-    const uint32_t t_o = tmem + (uint32_t((warp & 3) * 32) << 16) + uint32_t(x * 256);
-    const uint32_t t_s = t_o + 128, t_p = t_o + 192;
+    const uint32_t t_s = tmem + (uint32_t((warp & 3) * 32) << 16) + uint32_t(x * 256);
+    const uint32_t t_p = t_s + C::COL_P, t_o = t_s + C::COL_O;
+    uint8_t* stage = smem + C::OFF_OUT + warp * (32 * 64);
     uint32_t J = 0, slot = 0, turn = 0;   // steps of this row tile so far, place and turn of the unit ring
+    // the O product of step i
+    auto o_wait = [&](uint32_t i) -> bool { return prompt_wait(&o_done[NP * x + i % NP], (i / NP) & 1u, abort_flag, T); };
     bool ok = true;
     for (;;) {
       if (!warp_wait(&u_full[slot], turn & 1u, abort_flag, T)) {
@@ -239,71 +303,81 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       const int min_end = int(__reduce_min_sync(0xffffffffu, row_ok ? unsigned(end) : 0x7FFFFFFFu));
       float m = kNegInf, l = 0.f;
       for (int j = 0; j < n; ++j, ++J) {
-        if (!warp_wait(&s_full[x], J & 1u, abort_flag, T)) {
+        // S, and P's place, free once the O product that read it last is complete (a
+        // unit's first steps: the unit before has waited for its own)
+        uint64_t* const there = &s_full[NS * x + J % NS];
+        if (j < NP ? !prompt_wait(there, (J / NS) & 1u, abort_flag, T)
+                   : !prompt_wait2(there, (J / NS) & 1u, &o_done[NP * x + J % NP], (J / NP + 1) & 1u, abort_flag, T)) {
           ok = false;
           break;
         }
         tc_fence_after();
         uint32_t r0[32], r1[32];
-        tmem_ld32_async(t_s, r0);
-        tmem_ld32_async(t_s + 32, r1);
+        tmem_ld32_async(t_s + 64 * (J % NS), r0);
+        tmem_ld32_async(t_s + 64 * (J % NS) + 32, r1);
         tmem_wait_ld(r0);
         tmem_wait_ld(r1);
         tc_fence_before();
         __syncwarp();
-        mbar_arrive_lane0(&s_free[x], lane);
+        mbar_arrive_lane0(&s_free[NS * x + J % NS], lane);
         if ((j + 1) * kPromptStep > min_end) {
           mask_cols(r0, end - j * kPromptStep);
           mask_cols(r1, end - j * kPromptStep - 32);
         }
-        const float top = fmaxf(cols_max(r0), cols_max(r1)) * p.c;
-        if (__any_sync(0xffffffffu, top > m + kPromptSlack)) {
-          float s = 1.f;
-          if (top > m) {   // also the rows that could still wait: once here, it costs nothing
-            s = ex2(m - top);   // 0 at the row's first visible keys
-            l *= s;
-            m = top;
-          }
-          if (j > 0) {   // once the O product of the step before is complete
-            if (!warp_wait(&o_done[2 * x + ((J - 1) & 1u)], ((J - 1) >> 1) & 1u, abort_flag, T)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
+        // P against the reference that is there; a step that it does not suit is
+        // done again, so that no maximum is looked for in the others
+        float sum;
+        bool moves = j == 0;
 #pragma unroll 1
-            for (int cc = 0; cc < D; cc += 16) {
-              uint32_t o[16];
-              tmem_ld16(t_o + cc, o);
+        for (;;) {
+          if (moves) {
+            const float top = fmaxf(cols_max(r0), cols_max(r1)) * p.c;
+            float s = 1.f;
+            if (top > m) {   // also the rows that could still wait: once here, it costs nothing
+              s = ex2(m - top);   // 0 at the row's first visible keys
+              l *= s;
+              m = top;
+            }
+            if (j > 0) {   // once the O product of the step before is complete
+              if (!o_wait(J - 1)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+#pragma unroll 1
+              for (int cc = 0; cc < D; cc += 16) {
+                uint32_t o[16];
+                tmem_ld16(t_o + cc, o);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * s);
-              tmem_st16(t_o + cc, o);
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * s);
+                tmem_st16(t_o + cc, o);
+              }
             }
           }
+          const float shift = m == kNegInf ? 0.f : kLift - m;
+          const float2 c2 = make_float2(p.c, p.c), s2 = make_float2(shift, shift);
+          float2 a0 = make_float2(0.f, 0.f), a1 = a0;
+          uint32_t h[16];
+          prompt_exp32<FP16>(r0, c2, s2, a0, h);
+          tmem_st16(t_p + 32 * (J % NP), h);
+          prompt_exp32<FP16>(r1, c2, s2, a1, h);
+          tmem_st16(t_p + 32 * (J % NP) + 16, h);
+          a0 = __fadd2_rn(a0, a1);
+          sum = a0.x + a0.y;
+          if (moves) break;
+          moves = __any_sync(0xffffffffu, (m == kNegInf && j * kPromptStep < end) || !(sum <= kPromptMost));
+          if (!moves) break;
         }
-        const float shift = m == kNegInf ? 0.f : kLift - m;
-        const float2 c2 = make_float2(p.c, p.c), s2 = make_float2(shift, shift);
-        float2 a0 = make_float2(0.f, 0.f), a1 = a0;
-        uint32_t h0[16], h1[16];
-        prompt_exp32<FP16>(r0, c2, s2, a0, h0);
-        prompt_exp32<FP16>(r1, c2, s2, a1, h1);
-        // the place of P is free once the O product of two steps before is complete
-        if (j >= 2 && !warp_wait(&o_done[2 * x + (J & 1u)], ((J >> 1) + 1) & 1u, abort_flag, T)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        tmem_st16(t_p + 32 * (J & 1u), h0);
-        tmem_st16(t_p + 32 * (J & 1u) + 16, h1);
-        a0 = __fadd2_rn(a0, a1);
-        l += a0.x + a0.y;
+        if (!ok) break;
+        l += sum;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        mbar_arrive_lane0(&p_full[2 * x + (J & 1u)], lane);
+        mbar_arrive_lane0(&p_full[NP * x + J % NP], lane);
       }
       if (!ok) break;
       if (n > 0) {
-        if (!warp_wait(&o_done[2 * x + ((J - 1) & 1u)], ((J - 1) >> 1) & 1u, abort_flag, T)) {
+        if (!o_wait(J - 1)) {
           ok = false;
           break;
         }
@@ -311,17 +385,20 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       }
       const int head = u.kvh * p.G + row % p.G;
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const bool bad = s_bad[slot] != 0;
+      const bool bad = s_bad[slot] != 0 && row_ok && l != 0.f;
       const float lse2 = l == 0.f ? kNegInf : m + (log2f(l) - kLift);
-      float* part = nullptr;
-      if (p.part_lse != nullptr) {
-        const int64_t at = (int64_t(u.chunk) * p.Tq + tok) * p.H + head;
-        if (row_ok) p.part_lse[at] = lse2;
-        part = p.part_o + at * D;
-      } else if (row_ok && p.lse != nullptr) {
-        p.lse[int64_t(head) * p.Tq + tok] = lse2 * 0.69314718055994531f;
+      const bool part = p.part_lse != nullptr;
+      int64_t at;   // of the row's results, -1: not written
+      if (part) {
+        const int64_t r = (int64_t(u.chunk) * p.Tq + tok) * p.H + head;
+        if (row_ok) p.part_lse[r] = lse2;
+        at = row_ok && l != 0.f ? r * D : -1;
+      } else {
+        if (row_ok && p.lse != nullptr) p.lse[int64_t(head) * p.Tq + tok] = lse2 * 0.69314718055994531f;
+        at = row_ok ? int64_t(tok) * p.out_stride + int64_t(head) * D : -1;
       }
-      uint16_t* out = static_cast<uint16_t*>(p.out) + int64_t(tok) * p.out_stride + int64_t(head) * D;
+      // 64 bytes of each row at a time through shared memory, so that four lanes
+      // store them together
 #pragma unroll 1
       for (int cc = 0; cc < D; cc += 16) {
         uint32_t o[16];
@@ -329,7 +406,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         float f[16];
 #pragma unroll
         for (int k = 0; k < 16; ++k) f[k] = n > 0 && l != 0.f ? __uint_as_float(o[k]) * inv : 0.f;
-        if (bad && row_ok && l != 0.f) {   // infinities and NaN of the V rows that this row sees
+        if (bad) {   // infinities and NaN of the V rows that this row sees
           const uint16_t* v = static_cast<const uint16_t*>(p.v) + int64_t(u.k_base + c0) * p.v_stride + int64_t(u.kvh) * D + cc;
           for (int j = u.fix * kPromptStep; j < end; ++j) {
 #pragma unroll
@@ -339,20 +416,35 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
             }
           }
         }
-        if (row_ok) {
-          if (part != nullptr) {
-            if (l != 0.f) {
+        auto put = [&](int unit, uint4 w) {
+          *reinterpret_cast<uint4*>(stage + lane * 64 + ((unit ^ ((lane >> 1) & 3)) << 4)) = w;
+        };
+        // `units` 16-byte pieces of each row to dst + row's place
+        auto flush = [&](uint8_t* dst, int bytes, int units) {
+          __syncwarp();
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                *reinterpret_cast<float4*>(part + cc + 4 * k) = make_float4(f[4 * k], f[4 * k + 1], f[4 * k + 2], f[4 * k + 3]);
-            }
-          } else {
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              *reinterpret_cast<uint4*>(out + cc + 8 * k) =
-                  make_uint4(pack16<FP16>(f[8 * k], f[8 * k + 1]), pack16<FP16>(f[8 * k + 2], f[8 * k + 3]),
-                             pack16<FP16>(f[8 * k + 4], f[8 * k + 5]), pack16<FP16>(f[8 * k + 6], f[8 * k + 7]));
+          for (int k = 0; k < 4; ++k) {
+            const int i = 32 * k + lane, r = i / units, un = i - r * units;
+            const int64_t to = __shfl_sync(0xffffffffu, at, r & 31);
+            if (r < 32 && to >= 0)
+              *reinterpret_cast<uint4*>(dst + to * bytes + 16 * un) =
+                  *reinterpret_cast<const uint4*>(stage + r * 64 + ((un ^ ((r >> 1) & 3)) << 4));
           }
+          __syncwarp();
+        };
+        if (part) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            put(k, make_uint4(__float_as_uint(f[4 * k]), __float_as_uint(f[4 * k + 1]), __float_as_uint(f[4 * k + 2]), __float_as_uint(f[4 * k + 3])));
+          flush(reinterpret_cast<uint8_t*>(p.part_o + cc), 4, 4);
+        } else {
+          const int odd = (cc >> 4) & 1;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            put(2 * odd + k, make_uint4(pack16<FP16>(f[8 * k], f[8 * k + 1]), pack16<FP16>(f[8 * k + 2], f[8 * k + 3]),
+                                        pack16<FP16>(f[8 * k + 4], f[8 * k + 5]), pack16<FP16>(f[8 * k + 6], f[8 * k + 7])));
+          if (odd) flush(reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.out) + cc - 16), 2, 4);
+          else if (cc + 16 == D) flush(reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.out) + cc), 2, 2);
         }
       }
       tc_fence_before();
@@ -370,16 +462,14 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     }
   } else if (warp < C::LOAD_WARP) {
     // ------------------------------------------------------------ issuers
-    const int x = __shfl_sync(0xffffffffu, warp, 0) - C::MMA_WARP;
-    constexpr uint32_t kIdS = idesc_f16_f32(kTile, kPromptStep, false, !FP16);
-    constexpr uint32_t kIdO = idesc_f16_f32(kTile, D, true, !FP16);
-    const uint32_t t_o = __shfl_sync(0xffffffffu, tmem, 0) + uint32_t(x * 256);
-    const uint32_t t_s = t_o + 128, t_p = t_o + 192;
-    // advanced by (bytes >> 4)
-    const uint64_t dq = smem_desc(smem_u32(smem + C::OFF_Q) + x * C::Q_BYTES, 2, 1024);
-    const uint64_t dk = smem_desc(smem_u32(smem + C::OFF_K), 2, 1024);
-    const uint64_t dv = smem_desc_mn(smem_u32(smem + C::OFF_V), kPromptStep * 128, 1024);
-    uint32_t J = 0, ks = 0, vs = 0, slot = 0, turn = 0;   // steps of this row tile; K and V steps of the CTA; unit ring
+    // A warp for each product of a row tile: with one for both, the next S product
+    // waited behind the O product's issue (300 clocks of every step).
+    const int who = __shfl_sync(0xffffffffu, warp, 0) - C::MMA_WARP;
+    const int x = who & 1;
+    const bool second = who >= 2;   // O += P V
+    const uint32_t t_s = __shfl_sync(0xffffffffu, tmem, 0) + uint32_t(x * 256);
+    const uint32_t t_p = t_s + C::COL_P, t_o = t_s + C::COL_O;
+    uint32_t J = 0, st = 0, par = 0, slot = 0, turn = 0;   // steps of this row tile; stage of K or V and its turn; unit ring
     uint32_t live = 0;                                     // units in which this row tile had steps
     bool ok = true;
     for (;;) {
@@ -396,58 +486,61 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         slot = 0;
         ++turn;
       }
-      // S of step j; steps that this row tile does not see are only let go
-      auto s_product = [&](int j) -> bool {
-        const uint32_t st = ks % KS;
-        if (!warp_wait(&k_full[st], (ks / KS) & 1u, abort_flag, T)) return false;
-        ++ks;
-        if (j >= n) {
-          mbar_arrive_lane0(&k_free[st], lane);
-          return true;
-        }
-        const uint32_t at = J + j;
-        if (at > 0 && !warp_wait(&s_free[x], (at - 1) & 1u, abort_flag, T)) return false;
-        tc_fence_after();
+      if (!second) {
+        constexpr uint32_t kIdS = idesc_f16_f32(kTile, kPromptStep, false, !FP16);
+        // advanced by (bytes >> 4)
+        const uint64_t dq = smem_desc(smem_u32(smem + C::OFF_Q) + x * C::Q_BYTES, 2, 1024);
+        const uint64_t dk = smem_desc(smem_u32(smem + C::OFF_K), 2, 1024);
+        if (n > 0) ok = prompt_wait(&q_full[x], live & 1u, abort_flag, T);
+        for (int j = 0; j < steps && ok; ++j) {
+          ok = prompt_wait(&k_full[st], par, abort_flag, T);
+          if (!ok) break;
+          if (j < n) {
+            const uint32_t at = J + j, place = at % NS;
+            ok = at < NS || prompt_wait(&s_free[NS * x + place], (at / NS + 1) & 1u, abort_flag, T);
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t a = (kk >> 2) * (kTile * 128) + (kk & 3) * 32, b = (kk >> 2) * (kPromptStep * 128) + (kk & 3) * 32;
-          mma_ss_elect(t_s, dq + (a >> 4), dk + ((st * C::ST_BYTES + b) >> 4), kIdS, kk > 0);
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t a = (kk >> 2) * (kTile * 128) + (kk & 3) * 32, b = (kk >> 2) * (kPromptStep * 128) + (kk & 3) * 32;
+              mma_ss_elect(t_s + 64 * place, dq + (a >> 4), dk + ((st * C::ST_BYTES + b) >> 4), kIdS, kk > 0);
+            }
+            commit_elect(&s_full[NS * x + place]);
+            commit_elect(&k_free[st]);
+            if (j == n - 1) commit_elect(&q_free[x]);
+          } else {   // steps that this row tile does not see are only let go
+            mbar_arrive_lane0(&k_free[st], lane);
+          }
+          if (++st == KS) {
+            st = 0;
+            par ^= 1u;
+          }
         }
-        commit_elect(&s_full[x]);
-        commit_elect(&k_free[st]);
-        if (j == n - 1) commit_elect(&q_free[x]);
-        return true;
-      };
-      if (n > 0 && !warp_wait(&q_full[x], live & 1u, abort_flag, T)) {
-        ok = false;
-        break;
-      }
-      if (steps > 0) ok = s_product(0);
-      for (int j = 0; j < steps && ok; ++j) {
-        if (j + 1 < steps) ok = s_product(j + 1);
-        if (!ok) break;
-        const uint32_t st = vs % KS;
-        if (!warp_wait(&v_full[st], (vs / KS) & 1u, abort_flag, T)) {
-          ok = false;
-          break;
-        }
-        ++vs;
-        if (j >= n) {
-          mbar_arrive_lane0(&v_free[st], lane);
-          continue;
-        }
-        const uint32_t at = J + j, place = at & 1u;
-        if (!warp_wait(&p_full[2 * x + place], (at >> 1) & 1u, abort_flag, T) ||
-            (j == 0 && live > 0 && !warp_wait(&o_free[x], (live - 1) & 1u, abort_flag, T))) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
+      } else {
+        constexpr uint32_t kIdO = idesc_f16_f32(kTile, D, true, !FP16);
+        const uint64_t dv = smem_desc_mn(smem_u32(smem + C::OFF_V), kPromptStep * 128, 1024);
+        for (int j = 0; j < steps && ok; ++j) {
+          ok = prompt_wait(&v_full[st], par, abort_flag, T);
+          if (!ok) break;
+          if (j < n) {
+            const uint32_t at = J + j, place = at % NP;
+            ok = prompt_wait(&p_full[NP * x + place], (at / NP) & 1u, abort_flag, T) &&
+                 (j > 0 || live == 0 || prompt_wait(&o_free[x], (live - 1) & 1u, abort_flag, T));
+            if (!ok) break;
+            tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < kPromptStep / 16; ++kk)
-          mma_ts_elect(t_o, t_p + 32 * place + 8 * kk, dv + ((st * C::ST_BYTES + kk * 2048) >> 4), kIdO, j > 0 || kk > 0);
-        commit_elect(&o_done[2 * x + place]);
-        commit_elect(&v_free[st]);
+            for (int kk = 0; kk < kPromptStep / 16; ++kk)
+              mma_ts_elect(t_o, t_p + 32 * place + 8 * kk, dv + ((st * C::ST_BYTES + kk * 2048) >> 4), kIdO, j > 0 || kk > 0);
+            commit_elect(&o_done[NP * x + place]);
+            commit_elect(&v_free[st]);
+          } else {
+            mbar_arrive_lane0(&v_free[st], lane);
+          }
+          if (++st == KS) {
+            st = 0;
+            par ^= 1u;
+          }
+        }
       }
       if (!ok) break;
       J += uint32_t(n);
@@ -459,8 +552,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     }
     __syncwarp();
     // every product of this warp has completed before TMEM is freed
-    commit_elect(&drained[x]);
-    wait_drain(&drained[x], 0, T);
+    commit_elect(&drained[who]);
+    wait_drain(&drained[who], 0, T);
   } else if (warp == C::LOAD_WARP) {
     // ------------------------------------------------------------ producer
     const int64_t per = int64_t(p.Hkv) * p.chunks;   // units of a block of rows

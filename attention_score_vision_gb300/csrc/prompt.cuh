@@ -34,6 +34,9 @@ inline PromptPlan prompt_plan(int seg, int Tq, int max_k, int H, int Hkv, int d)
   const int tiles = int(ceil_div(max_k, kTile));
   a.chunks = 1;
   if (base > 0 && base < kAttWideCtas && tiles > 1) a.chunks = att_chunks(base, tiles, kAttWideCtas, false, 1);
+#ifdef PCHUNKS
+  if (a.chunks > 1 && tiles > PCHUNKS) a.chunks = PCHUNKS;
+#endif
   a.keys = a.chunks > 1 ? int(ceil_div(tiles, a.chunks)) * kTile : 0x7FFFFF80;
   a.units = Hkv * (blocks + seg) * a.chunks;
   a.slots = a.chunks > 1 ? a.chunks : 0;
