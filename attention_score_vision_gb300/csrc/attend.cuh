@@ -29,6 +29,11 @@ constexpr int kAttNarrowCtas1 = 4 * 152, kAttNarrowCtas2 = 3 * 152;
 // by rows: past 32 it gives away the 2 us of a short prefix for the 28 of a long
 // one. The rows of a suffix are bounded by the longest request of the batch.
 constexpr int kAttNarrowRows = 32;
+// Trees without a prefix take it up to more rows: 16 requests of up to 61 nodes
+// over up to 4,000 keys, 16 KV heads of 80, one query head each, take 95 us, in the
+// wide kernel 103. (Beside a prefix, which takes the wide kernel's launch, 32
+// requests of up to 64 rows take 236 us that way, in the wide kernel 219.)
+constexpr int kAttNarrowRowsTree = 64;
 constexpr int kAttNarrowRowsLong = 16;         // past
 constexpr int kAttNarrowKeys = 16384;          // this many keys of few requests
 
@@ -102,18 +107,12 @@ inline AttPart att_part(int64_t requests, int tokens, int max_keys, int Hkv, int
   }
   a.chunks = a.narrow ? att_chunks(base, tiles, a.narrow == 1 ? kAttNarrowCtas1 : kAttNarrowCtas2, true, 1)
                       : att_chunks(base, tiles, kAttWideCtas, false, int(ceil_div(tiles, kAttMaxChunkKeys / kTile)));
-#ifdef TREE_CHUNKS
-  if (narrow_rows != kAttNarrowRows && !a.narrow && tiles > TREE_CHUNKS) a.chunks = TREE_CHUNKS;
-#endif
   a.keys = int(ceil_div(tiles, a.chunks)) * kTile;
   a.units = base * a.chunks;
   *slots += a.chunks * (a.narrow ? 1 : 2);
   return a;
 }
 
-#ifndef TREE_ROWS
-#define TREE_ROWS 31
-#endif
 inline AttPlan att_plan(int R, int Tq, int max_q, int H, int Hkv, int d, int max_prefix,
                         int max_suffix, bool tree = false) {
   AttPlan a{};
@@ -126,7 +125,7 @@ inline AttPlan att_plan(int R, int Tq, int max_q, int H, int Hkv, int d, int max
   // (called, not replayed: 24.5, 25.0, 24.4 and 25.9, 26.5, 26.5).
   const bool two = a.pre.narrow == 2 && a.pre.units > 0 &&
                    int64_t(R) * Hkv * ceil_div(max_suffix, kTile) <= kAttJoinedTiles;
-  a.suf = att_part(Tq > 0 ? R : 0, max_q, max_suffix, Hkv, a.G, a.tt, two, &a.slots, tree ? TREE_ROWS : kAttNarrowRows);
+  a.suf = att_part(Tq > 0 ? R : 0, max_q, max_suffix, Hkv, a.G, a.tt, two, &a.slots, tree && max_prefix == 0 ? kAttNarrowRowsTree : kAttNarrowRows);
   a.too_large = a.pre.units + a.suf.units > 0x7FFFFFFFll || double(a.slots) * Tq * H * d > 1e15;
   if (a.too_large) return a;
   a.lse_off = kWsHeaderBytes;

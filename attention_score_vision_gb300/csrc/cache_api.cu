@@ -558,6 +558,11 @@ tsel_status tsel_prompt_attention(const void* q, int64_t q_row_stride, const voi
   p.status = &reinterpret_cast<WsHeader*>(ws)->status;
   p.timeout_ns = device_wait_timeout_ns();
   const int ctas = int(a.units < sms ? a.units : sms);
+  if (a.units > kPromptDealt * int64_t(ctas) && a.units < (1ll << 30)) {
+    p.next = &reinterpret_cast<WsHeader*>(ws)->sched_ctr[0];
+    const cudaError_t z = cudaMemsetAsync(p.next, 0, sizeof(int32_t), stream);
+    if (z != cudaSuccess) return cuda_fail(z, "unit counter");
+  }
   cudaError_t e = launch_prompt(head_dim, fp16, mq, mk, mv, p, ctas, stream);
   if (e != cudaSuccess) return cuda_fail(e, "prompt attention launch");
   if (a.slots == 0) return TSEL_OK;

@@ -5,7 +5,7 @@
 //
 // cache_move_kernel. Token k of a request's kept list goes from position
 // start + keep[k] - base to start + k: cached bytes move unchanged. A thread owns
-// one 16-byte piece of rows and has eight of them in flight. A CTA covers some of
+// one 16-byte piece of rows and has three of them in flight. A CTA covers some of
 // the K and V heads (and, where requests are few, some pieces of their rows) for
 // one chunk of tokens; a chunk's row numbers are worked out once in shared memory.
 //   In place the destination of one token may be the source of another. Kept
@@ -32,7 +32,7 @@ namespace {
 __device__ __forceinline__ int ceil_pages(int n, int shift) { return int((int64_t(n) + (1 << shift) - 1) >> shift); }
 
 template <bool IN_PLACE>
-__global__ void __launch_bounds__(kMoveThreads, MC) cache_move_kernel(const MoveParams p) {
+__global__ void __launch_bounds__(kMoveThreads, kMoveCtas) cache_move_kernel(const MoveParams p) {
   extern __shared__ int64_t s_rows[];   // [chunk mod 3][source, destination][tokens]: rows of head 0, -1 none
   pdl_wait();
   pdl_launch_dependents();

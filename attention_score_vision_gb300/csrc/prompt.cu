@@ -74,8 +74,8 @@ struct PromptCfg {
   static constexpr int SOFT_WARPS = 8;
   static constexpr int MMA_WARP = SOFT_WARPS;                   // [product][row tile]
   static constexpr int LOAD_WARP = MMA_WARP + 4;
-  static constexpr int FIX_WARP = LOAD_WARP + 1;
-  static constexpr int THREADS = 32 * (FIX_WARP + 1);
+  static constexpr int FIX_WARP = LOAD_WARP + 1;   // two
+  static constexpr int THREADS = 32 * (FIX_WARP + 2);
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = 2 * Q_BYTES;
   static constexpr int OFF_V = OFF_K + KS * ST_BYTES;
@@ -174,11 +174,10 @@ __device__ __forceinline__ bool prompt_wait2(uint64_t* bar, uint32_t parity, uin
   return done != 0 || (warp_wait(bar, parity, abort_flag, timeout_ns) && warp_wait(bar2, parity2, abort_flag, timeout_ns));
 }
 
-// Two values of V of which one is an infinity or NaN: a mask of those halves.
+// Bits 15 and 31: the half's exponent is all ones (an infinity or NaN).
 template <bool FP16>
-__device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
-  const uint32_t m = FP16 ? 0x7C007C00u : 0x7F807F80u;
-  return __vcmpeq2(w & m, m);
+__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
+  return (w & (FP16 ? 0x7C007C00u : 0x7F807F80u)) + (FP16 ? 0x04000400u : 0x00800080u);
 }
 
 template <bool FP16>
@@ -226,7 +225,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         mbar_init(&k_full[i], 1);
         mbar_init(&k_free[i], 2);
         mbar_init(&v_in[i], 1);
-        mbar_init(&v_full[i], 1);
+        mbar_init(&v_full[i], 2);
         mbar_init(&v_free[i], 2);
       }
       for (int i = 0; i < 2; ++i) {
@@ -245,7 +244,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
       for (int i = 0; i < 4; ++i) mbar_init(&drained[i], 1);
       for (int i = 0; i < kPromptRing; ++i) {
         mbar_init(&u_full[i], 1);
-        mbar_init(&u_free[i], C::SOFT_WARPS + 4 + 1);   // softmax, issuers, V warp
+        mbar_init(&u_free[i], C::SOFT_WARPS + 4 + 2);   // softmax, issuers, V warps
       }
       *abort_flag = 0;
       fence_barrier_init();
@@ -562,8 +561,14 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
     uint32_t ks = 0, qn[2] = {0, 0}, slot = 0, turn = 0;
     bool ok = true;
     for (int64_t round = 0; ok; ++round) {
-      // there and back, so that no CTA has the longer unit of every round
+      // There and back, so that no CTA has the longer unit of every round; from a
+      // counter where there are many, since their times differ.
       int64_t i = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      if (p.next != nullptr && round > 0) {
+        int taken = 0;
+        if (lane == 0) taken = atomicAdd(p.next, 1);
+        i = int64_t(gridDim.x) + __shfl_sync(0xffffffffu, taken, 0);
+      }
       PromptUnit u{};
       while (first < p.seg) {
         const int at = first + lane;
@@ -697,23 +702,32 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
           break;
         }
         if (j >= u.fix) {
+          // this warp's half of the rows, the pieces of a row in any order
           const int left = u.k1 - u.c0 - j * kPromptStep;   // keys that some row sees
+          uint4* tile = reinterpret_cast<uint4*>(smem + C::OFF_V + st * C::ST_BYTES) + (warp - C::FIX_WARP) * (kPromptStep / 2) * 8;
+          const int first = (warp - C::FIX_WARP) * (kPromptStep / 2);
           uint32_t found = 0;
-          uint8_t* tile = smem + C::OFF_V + st * C::ST_BYTES;
-#pragma unroll 4
-          for (int i = lane; i < C::DC * kPromptStep * 8; i += 32) {
-            uint4* at = reinterpret_cast<uint4*>(tile + 16 * i);
-            if (((i >> 3) & (kPromptStep - 1)) >= left) {
-              *at = make_uint4(0, 0, 0, 0);
-              continue;
+#pragma unroll
+          for (int cc = 0; cc < C::DC; ++cc) {
+#pragma unroll
+            for (int i = 0; i < kPromptStep / 2 * 8 / 32; ++i) {
+              uint4* at = tile + cc * (kPromptStep * 8) + 32 * i + lane;
+              if (first + 4 * i + (lane >> 3) >= left) *at = make_uint4(0, 0, 0, 0);
+              const uint4 w = *at;
+              found |= not_finite<FP16>(w.x) | not_finite<FP16>(w.y) | not_finite<FP16>(w.z) | not_finite<FP16>(w.w);
             }
-            uint4 w = *at;
-            const uint4 b = make_uint4(not_finite2<FP16>(w.x), not_finite2<FP16>(w.y), not_finite2<FP16>(w.z), not_finite2<FP16>(w.w));
-            const uint32_t any = b.x | b.y | b.z | b.w;
-            found |= any;
-            if (any) *at = make_uint4(w.x & ~b.x, w.y & ~b.y, w.z & ~b.z, w.w & ~b.w);
           }
-          if (found) s_bad[slot] = 1;
+          if (found & 0x80008000u) {
+            s_bad[slot] = 1;
+            for (int i = lane; i < C::DC * (kPromptStep / 2) * 8; i += 32) {
+              uint32_t* at = reinterpret_cast<uint32_t*>(tile + (i >> 8) * (kPromptStep * 8) + (i & 255));
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t b = not_finite<FP16>(at[k]);
+                at[k] &= ((b & 0x8000u) ? 0u : 0xFFFFu) | ((b & 0x80000000u) ? 0u : 0xFFFF0000u);
+              }
+            }
+          }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
         __syncwarp();

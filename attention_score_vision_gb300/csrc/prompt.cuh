@@ -12,7 +12,27 @@
 namespace tsel {
 
 constexpr int kPromptStep = 64;       // keys of a step
+// Units of a CTA up to which they are dealt out; beyond, they come from a counter (a
+// memset before the launch). 24 requests of up to 1,370 rows, 14 units a CTA: 180 us
+// with it, 197 without.
+constexpr int kPromptDealt = 3;
 constexpr int kPromptSorted = 256;    // segments up to which units go longest first
+
+// Chunks for `base` units of `tiles` 128-key tiles: the count with the least
+// estimated time, in key tiles: a unit's and three for its start and end, and
+// three for joining (256 rows of 256 keys, 4 heads of 64: 8.0 us in one chunk, 10.5 in two).
+inline int prompt_chunks(int64_t base, int tiles) {
+  int best = 1;
+  double best_cost = tiles + 3.0;
+  for (int n = 2; n <= tiles && base * n <= 2 * kAttWideCtas && n <= 64; ++n) {
+    const double cost = double(ceil_div(base * n, kAttWideCtas)) * (double(ceil_div(tiles, n)) + 3.0) + 3.0 + 0.05 * n;
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = n;
+    }
+  }
+  return best;
+}
 
 struct PromptPlan {
   int G, tt;           // query heads per KV head, tokens per 128-row tile
@@ -33,10 +53,7 @@ inline PromptPlan prompt_plan(int seg, int Tq, int max_k, int H, int Hkv, int d)
   const int64_t base = Hkv * (blocks > seg ? blocks : seg);
   const int tiles = int(ceil_div(max_k, kTile));
   a.chunks = 1;
-  if (base > 0 && base < kAttWideCtas && tiles > 1) a.chunks = att_chunks(base, tiles, kAttWideCtas, false, 1);
-#ifdef PCHUNKS
-  if (a.chunks > 1 && tiles > PCHUNKS) a.chunks = PCHUNKS;
-#endif
+  if (base > 0 && base < kAttWideCtas) a.chunks = prompt_chunks(base, tiles);
   a.keys = a.chunks > 1 ? int(ceil_div(tiles, a.chunks)) * kTile : 0x7FFFFF80;
   a.units = Hkv * (blocks + seg) * a.chunks;
   a.slots = a.chunks > 1 ? a.chunks : 0;
@@ -58,6 +75,7 @@ struct PromptParams {
   int causal;
   int chunks, keys;
   float c;                     // softmax_scale * log2(e)
+  int32_t* next;               // unit counter, 0 at the start; null: units are dealt out
   float* part_lse;             // [chunks][Tq][H], base 2; null: results are written at once
   float* part_o;               // [chunks][Tq][H][d]
   void* out;
