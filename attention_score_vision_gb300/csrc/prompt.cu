@@ -14,25 +14,43 @@
 // are cut into chunks only where units are few; attend.cu's join then adds the
 // chunks up.
 //
-// Roles of a CTA (14 warps):
+// Roles of a CTA (15 warps):
 //   - producer: decodes units into a ring and loads Q tiles and steps of 64 keys
 //     of K and V by TMA (128-byte swizzle; columns past the head dimension and
 //     rows past the tensor read as zeros);
 //   - four issuers, one for each product of a row tile: S = Q K^T (64 columns) and
 //     O += P V, both tcgen05 with fp32 accumulators in TMEM. A row tile has 256
-//     columns: O, S 64 (twice up to heads of 96), and P 32 beside S (twice but for heads
-//     of 80 and 96), so that the next S product waits only until the softmax has S in
-//     registers, never for the O product that reads P;
+//     columns: O, S (twice for heads of 64) and two places for P, so that the next S
+//     product waits only until the softmax has S in registers, never for the O
+//     product that reads P;
 //   - four softmax warps for each row tile, a thread to a row: P = 2^(S c - m) goes
-//     to TMEM as the A operand of the second product. The reference m may lag the
-//     row's maximum by 2^9; past that O is rescaled in TMEM;
-//   - one warp that passes each V step on: in steps that some row does not see whole,
-//     it clears rows past the last visible key and takes infinities and NaN out (a
+//     to TMEM as the A operand of the second product. The reference m moves, and O
+//     is rescaled in TMEM, only when a row's P of a step add up to more than 2^15: no
+//     maximum is looked for before that, and the step is then done again;
+//   - two warps that pass each V step on: in steps that some row does not see whole,
+//     they clear rows past the last visible key and take infinities and NaN out (a
 //     product with P = 0 would make NaN of rows that do not see them). The rows that
-//     do see them get them back at the end.
+//     do see them get them back at the end. (One warp took 3,000 clocks a step of a
+//     causal unit's end, two 650.)
 // P is rounded to the type of V (bf16: eight bits; fp16: eleven, down to 2^-20 of
 // the reference, ending at 2^-30 of it), since both operands of a product have one
 // type; statistics, sums and O are fp32.
+//
+// What bounds it: for heads of 128 the two row tiles need 1,310 clocks of the tensor
+// cores for 64 keys (measured alone: 50 for 128 x 64 x 16 with both operands in
+// shared memory, 64 for 128 x 128 x 16 with A in TMEM) and a step takes about 1,550: the
+// softmax warps' chain, some 350 instructions at four clocks each, of which 64 are
+// exponentials (without them a step still took 85% of its time). 36,973 rows, causal,
+// 16 heads on 8 of 128: 3.70 ms, 1.51 PFLOP/s, 79% of cuBLAS's bf16 rate; images of
+// up to 4,096 tokens, 16 heads of 80: 0.90 ms for 61,585, 0.96 PFLOP/s; a packed
+// batch of 24 requests of up to 1,370 (fp16, 32 heads on 8 of 128): 162 us; there a
+// unit's end (O out of TMEM and to memory) costs as much as four steps.
+// Tried and slower, or no faster: S of 128 keys in one place for both row tiles (a
+// step of the batch 25% longer, the others 1 to 4% shorter), two warpgroups to a row
+// tile for even and odd steps (5.8 ms: the issuers' waits), two threads to a row (4.05
+// ms), more registers for the softmax (setmaxnreg; 3.85), waits that spin (3.87), the
+// row tiles half a step apart (3.74), results through shared memory 64 bytes of a row
+// at a time or a row to a thread (the same), 32 columns of O at a time (spills: 6.7).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -326,13 +344,13 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         // P against the reference that is there; a step that it does not suit is
         // done again, so that no maximum is looked for in the others
         float sum;
-        bool moves = j == 0;
+        bool moves = j == 0, mine = moves;   // the warp does it again; this row's reference moves
 #pragma unroll 1
         for (;;) {
           if (moves) {
             const float top = fmaxf(cols_max(r0), cols_max(r1)) * p.c;
             float s = 1.f;
-            if (top > m) {   // also the rows that could still wait: once here, it costs nothing
+            if (mine && top > m) {   // no other row's: what a row gives does not depend on its neighbours
               s = ex2(m - top);   // 0 at the row's first visible keys
               l *= s;
               m = top;
@@ -364,7 +382,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
           a0 = __fadd2_rn(a0, a1);
           sum = a0.x + a0.y;
           if (moves) break;
-          moves = __any_sync(0xffffffffu, (m == kNegInf && j * kPromptStep < end) || !(sum <= kPromptMost));
+          mine = end > 0 && ((m == kNegInf && j * kPromptStep < end) || !(sum <= kPromptMost));
+          moves = __any_sync(0xffffffffu, mine);
           if (!moves) break;
         }
         if (!ok) break;
