@@ -359,6 +359,8 @@ static tsel_status attend_cache(
     return fail(TSEL_ERR_UNSUPPORTED, "trees of up to %d nodes (at most %d)", max_seqlen_q, kAttTreeNodes);
   if (tree && total_q > 0 && (parents == nullptr || !aligned(parents, 4)))
     return fail(TSEL_ERR_INVALID_VALUE, "parents");
+  if (tree && total_q > 0 && max_suffix_len < 1)
+    return fail(TSEL_ERR_INVALID_VALUE, "max_suffix_len=%d: the nodes' keys are the suffix's last", max_suffix_len);
   if (max_prefix_len > 0 && (prefix_pages == nullptr || prefix_len == nullptr))
     return fail(TSEL_ERR_INVALID_VALUE, "null prefix_pages or prefix_len");
   if (max_suffix_len > 0 && num_req > 0 && (page_table == nullptr || suffix_lens == nullptr))

@@ -734,7 +734,7 @@ TSEL_API size_t tsel_tree_attention_workspace_size(int num_req, int total_q, int
  *           children. Anything else sets TSEL_DEV_PARENTS; the node is then a root.
  * max_nodes at most 64; the rows cu_seqlens_q[r] .. of a request are its nodes,
  *           at most max_nodes and at most suffix_lens[r] of them (else
- *           TSEL_DEV_SEQLENS).
+ *           TSEL_DEV_SEQLENS). max_suffix_len at least 1: a node's own key is there.
  * All else as in tsel_prefix_attention (a tree whose node i hangs on i - 1 gives
  * its results). Keys that a node does not see never reach it, with that call's
  * one exception; the tokens that are accepted can be moved together by

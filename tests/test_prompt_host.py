@@ -120,7 +120,7 @@ def _tree(lib, **over):
 
 def test_tree_host_checks(lib, tsel):
     assert _tree(lib, tq=0) == 0 and _tree(lib, tq=0, mn=64, par=0) == 0
-    for over, code in ((dict(mn=65), 2), (dict(par=0), 1), (dict(par=18), 1), (dict(mn=-1), 1), (dict(d=72), 2), (dict(pts=3), 1), (dict(q=8), 1),
+    for over, code in ((dict(mn=65), 2), (dict(par=0), 1), (dict(par=18), 1), (dict(mn=-1), 1), (dict(ms=0), 1), (dict(d=72), 2), (dict(pts=3), 1), (dict(q=8), 1),
                        (dict(out=0), 1), (dict(dtype=2), 2), (dict(ws=0), 1), (dict(wsb=4096), 3), (dict(kp=0), 1), (dict(mp=2 ** 30 + 1), 2)):
         assert _tree(lib, **over) == code, over
     size = tsel.tsel_tree_attention_workspace_size
