@@ -474,7 +474,7 @@ size_t tsel_prompt_attention_workspace_size(int num_seg, int total_q, int max_se
       num_heads / num_kv_heads > kTile || !cache_head_dim(head_dim) || total_q > kAttMaxKeys ||
       max_seqlen_k > kAttMaxKeys)
     return 0;
-  const PromptPlan a = prompt_plan(num_seg, total_q, max_seqlen_k, num_heads, num_kv_heads, head_dim);
+  const PromptPlan a = prompt_plan(num_seg, total_q, max_seqlen_q, max_seqlen_k, num_heads, num_kv_heads, head_dim);
   return a.too_large ? 0 : size_t(a.total);
 }
 
@@ -506,7 +506,7 @@ tsel_status tsel_prompt_attention(const void* q, int64_t q_row_stride, const voi
     return fail(TSEL_ERR_INVALID_VALUE, "cu_seqlens_q or cu_seqlens_k");
   if (lse != nullptr && !aligned(lse, 4)) return fail(TSEL_ERR_INVALID_VALUE, "lse misaligned");
   TSEL_TRY(check_header(workspace, workspace_bytes));
-  const PromptPlan a = prompt_plan(num_seg, total_q, max_seqlen_k, num_heads, num_kv_heads, head_dim);
+  const PromptPlan a = prompt_plan(num_seg, total_q, max_seqlen_q, max_seqlen_k, num_heads, num_kv_heads, head_dim);
   if (a.too_large) return fail(TSEL_ERR_UNSUPPORTED, "too many units of work");
   if (workspace_bytes < size_t(a.total))
     return fail(TSEL_ERR_WORKSPACE, "workspace %zu < %lld bytes", workspace_bytes, (long long)a.total);
@@ -548,6 +548,7 @@ tsel_status tsel_prompt_attention(const void* q, int64_t q_row_stride, const voi
   p.causal = (flags & TSEL_ATT_CAUSAL) ? 1 : 0;
   p.chunks = a.chunks;
   p.keys = a.keys;
+  p.keys_one = a.keys_one;
   const float scale = softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt(float(head_dim));
   p.c = std::fmax(scale * 1.4426950408889634f, 1e-38f);
   uint8_t* ws = static_cast<uint8_t*>(workspace);

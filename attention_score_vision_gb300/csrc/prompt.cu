@@ -628,15 +628,17 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
         u.valid = 1;
         u.kvh = int(v - vh * p.Hkv);
         u.chunk = int(vh - blk * p.chunks);
-        const int b = (nq - 1) / (2 * p.tt) - int(blk);   // the last rows see most keys
+        // the last rows see most keys; in chunks, blocks of two row tiles come first
+        const int b = p.chunks > 1 ? int(blk) : (nq - 1) / (2 * p.tt) - int(blk);
         u.tok0 = qa + b * 2 * p.tt;
         u.tok_end = min(qa + nq, u.tok0 + 2 * p.tt);
         u.k_base = ka;
         u.lim = p.causal ? nk - nq + 1 - qa : nk;
         auto seen = [&](int tok) { return max(min(u.lim + (p.causal ? tok : 0), nk), 0); };
         const int all = seen(u.tok_end - 1);
-        u.c0 = int(min(int64_t(u.chunk) * p.keys, int64_t(all)));
-        u.k1 = int(min(int64_t(u.c0) + p.keys, int64_t(all)));
+        const int keys = u.tok0 + p.tt < u.tok_end ? p.keys : p.keys_one;
+        u.c0 = int(min(int64_t(u.chunk) * keys, int64_t(all)));
+        u.k1 = int(min(int64_t(u.c0) + keys, int64_t(all)));
         const int t1 = min(u.tok0 + p.tt, u.tok_end);
         u.n0 = (max(min(seen(t1 - 1), u.k1) - u.c0, 0) + kPromptStep - 1) / kPromptStep;
         u.n1 = u.tok0 + p.tt < u.tok_end ? (u.k1 - u.c0 + kPromptStep - 1) / kPromptStep : 0;
