@@ -16,7 +16,9 @@ constexpr int kMoveThreads = 256;
 // 3 and 8 30.1, 2 and 8 35.3.
 constexpr int kMoveItems = 3, kMoveCtas = 8;
 constexpr int kMoveHeads = 32;        // K and V heads of a CTA, at most
-constexpr int kForkParts = 8;         // CTAs of a child
+// CTAs of a child. 256 children, 8 heads of 128, up to 127 rows copied each, forked,
+// grown and freed: 28.0 us with 8, 29.8 with 4, 30.4 with 16, 36.9 with 32.
+constexpr int kForkParts = 8;
 
 struct MoveParams {
   uint8_t* k_pages;
