@@ -5,7 +5,7 @@
 //
 // cache_move_kernel. Token k of a request's kept list goes from position
 // start + keep[k] - base to start + k: cached bytes move unchanged. A thread owns
-// one 16-byte piece of rows and has three of them in flight. A CTA covers some of
+// one 16-byte piece of rows and has a few of them in flight. A CTA covers some of
 // the K and V heads (and, where requests are few, some pieces of their rows) for
 // one chunk of tokens; a chunk's row numbers are worked out once in shared memory.
 //   In place the destination of one token may be the source of another. Kept
@@ -17,7 +17,9 @@
 // the bytes.)
 //   To other pages it is bound by HBM and issue: 36,831 tokens, 8 heads of 128 (152 MB),
 // 30.1 us, 5.05 TB/s, 76% of the copy rate; schedulers issue in 80% of the cycles
-// (row numbers for 16-byte pieces). In place a single request has at most 64 CTAs.
+// (row numbers for 16-byte pieces). In place the chunks of a request follow one
+// another, on at most 64 CTAs for one of 8 heads of 128: 177 us for the same tokens,
+// five times as long (four requests at once 216), a chunk of 768 tokens every 3.7 us.
 //
 // cache_resize_kernel, fork_plan_kernel. Reference counts are whole numbers added
 // with atomics, so their order does not matter; free pages (count 0) are found by
@@ -39,7 +41,8 @@ namespace {
 __device__ __forceinline__ int ceil_pages(int n, int shift) { return int((int64_t(n) + (1 << shift) - 1) >> shift); }
 
 template <bool IN_PLACE>
-__global__ void __launch_bounds__(kMoveThreads, kMoveCtas) cache_move_kernel(const MoveParams p) {
+__global__ void __launch_bounds__(kMoveThreads, IN_PLACE ? kMoveCtasInPlace : kMoveCtas) cache_move_kernel(const MoveParams p) {
+  constexpr int kItems = IN_PLACE ? kMoveItemsInPlace : kMoveItems;
   extern __shared__ int64_t s_rows[];   // [chunk mod 3][source, destination][tokens]: rows of head 0, -1 none
   pdl_wait();
   pdl_launch_dependents();
@@ -65,29 +68,67 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) cache_move_kernel(con
   const int32_t* table = p.table + r * p.table_stride;
   const int32_t* to = IN_PLACE ? table : p.dst_table + r * p.dst_stride;
   const int mask = (1 << p.page_shift) - 1;
-  // rows of a chunk's tokens: [(page * Hkv) << shift] + place
+  // Rows of a chunk's tokens: [(page * Hkv) << shift] + place. In place four tokens of
+  // a thread at a time, so that their two loads in a row overlap.
   auto find = [&](int c, int64_t* rows) {
-    for (int i = threadIdx.x; i < p.tokens; i += kMoveThreads) {
-      const int k = c * p.tokens + i;
-      int64_t src = -1, dst = -1;
-      if (k < n) {
-        const int64_t rel = int64_t(__ldg(p.keep + a + k)) - base;
-        const int64_t at = start + rel;
-        if (rel < k || at >= int64_t(p.width) << p.page_shift || (k > 0 && rel <= int64_t(__ldg(p.keep + a + k - 1)) - base)) {
-          set_status(p.status, TSEL_DEV_KEEP_IDX);
-        } else if (!IN_PLACE || rel != k) {
-          const int put = start + k;
-          const int pg = __ldg(table + (at >> p.page_shift)), pd = __ldg(to + (put >> p.page_shift));
-          if (pg < 0 || pg >= p.num_pages || pd < 0 || pd >= p.num_pages) {
-            set_status(p.status, TSEL_DEV_PAGES);
+    if constexpr (!IN_PLACE) {
+      for (int i = threadIdx.x; i < p.tokens; i += kMoveThreads) {
+        const int k = c * p.tokens + i;
+        int64_t src = -1, dst = -1;
+        if (k < n) {
+          const int64_t rel = int64_t(__ldg(p.keep + a + k)) - base;
+          const int64_t at = start + rel;
+          if (rel < k || at >= int64_t(p.width) << p.page_shift || (k > 0 && rel <= int64_t(__ldg(p.keep + a + k - 1)) - base)) {
+            set_status(p.status, TSEL_DEV_KEEP_IDX);
           } else {
-            src = ((int64_t(pg) * p.Hkv) << p.page_shift) + (at & mask);
-            dst = ((int64_t(pd) * p.Hkv) << p.page_shift) + (put & mask);
+            const int put = start + k;
+            const int pg = __ldg(table + (at >> p.page_shift)), pd = __ldg(to + (put >> p.page_shift));
+            if (pg < 0 || pg >= p.num_pages || pd < 0 || pd >= p.num_pages) {
+              set_status(p.status, TSEL_DEV_PAGES);
+            } else {
+              src = ((int64_t(pg) * p.Hkv) << p.page_shift) + (at & mask);
+              dst = ((int64_t(pd) * p.Hkv) << p.page_shift) + (put & mask);
+            }
           }
         }
+        rows[i] = src;
+        rows[p.tokens + i] = dst;
       }
-      rows[i] = src;
-      rows[p.tokens + i] = dst;
+    } else {
+      for (int i0 = threadIdx.x; i0 < p.tokens; i0 += 4 * kMoveThreads) {
+        int64_t rel[4], before[4];
+        int pg[4], pd[4];
+        unsigned moves = 0;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int i = i0 + x * kMoveThreads, k = c * p.tokens + i;
+          const bool in = i < p.tokens && k < n;
+          rel[x] = in ? int64_t(__ldg(p.keep + a + k)) - base : -1;
+          before[x] = in && k > 0 ? int64_t(__ldg(p.keep + a + k - 1)) - base : -1;
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int i = i0 + x * kMoveThreads, k = c * p.tokens + i;
+          pg[x] = pd[x] = -1;
+          if (i >= p.tokens || k >= n) continue;
+          if (rel[x] < k || start + rel[x] >= int64_t(p.width) << p.page_shift || (k > 0 && rel[x] <= before[x])) {
+            set_status(p.status, TSEL_DEV_KEEP_IDX);
+          } else if (rel[x] != k) {
+            moves |= 1u << x;
+            pg[x] = __ldg(table + ((start + rel[x]) >> p.page_shift));
+            pd[x] = __ldg(to + ((start + k) >> p.page_shift));
+          }
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int i = i0 + x * kMoveThreads, put = start + c * p.tokens + i;
+          if (i >= p.tokens) continue;
+          const bool good = pg[x] >= 0 && pg[x] < p.num_pages && pd[x] >= 0 && pd[x] < p.num_pages;
+          if (!good && ((moves >> x) & 1u)) set_status(p.status, TSEL_DEV_PAGES);
+          rows[i] = good ? ((int64_t(pg[x]) * p.Hkv) << p.page_shift) + ((start + rel[x]) & mask) : -1;
+          rows[p.tokens + i] = good ? ((int64_t(pd[x]) * p.Hkv) << p.page_shift) + (put & mask) : -1;
+        }
+      }
     }
   };
 
@@ -99,28 +140,23 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) cache_move_kernel(con
   const bool scales = works && piece == 0 && slice == 0;   // also moves the row's scale byte
   // item i of this thread: (token, head), head fastest, `groups` apart
   const int tok_step = groups / heads, head_step = groups - tok_step * heads;
-  int buf = 0;
-  find(first_chunk, s_rows);
-  __syncthreads();
-  for (int c = first_chunk; c < chunks; ++c) {
-    const int64_t* rows = s_rows + buf * 2 * p.tokens;
+  auto rows_of = [&](int c) -> int64_t* { return s_rows + (c % 3) * 2 * p.tokens; };
+  auto each = [&](int c, auto&& f) {
     const int left = min(n - c * p.tokens, p.tokens);
-    uint4 data[kMoveItems];
-    uint8_t exps[kMoveItems];
-    auto each = [&](auto&& f) {
-      int tok = group / heads, h = group - tok * heads;
+    int tok = group / heads, h = group - tok * heads;
 #pragma unroll
-      for (int i = 0; i < kMoveItems; ++i) {
-        if (works && tok < left) f(i, tok, head0 + h);
-        tok += tok_step;
-        h += head_step;
-        if (h >= heads) {
-          h -= heads;
-          ++tok;
-        }
+    for (int i = 0; i < kItems; ++i) {
+      if (works && tok < left) f(i, tok, head0 + h);
+      tok += tok_step;
+      h += head_step;
+      if (h >= heads) {
+        h -= heads;
+        ++tok;
       }
-    };
-    each([&](int i, int tok, int h) {
+    }
+  };
+  auto load = [&](int c, const int64_t* rows, uint4 (&data)[kItems], uint8_t (&exps)[kItems]) {
+    each(c, [&](int i, int tok, int h) {
       const int64_t row = rows[tok];
       if (row < 0) return;
       const bool v = h >= p.Hkv;
@@ -128,19 +164,44 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) cache_move_kernel(con
       data[i] = __ldcg(reinterpret_cast<const uint4*>((v ? p.v_pages : p.k_pages) + at * p.d) + piece0 + piece);
       if (scales) exps[i] = __ldcg((v ? p.v_exps : p.k_exps) + at);
     });
-    // every load of the chunk before its stores; and the next chunk's rows, in a
-    // place that no thread can still read for its stores of the chunk before
-    buf = buf == 2 ? 0 : buf + 1;
-    if (IN_PLACE && c + 1 < chunks) find(c + 1, s_rows + buf * 2 * p.tokens);
-    if (IN_PLACE) __syncthreads();
-    each([&](int i, int tok, int h) {
+  };
+  auto store = [&](int c, const int64_t* rows, const uint4 (&data)[kItems], const uint8_t (&exps)[kItems]) {
+    each(c, [&](int i, int tok, int h) {
       if (rows[tok] < 0) return;
       const bool v = h >= p.Hkv;
       const int64_t at = rows[p.tokens + tok] + (int64_t(v ? h - p.Hkv : h) << p.page_shift);
       reinterpret_cast<uint4*>((v ? p.v_pages : p.k_pages) + at * p.d)[piece0 + piece] = data[i];
       if (scales) ((v ? p.v_exps : p.k_exps) + at)[0] = exps[i];
     });
-    if (!IN_PLACE) break;
+  };
+  uint4 data[kItems];
+  uint8_t exps[kItems];
+  if constexpr (!IN_PLACE) {
+    find(first_chunk, s_rows);
+    __syncthreads();
+    load(first_chunk, s_rows, data, exps);
+    store(first_chunk, s_rows, data, exps);
+  } else {
+    // Every load of a chunk comes before its stores: the barrier between them. The
+    // next chunk's loads go out before this one's stores. Row numbers are kept for
+    // three chunks: the last one's stores may still read theirs.
+    uint4 more[kItems];
+    uint8_t more_exps[kItems];
+    find(0, rows_of(0));
+    __syncthreads();
+    load(0, rows_of(0), data, exps);
+    for (int c = 0;; c += 2) {
+      if (c + 1 < chunks) find(c + 1, rows_of(c + 1));
+      __syncthreads();
+      if (c + 1 < chunks) load(c + 1, rows_of(c + 1), more, more_exps);
+      store(c, rows_of(c), data, exps);
+      if (c + 1 >= chunks) break;
+      if (c + 2 < chunks) find(c + 2, rows_of(c + 2));
+      __syncthreads();
+      if (c + 2 < chunks) load(c + 2, rows_of(c + 2), data, exps);
+      store(c + 1, rows_of(c + 1), more, more_exps);
+      if (c + 2 >= chunks) break;
+    }
   }
 }
 
@@ -395,7 +456,8 @@ void move_plan(MoveParams& p, int want) {
   auto parts = [&]() { return int64_t(p.R) * ceil_div(all, p.heads) * ceil_div(row, p.pieces); };
   auto size = [&]() {
     const int groups = kMoveThreads / p.pieces;
-    p.tokens = groups * kMoveItems / p.heads;
+    p.tokens = groups * (p.dst_table == nullptr ? kMoveItemsInPlace : kMoveItems) / p.heads;
+    if (p.tokens > kMoveMaxTokens) p.tokens = kMoveMaxTokens;
     p.chunks = p.dst_table == nullptr ? 1 : int(ceil_div(p.max_keep, p.tokens));
   };
   size();
