@@ -559,7 +559,9 @@ tsel_status tsel_prompt_attention(const void* q, int64_t q_row_stride, const voi
   p.out = out;
   p.lse = lse;
   p.status = &reinterpret_cast<WsHeader*>(ws)->status;
-  p.timeout_ns = device_wait_timeout_ns();
+  // a row tile without rows in a unit waits for the whole of it: 100 ns a key are
+  // several times what a unit takes
+  p.timeout_ns = device_wait_timeout_ns() + 100ull * uint64_t(max_seqlen_k);
   const int ctas = int(a.units < sms ? a.units : sms);
   if (a.units > kPromptDealt * int64_t(ctas) && a.units < (1ll << 30)) {
     p.next = &reinterpret_cast<WsHeader*>(ws)->sched_ctr[0];
