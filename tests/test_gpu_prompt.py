@@ -326,7 +326,8 @@ def test_offsets_past_32_bits(tsel):
     out, lse = tsel.tsel_prompt_attention(q, k, v, i32([0, 0, 90]), i32([0, n - 700, n]), 90, n, flags=tsel.TSEL_ATT_CAUSAL, workspace=ws)
     assert tsel.tsel_read_device_status(ws) == 0
     _close(out, lse, q, k[-700:], v[-700:], _cu([90]), _cu([700]), 128 ** -0.5, True, BF)
-    # one row over all of them: zero keys weigh 1 each, values 0
+    # One row over all of them: zero keys weigh 1 each, values 0. Their sums are whole
+    # numbers below 2^24 in a chunk, so exact; P and the output are rounded once each.
     out, lse = tsel.tsel_prompt_attention(q[:1], k, v, i32([0, 1]), i32([0, n]), 1, n)
     z = _np(q[0]) @ _np(k[-700:, 0]).T * 128 ** -0.5
     total = (n - 700) + np.exp(z).sum(-1)

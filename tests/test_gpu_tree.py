@@ -168,3 +168,34 @@ def test_bad_trees_are_flagged(tsel):
         out, _ = tsel.tsel_tree_attention(b.q, i32(b.cu), nodes[0], i32(b.parents), b.cache, None, None, 0, i32(b.table), i32([nodes[0] - 1]),
                                           b.max_suffix, workspace=ws)
         assert tsel.tsel_read_device_status(ws) == tsel.TSEL_DEV_SEQLENS
+
+
+@pytest.mark.parametrize("nodes,prefix,H", [([5, 3], 0, 2), ([5, 3], 200, 1), ([40, 9], 30, 2)])
+def test_padding_rows_and_given_results(tsel, nodes, prefix, H):
+    """Rows past the last request are left alone, their parents are not read as a tree, and
+    results may go to q itself."""
+    b = Batch(tsel, 21, nodes, [33, 50], prefix, H, 1, 64, 16, BF)
+    clean, clean_lse = b.call(tsel)
+    n = b.q.shape[0]
+    q = torch.cat([b.q, torch.full_like(b.q[:7], float("nan"))])
+    parents = i32(list(b.parents) + [99] * 7)
+    out, lse = torch.full_like(q, 3.0), torch.full((H, n + 7), 4.0, device="cuda")
+    ws = torch.zeros(tsel.tsel_tree_attention_workspace_size(2, n + 7, b.max_nodes, H, 1, 64, prefix, b.max_suffix), dtype=torch.uint8, device="cuda")
+    pre = (i32(b.prefix_pages), i32([prefix]), prefix) if prefix else (None, None, 0)
+    for target in (out, q):
+        tsel.tsel_tree_attention(q, i32(b.cu), b.max_nodes, parents, b.cache, *pre, i32(b.table), i32(b.lens), b.max_suffix, out=target,
+                                 lse=lse, workspace=ws)
+        assert tsel.tsel_read_device_status(ws) == 0
+        b.close(target[:n], lse[:, :n])
+    assert bool((out[n:] == 3).all()) and bool((lse[:, n:] == 4).all()) and bool(torch.isnan(q[n:]).all())
+    b.close(clean, clean_lse)
+
+
+def test_trees_on_two_streams_at_once(tsel):
+    b = Batch(tsel, 22, [16, 9, 30], [300, 40, 7], 150, 2, 2, 80, 32, HF)
+    want, _ = b.call(tsel)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = [b.call(tsel, stream=s)[0] for _ in range(4) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
