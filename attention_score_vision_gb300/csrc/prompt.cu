@@ -49,8 +49,9 @@
 // step of the batch 25% longer, the others 1 to 4% shorter), two warpgroups to a row
 // tile for even and odd steps (5.8 ms: the issuers' waits), two threads to a row (4.05
 // ms), more registers for the softmax (setmaxnreg; 3.85), waits that spin (3.87), the
-// row tiles half a step apart (3.74), results through shared memory 64 bytes of a row
-// at a time or a row to a thread (the same), 32 columns of O at a time (spills: 6.7).
+// row tiles half a step apart (3.74), a row's results by its own
+// thread instead of four lanes together (the same), 32 columns of O at a time
+// (spills: 6.7).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -85,14 +86,14 @@ struct PromptCfg {
   static constexpr int Q_BYTES = DC * kTile * 128;
   static constexpr int ST_BYTES = DC * kPromptStep * 128;       // one step of K or V
   static constexpr int KS = 8 / DC;                             // stages of each
-  // TMEM columns of a row tile: two places for S where O leaves room, else two for P
+  // TMEM columns of a row tile: S (two places where O leaves room), two places for P, O
   static constexpr int NS = D <= 64 ? 2 : 1, NP = 2;
   static constexpr int COL_P = 64 * NS, COL_O = COL_P + 32 * NP;
   static_assert(COL_O + D <= 256, "half of TMEM");
   static constexpr int SOFT_WARPS = 8;
   static constexpr int MMA_WARP = SOFT_WARPS;                   // [product][row tile]
   static constexpr int LOAD_WARP = MMA_WARP + 4;
-  static constexpr int FIX_WARP = LOAD_WARP + 1;   // two
+  static constexpr int FIX_WARP = LOAD_WARP + 1;                // two
   static constexpr int THREADS = 32 * (FIX_WARP + 2);
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_K = 2 * Q_BYTES;
