@@ -349,6 +349,8 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
 #pragma unroll 1
         for (;;) {
           if (moves) {
+            // P goes to the same columns again: stores to TMEM are not ordered among themselves
+            if (j > 0) tmem_wait_st();
             const float top = fmaxf(cols_max(r0), cols_max(r1)) * p.c;
             float s = 1.f;
             if (mine && top > m) {   // no other row's: what a row gives does not depend on its neighbours
