@@ -335,3 +335,27 @@ def test_offsets_past_32_bits(tsel):
     ref = np.exp(z) @ _np(v[-700:, 0]) / total[:, None]
     av = np.exp(z) @ np.abs(_np(v[-700:, 0])) / total[:, None]
     assert np.all(np.abs(_np(out)[0] - ref) <= av * 2.0 ** -7)
+
+
+def _redone(rng, rows, keys, d, dtype):
+    """Logits that climb by some 20 with every 64 keys, past the 15 ln 2 at which a step is done again."""
+    q = torch.from_numpy(np.abs(rng.standard_normal((rows, 2, d)))).to(dtype).cuda()
+    k = torch.from_numpy(np.abs(rng.standard_normal((keys, 1, d)))).to(dtype).cuda()
+    k *= torch.linspace(0, keys / 16, keys, device="cuda").to(dtype)[:, None, None]
+    v = torch.from_numpy(rng.standard_normal((keys, 1, d))).to(dtype).cuda()
+    return q, k, v
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("d", [64, 80, 128])
+def test_every_step_done_again(tsel, dtype, d):
+    """Each step's probabilities are stored twice, the first time past fp16's range."""
+    rng = np.random.default_rng(d)
+    scale = 8.0 / d                        # the mean of a logit, 0.64 d scale times a key's factor, grows alike for every d
+    for rows, keys in ((256, 1280), (5, 1280), (129, 333)):
+        q, k, v = _redone(rng, rows, keys, d, dtype)
+        for causal in (False, True):
+            out, lse, cu_q, cu_k = _run(tsel, q, k, v, [rows], [keys], causal, softmax_scale=scale)
+            _close(out, lse, q, k, v, cu_q, cu_k, scale, causal, dtype)
+            again, lse2, _, _ = _run(tsel, q, k, v, [rows], [keys], causal, softmax_scale=scale)
+            assert torch.equal(again, out) and torch.equal(lse2, lse)
