@@ -718,6 +718,9 @@ __global__ void __launch_bounds__(AttCfg<D, TREE>::THREADS, 1) attend_kernel(con
 // share a row (its partials go round them) and are added up in their order, so
 // a row with many partials is not one long chain of loads; D / 4 lanes of four
 // columns. Chunks without visible keys have lse = -inf and wrote no columns.
+//   PACKED: rows of packed sequences. Only those of segments that keep the bounds have
+// partials; a row looks for its segment among all of them, 32 at a time (keys are cut
+// into chunks for a few segments alone), since one with bad bounds may lie anywhere.
 constexpr int kJoinWarps = 8;
 
 // What is left of a partial too far below the row's largest, its weight 0: its
@@ -729,7 +732,22 @@ __device__ __forceinline__ void keep_nan(float4& acc, const float4& o) {
   if (o.w != o.w) acc.w = o.w;
 }
 
-template <int D, int WPR>
+// Every lane of the warp calls it.
+__device__ __forceinline__ bool join_has_row(const AttParams& p, int64_t tok) {
+  const int lane = threadIdx.x & 31;
+  for (int first = 0; first < p.R; first += 32) {
+    const int g = first + lane;
+    bool mine = false;
+    if (g < p.R) {
+      const int qa = __ldg(p.cu_q + g), nq = __ldg(p.cu_q + g + 1) - qa, ka = __ldg(p.cu_k + g), nk = __ldg(p.cu_k + g + 1) - ka;
+      mine = att_segment_ok(g, qa, nq, ka, nk, p.max_q, p.max_k, p.Tq, p.Tk) && tok >= qa && tok < int64_t(qa) + nq;
+    }
+    if (__any_sync(0xffffffffu, mine)) return true;
+  }
+  return false;
+}
+
+template <int D, int WPR, bool PACKED>
 __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const AttParams p) {
   __shared__ float s_acc[WPR > 1 ? kJoinWarps : 1][D];
   __shared__ float s_m[kJoinWarps], s_sum[kJoinWarps];
@@ -741,14 +759,15 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const AttP
   // also where no suffix kernel looks at the requests one by one
   if (total < 0 || total > p.Tq || total > int64_t(p.R) * p.max_q) {
     if (blockIdx.x == 0 && threadIdx.x == 0) set_status(p.status, TSEL_DEV_SEQLENS);
-    return;
+    if (!PACKED) return;
   }
-  const int64_t rows = int64_t(total) * p.H;
+  const int64_t rows = int64_t(PACKED ? p.Tq : total) * p.H;
   const int64_t step = int64_t(p.Tq) * p.H;
   const int64_t r = int64_t(blockIdx.x) * (kJoinWarps / WPR) + warp / WPR;
+  const bool has = r < rows && (!PACKED || join_has_row(p, r / p.H));
   float m = kNegInf, sum = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (r < rows) {
+  if (has) {
     for (int base = 0; base < p.slots; base += 32 * WPR) {
       const int at = base + lane * WPR + part;   // a lane per partial
       const float mine = at < p.slots ? p.part_lse[at * step + r] : kNegInf;
@@ -824,7 +843,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const AttP
       }
     }
   }
-  if (r >= rows) return;
+  if (!has) return;
   const float ref = m == kNegInf ? 0.f : m;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const int64_t tok = r / p.H;
@@ -882,7 +901,7 @@ cudaError_t launch_attend(int head_dim, const AttParams& p, int64_t units, cudaS
 }
 
 namespace {
-template <int D>
+template <int D, bool PACKED>
 cudaError_t launch_join_t(const AttParams& p, cudaStream_t stream) {
   // Warps to a row with more than eight partials: all eight while the rows are
   // fewer than the CTAs that fit (64 rows of 73 partials: a call takes 25.7 us,
@@ -891,20 +910,26 @@ cudaError_t launch_join_t(const AttParams& p, cudaStream_t stream) {
   // us, with two 91.1, with eight 96.3).
   const int64_t rows = int64_t(p.Tq) * p.H;
   const int wpr = p.slots <= 8 || rows > 4096 ? 1 : (rows > 1024 ? 2 : kJoinWarps);
-  auto kern = wpr == 1 ? attend_join_kernel<D, 1> : (wpr == 2 ? attend_join_kernel<D, 2> : attend_join_kernel<D, kJoinWarps>);
+  auto kern = wpr == 1 ? attend_join_kernel<D, 1, PACKED>
+                       : (wpr == 2 ? attend_join_kernel<D, 2, PACKED> : attend_join_kernel<D, kJoinWarps, PACKED>);
   return launch_kernel(kern, dim3(unsigned(ceil_div(rows, kJoinWarps / wpr))), 32 * kJoinWarps, 0, stream, 1, p);
 }
 }  // namespace
 
 cudaError_t launch_attend_join(int head_dim, const AttParams& p, cudaStream_t stream) {
+#define TSEL_JOIN_CASE(DD) \
+  case DD:                 \
+    return p.cu_k != nullptr ? launch_join_t<DD, true>(p, stream) : launch_join_t<DD, false>(p, stream);
   switch (head_dim) {
-    case 64: return launch_join_t<64>(p, stream);
-    case 80: return launch_join_t<80>(p, stream);
-    case 96: return launch_join_t<96>(p, stream);
-    case 112: return launch_join_t<112>(p, stream);
-    case 128: return launch_join_t<128>(p, stream);
-    default: return cudaErrorInvalidValue;
+    TSEL_JOIN_CASE(64)
+    TSEL_JOIN_CASE(80)
+    TSEL_JOIN_CASE(96)
+    TSEL_JOIN_CASE(112)
+    TSEL_JOIN_CASE(128)
+    default:
+      return cudaErrorInvalidValue;
   }
+#undef TSEL_JOIN_CASE
 }
 
 }  // namespace tsel

@@ -153,6 +153,8 @@ struct AttParams {
   const int32_t* suffix_lens;
   int max_suffix;
   const int32_t* parents;      // [Tq] of the drafted tokens' trees, or null: one after another
+  const int32_t* cu_k;         // of packed sequences (with Tk, max_k), or null: read by the join alone
+  int Tk, max_k;
   int H, Hkv;
   float c;                     // softmax_scale * log2(e)
   int G, tt, slots;
@@ -229,6 +231,13 @@ __device__ __forceinline__ AttUnit att_unit(const AttParams& p, U u, int per) {
     w.pages = p.page_table + r * p.table_stride;
   }
   return w;
+}
+
+// Whether segment g of a packed batch, nq rows from qa on over nk keys from ka on, keeps
+// the bounds of its call.
+__device__ __forceinline__ bool att_segment_ok(int g, int qa, int nq, int ka, int nk, int max_q, int max_k, int Tq, int Tk) {
+  return qa >= 0 && nq >= 0 && nq <= max_q && qa <= Tq - nq && ka >= 0 && nk >= 0 && nk <= max_k && ka <= Tk - nk &&
+         (g > 0 || (qa == 0 && ka == 0));
 }
 
 // Ancestors of the up to 64 nodes of a tree, a node itself among them: a bit each,

@@ -573,6 +573,9 @@ tsel_status tsel_prompt_attention(const void* q, int64_t q_row_stride, const voi
   if (a.slots == 0) return TSEL_OK;
   AttParams j{};
   j.cu_q = cu_seqlens_q;
+  j.cu_k = cu_seqlens_k;
+  j.Tk = total_k;
+  j.max_k = max_seqlen_k;
   j.R = num_seg;
   j.Tq = total_q;
   j.max_q = max_seqlen_q;

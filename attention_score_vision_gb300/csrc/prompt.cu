@@ -601,9 +601,7 @@ __global__ void __launch_bounds__(PromptCfg<D>::THREADS, 1)
           nq = __ldg(p.cu_q + g + 1) - qa;
           ka = __ldg(p.cu_k + g);
           nk = __ldg(p.cu_k + g + 1) - ka;
-          const bool good = qa >= 0 && nq >= 0 && nq <= p.max_q && qa <= p.Tq - nq && ka >= 0 && nk >= 0 && nk <= p.max_k &&
-                            ka <= p.Tk - nk && (g > 0 || (qa == 0 && ka == 0));
-          if (!good) {
+          if (!att_segment_ok(g, qa, nq, ka, nk, p.max_q, p.max_k, p.Tq, p.Tk)) {
             set_status(p.status, TSEL_DEV_SEQLENS);
             nq = 0;
           }

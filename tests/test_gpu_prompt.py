@@ -359,3 +359,36 @@ def test_every_step_done_again(tsel, dtype, d):
             _close(out, lse, q, k, v, cu_q, cu_k, scale, causal, dtype)
             again, lse2, _, _ = _run(tsel, q, k, v, [rows], [keys], causal, softmax_scale=scale)
             assert torch.equal(again, out) and torch.equal(lse2, lse)
+
+
+BAD_LENGTHS = [
+    # cu_q, cu_k, max_q, max_k, the good segment, rows of no segment
+    ([0, 20, 61], [0, 600, 1300], 40, 700, 0, []),
+    ([0, 20, 60], [0, 600, 1301], 40, 700, 0, []),
+    ([0, 20, 10], [0, 600, 1300], 40, 700, 0, [30, 59]),
+    ([0, 20, 60], [0, 600, 599], 40, 700, 0, []),
+    ([0, 20, 60], [0, 600, 1300], 30, 700, 0, []),
+    ([0, 20, 60], [0, 600, 1300], 40, 650, 0, []),
+    ([0, 20, -5], [0, 600, 1300], 40, 700, 0, [30, 59]),
+    ([0, 20, 1 << 30], [0, 600, 1 << 30], 40, 700, 0, []),
+    ([0, 45, 60], [0, 600, 1300], 40, 700, 1, []),
+    ([0, 20, 60], [2, 600, 1300], 40, 700, 1, []),
+    ([0, 35, 50], [0, 800, 1300], 20, 700, 1, [50, 59]),
+]
+
+
+@pytest.mark.parametrize("case", range(len(BAD_LENGTHS)))
+def test_bad_lengths_spare_the_other_segment_in_chunks(tsel, case):
+    cu_q, cu_k, max_q, max_k, good, free = BAD_LENGTHS[case]
+    rng = np.random.default_rng(14)
+    q, k, v = _inputs(rng, 60, 1300, 2, 1, 64, BF)
+    size = tsel.tsel_prompt_attention_workspace_size(2, 60, max_q, max_k, 2, 1, 64)
+    assert size > 4 * 60 * 2 * 64 * 2      # at least two chunks
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    out, lse = torch.full_like(q, 7.0), torch.full((2, 60), 5.0, device="cuda")
+    tsel.tsel_prompt_attention(q, k, v, i32(cu_q), i32(cu_k), max_q, max_k, flags=tsel.TSEL_ATT_CAUSAL, out=out, lse=lse, workspace=ws)
+    assert tsel.tsel_read_device_status(ws) == tsel.TSEL_DEV_SEQLENS
+    a, b, c, e = cu_q[good], cu_q[good + 1], cu_k[good], cu_k[good + 1]
+    _close(out[a:b], lse[:, a:b], q[a:b], k[c:e], v[c:e], [0, b - a], [0, e - c], 64 ** -0.5, True, BF)
+    if free:
+        assert bool((out[free[0]:free[1] + 1] == 7).all()) and bool((lse[:, free[0]:free[1] + 1] == 5).all())
