@@ -724,12 +724,23 @@ __global__ void __launch_bounds__(AttCfg<D, TREE>::THREADS, 1) attend_kernel(con
 constexpr int kJoinWarps = 8;
 
 // What is left of a partial too far below the row's largest, its weight 0: its
-// NaN, but no number and no infinity (a mean past fp32's range).
-__device__ __forceinline__ void keep_nan(float4& acc, const float4& o) {
-  if (o.x != o.x) acc.x = o.x;
-  if (o.y != o.y) acc.y = o.y;
-  if (o.z != o.z) acc.z = o.z;
-  if (o.w != o.w) acc.w = o.w;
+// NaN, but no number. INF: and its infinities, which are of V rows that the row sees;
+// cached rows are finite, so an infinity of theirs is a mean past fp32's range, which
+// goes too.
+template <bool INF>
+__device__ __forceinline__ void keep_special(float& acc, float o) {
+  if (INF) {
+    if (!(fabsf(o) < __builtin_huge_valf())) acc += o;
+  } else if (o != o) {
+    acc = o;
+  }
+}
+template <bool INF>
+__device__ __forceinline__ void keep_special(float4& acc, const float4& o) {
+  keep_special<INF>(acc.x, o.x);
+  keep_special<INF>(acc.y, o.y);
+  keep_special<INF>(acc.z, o.z);
+  keep_special<INF>(acc.w, o.w);
 }
 
 // Every lane of the warp calls it.
@@ -799,7 +810,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const AttP
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           if (wv[x] == 0.f) {
-            keep_nan(acc, o[x]);
+            keep_special<PACKED>(acc, o[x]);
             continue;
           }
           sum += wv[x];
@@ -832,7 +843,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const AttP
         const float4 v = *reinterpret_cast<const float4*>(&s_acc[warp + x][4 * lane]);
         if (f == 0.f) {   // this warp's NaN partials among lower ones: also in its sum
           if (s_sum[warp + x] != s_sum[warp + x]) sum = s_sum[warp + x];
-          keep_nan(acc, v);
+          keep_special<PACKED>(acc, v);
           continue;
         }
         sum += f * s_sum[warp + x];

@@ -392,3 +392,21 @@ def test_bad_lengths_spare_the_other_segment_in_chunks(tsel, case):
     _close(out[a:b], lse[:, a:b], q[a:b], k[c:e], v[c:e], [0, b - a], [0, e - c], 64 ** -0.5, True, BF)
     if free:
         assert bool((out[free[0]:free[1] + 1] == 7).all()) and bool((lse[:, free[0]:free[1] + 1] == 5).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("rows,keys,H", [(60, 128, 2), (300, 700, 1), (3, 2000, 2), (3, 20000, 2), (700, 20000, 2)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_infinities_under_a_weight_that_underflows(tsel, dtype, rows, keys, H, value):
+    """A row that sees an infinite V gives an infinity or NaN of its column however small the key's weight,
+    in one chunk (the first case) and in several."""
+    rng = np.random.default_rng(13)
+    q, k, v = torch.ones(rows, H, 64, device="cuda"), torch.zeros(keys, 1, 64, device="cuda"), rng.standard_normal((keys, 1, 64))
+    k[:keys // 3] = -20.0                 # logits 160 below the others': 2^-230 of their weight
+    q, k, v = q.to(dtype), k.to(dtype), torch.from_numpy(v).to(dtype).cuda()
+    clean, clean_lse, _, _ = _run(tsel, q, k, v, [rows], [keys], False)
+    v[5, 0, 33] = value
+    out, lse, _, _ = _run(tsel, q, k, v, [rows], [keys], False)
+    assert not bool(torch.isfinite(out[..., 33]).any()) and torch.equal(lse, clean_lse)
+    out[..., 33] = clean[..., 33]
+    assert torch.equal(out, clean)
