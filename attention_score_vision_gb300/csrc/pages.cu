@@ -213,28 +213,31 @@ constexpr int kPagesThreads = 1024;
 constexpr int kPagesWarps = kPagesThreads / 32;
 constexpr int kPagesPerLane = 8;
 
-// Inclusive sums over the block's threads; the total in *total.
-__device__ __forceinline__ int block_sum(int mine, int* s_warps, int* total) {
+// Inclusive sums (MAX: largest values) over the block's threads; of all in *total.
+template <bool MAX>
+__device__ __forceinline__ int block_scan(int mine, int* s_warps, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto both = [](int a, int b) { return MAX ? max(a, b) : a + b; };
   int v = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += y;
+    if (lane >= o) v = both(v, y);
   }
-  __syncthreads();   // the sums of the call before have been read
+  __syncthreads();   // the results of the call before have been read
   if (lane == 31) s_warps[warp] = v;
   __syncthreads();
   int before = s_warps[lane];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, before, o);
-    if (lane >= o) before += y;
+    if (lane >= o) before = both(before, y);
   }
   *total = __shfl_sync(0xffffffffu, before, 31);
   const int up_to = __shfl_sync(0xffffffffu, before, max(warp - 1, 0));   // of the warps before
-  return v + (warp > 0 ? up_to : 0);
+  return warp > 0 ? both(v, up_to) : v;
 }
+__device__ __forceinline__ int block_sum(int mine, int* s_warps, int* total) { return block_scan<false>(mine, s_warps, total); }
 
 // Writes the lowest `want` free pages into list; returns how many there are (at
 // most `want`).
@@ -358,21 +361,34 @@ __global__ void __launch_bounds__(kPagesThreads) fork_plan_kernel(const PagesPar
   pdl_launch_dependents();
   const int64_t room = int64_t(p.width) << p.page_shift;
   const int mask = (1 << p.page_shift) - 1;
+  // The largest child so far, in the places of the pages found later: a list that
+  // ascends whatever the caller's does. A child is taken only where it rises, so none
+  // is taken twice, and a parent is looked for in it.
+  int* tops = p.found;
+  int top = -1;
+  for (int base = 0; base < p.n; base += kPagesThreads) {
+    const int i = base + int(threadIdx.x);
+    int most;
+    const int up_to = block_scan<true>(i < p.n ? __ldg(p.children + i) : -1, s_warps, &most);
+    if (i < p.n) tops[i] = max(top, up_to);
+    top = max(top, most);
+  }
+  __syncthreads();
   int want = 0;
   for (int base = 0; base < p.n; base += kPagesThreads) {
     const int i = base + int(threadIdx.x);
     int state = -2;   // no child, no page, a page
     if (i < p.n) {
       const int src = __ldg(p.parents + i), dst = __ldg(p.children + i);
-      bool ok = src >= 0 && src < p.rows && dst >= 0 && dst < p.rows && (i == 0 || dst > __ldg(p.children + i - 1));
+      bool ok = src >= 0 && src < p.rows && dst >= 0 && dst < p.rows && dst > (i > 0 ? tops[i - 1] : -1);
       if (ok) {   // no child is a parent
         int lo = 0, hi = p.n;
         while (lo < hi) {
           const int mid = (lo + hi) >> 1;
-          if (__ldg(p.children + mid) < src) lo = mid + 1;
+          if (tops[mid] < src) lo = mid + 1;
           else hi = mid;
         }
-        ok = lo >= p.n || __ldg(p.children + lo) != src;
+        ok = lo >= p.n || tops[lo] != src;
       }
       const int len = ok ? __ldcg(p.lens + src) : 0;
       ok = ok && len >= 0 && len <= room && __ldcg(p.lens + dst) == 0;

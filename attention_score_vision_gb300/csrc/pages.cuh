@@ -68,7 +68,7 @@ struct PagesParams {
   int Hkv, d;
   int parts;                   // CTAs of a child
   int32_t* plan;               // [rows + 1]
-  int32_t* found;              // [rows * width]
+  int32_t* found;              // [rows * width], [rows] at least
   uint32_t* status;
 };
 

@@ -626,8 +626,9 @@ TSEL_API tsel_status tsel_cache_resize(int32_t* refs, int num_pages, int page_si
  * tsel_cache_resize.
  *
  * parents, children  int32 [num_forks] device, rows of page_table: children
- *             ascending, of length 0, none of them a parent in the same call
- *             (else TSEL_DEV_REQUESTS, and that child is left as it is).
+ *             ascending (each above all before it), of length 0, none of them a
+ *             parent in the same call (else TSEL_DEV_REQUESTS, and that child is
+ *             left as it is).
  *             num_forks at most num_rows.
  * A child for which no page is free is left as it is (TSEL_DEV_PAGES); so is one
  * whose parent's last page is outside the cache. Other pages outside the cache are

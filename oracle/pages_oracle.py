@@ -51,6 +51,19 @@ def resize(refs, table, lens, new_lens, page_size):
     return ok
 
 
+def good_forks(lens, parents, children):
+    """Which forks are taken: children above all before them, of length 0, from rows that are
+    not themselves listed as children above all before them."""
+    rows, top, listed = len(lens), -1, set()
+    above = []
+    for c in children:
+        above.append(c > top)
+        top = max(top, c)
+        if above[-1]:
+            listed.add(c)
+    return [bool(a and 0 <= c < rows and 0 <= p < rows and p not in listed and lens[c] == 0) for p, c, a in zip(parents, children, above)]
+
+
 def fork(cache, refs, table, lens, parents, children):
     """Children without a page stay as they are."""
     page = cache[0].shape[2]

@@ -262,3 +262,57 @@ def test_fork_refuses_and_runs_out(tsel):
     O.fork(host, refs, table, lens, [0, 0, 0], [2, 3, 4])
     assert lens.tolist() == [20, 32, 20, 20, 0]
     unchanged()
+
+
+def _dev_state(tsel, rng, rows, width, pages, page, lens):
+    """Rows with pages of their own, here and on the device, and a workspace."""
+    host = list(_state(rng, rows, width, pages, page, lens))
+    return host, [i32(x) for x in host], _ws(tsel, tsel.tsel_cache_resize_workspace_size(rows, width))
+
+
+def _status(tsel, ws):
+    bits = tsel.tsel_read_device_status(ws)
+    tsel.tsel_clear_device_status(ws)
+    return bits
+
+
+def _equal(dev, host):
+    for a, b in zip(dev, host):
+        assert np.array_equal(a.cpu().numpy(), b)
+
+
+@pytest.mark.parametrize("parents,children", [([0, 0, 0], [5, 3, 5]), ([0, 0, 5], [5, 3, 6]), ([1, 0, 1, 0], [2, 6, 4, 6]),
+                                              ([0, 1, 6, 0], [3, 6, 4, 7]), ([0, 0, 1], [2, 99, 5]), ([0, 1, 0], [-4, 2, 2])])
+def test_fork_lists_out_of_order(tsel, parents, children):
+    """An entry that is not above all those before it is refused, and a parent is found among the children
+    whatever the order."""
+    rng = np.random.default_rng(22)
+    host, dev, ws = _dev_state(tsel, rng, 8, 4, 30, 16, [40, 33, 0, 0, 0, 0, 0, 0])
+    cache, bytes_ = _cache(tsel, rng, 30, 16, 2, 64)
+    tsel.tsel_cache_fork(cache, *dev, i32(parents), i32(children), workspace=ws)
+    assert _status(tsel, ws) == tsel.TSEL_DEV_REQUESTS
+    good = O.good_forks(host[2], parents, children)
+    assert 0 < sum(good) < len(good)
+    O.fork(bytes_, *host, [p for p, g in zip(parents, good) if g], [c for c, g in zip(children, good) if g])
+    _equal(dev, host)
+    _same(cache, bytes_)
+
+
+def test_fork_lists_out_of_order_in_many_rows(tsel):
+    """Lists longer than a round of the planning CTA."""
+    rng = np.random.default_rng(23)
+    page, rows, pages = 16, 5000, 12000
+    host, dev, ws = _dev_state(tsel, rng, rows, 3, pages, page, [int(n) for n in rng.integers(0, 40, 50)] + [0] * (rows - 50))
+    cache, bytes_ = _cache(tsel, rng, pages, page, 1, 64)
+    children = np.sort(rng.permutation(np.arange(50, rows))[:3500]).astype(np.int32)
+    parents = rng.integers(0, 50, 3500).astype(np.int32)
+    some = rng.permutation(3500)[:60]
+    children[some[:30]] = rng.integers(-3, rows + 1, 30)     # out of order, some of them rows that hold tokens
+    parents[some[30:]] = rng.integers(-1, rows + 1, 30)      # some of them children
+    good = np.asarray(O.good_forks(host[2], parents, children))
+    assert 30 < good.sum() < 3500
+    tsel.tsel_cache_fork(cache, *dev, i32(parents), i32(children), workspace=ws)
+    assert _status(tsel, ws) == tsel.TSEL_DEV_REQUESTS
+    O.fork(bytes_, *host, parents[good], children[good])
+    _equal(dev, host)
+    _same(cache, bytes_)

@@ -255,3 +255,9 @@ def test_binding_refuses_pages(tsel):
     refused(ValueError, f, cache, _ints(3), t, _ints(2), _ints(1), _ints(1))      # counts of another pool
     refused(ValueError, f, cache, _ints(4), t, _ints(2), _ints(1), _ints(2))
     refused(ValueError, f, cache, _ints(4), t, _ints(1), _ints(1), _ints(1))
+
+
+def test_pages_oracle_lists_out_of_order():
+    assert PO.good_forks([9, 6] + [0] * 6, [0, 0, 0], [5, 3, 5]) == [True, False, False]
+    assert PO.good_forks([9, 6] + [0] * 6, [0, 0, 5], [5, 3, 6]) == [True, False, False]
+    assert PO.good_forks([9, 6] + [0] * 6, [0, 3, 8, 1], [2, 3, 4, 5]) == [True, False, False, True]
