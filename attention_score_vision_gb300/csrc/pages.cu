@@ -282,6 +282,15 @@ __device__ __forceinline__ bool resized_row(const PagesParams& p, int r, int* ha
   return true;
 }
 
+// Whether row r would grow from inside a page that other rows hold too: what is then
+// written behind its length would be theirs as well.
+__device__ __forceinline__ bool shared_end(const PagesParams& p, int r) {
+  const int now = p.lens[r];
+  if (__ldg(p.new_lens + r) <= now || (now & ((1 << p.page_shift) - 1)) == 0) return false;
+  const int page = p.table[r * p.table_stride + (now >> p.page_shift)];
+  return page >= 0 && page < p.num_pages && __ldcg(p.refs + page) > 1;
+}
+
 __global__ void __launch_bounds__(kPagesThreads) cache_resize_kernel(const PagesParams p) {
   __shared__ int s_warps[kPagesWarps];
   pdl_wait();
@@ -291,10 +300,15 @@ __global__ void __launch_bounds__(kPagesThreads) cache_resize_kernel(const Pages
   for (int base = 0; base < p.rows; base += kPagesThreads) {
     const int r = base + int(threadIdx.x);
     int have = 0, need = 0;
-    const int more = r < p.rows && resized_row(p, r, &have, &need) ? max(need - have, 0) : 0;
+    bool goes = r < p.rows && resized_row(p, r, &have, &need);
+    if (goes && shared_end(p, r)) {
+      set_status(p.status, TSEL_DEV_REQUESTS);
+      goes = false;
+    }
+    const int more = goes ? max(need - have, 0) : 0;
     int total;
     const int up_to = want + block_sum(more, s_warps, &total);
-    if (r < p.rows) p.plan[r] = up_to - more;
+    if (r < p.rows) p.plan[r] = goes ? up_to - more : -1;   // -1: stays as it is
     want += total;
   }
   const int found = free_pages(p.refs, p.num_pages, want, p.found, s_warps);
@@ -305,6 +319,7 @@ __global__ void __launch_bounds__(kPagesThreads) cache_resize_kernel(const Pages
     int have = 0, need = 0, first = 0;
     bool goes = r < p.rows && resized_row(p, r, &have, &need) && need >= have;
     if (goes) first = p.plan[r];
+    goes = goes && first >= 0;
     if (goes && need > have && first + (need - have) > found) {   // not enough: the row stays as it is
       set_status(p.status, TSEL_DEV_PAGES);
       goes = false;

@@ -600,7 +600,12 @@ TSEL_API size_t tsel_cache_resize_workspace_size(int num_rows, int pages_per_row
  * TSEL_DEV_PAGES is set.
  *   Shrinking rows lower the counts of the pages past their new length; the
  * entries stay in the table. A page outside the cache, or one whose count is 0
- * already, sets TSEL_DEV_PAGES and is passed over.
+ * already, sets TSEL_DEV_PAGES and is passed over. After tsel_cache_fork a row may
+ * come to end inside a page that others hold too. It can be read so, but it does
+ * not grow from there, since what is written behind it would be theirs as well: a
+ * new length above lens[r], where lens[r] is inside a page whose count was above 1
+ * when the call began, sets TSEL_DEV_REQUESTS, and the row stays as it is. A fork
+ * of it copies the rows in use; that row can grow.
  *
  * refs        int32 [num_pages] device.
  * page_table  int32 device, row r at page_table + r * page_table_stride,

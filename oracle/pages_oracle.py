@@ -26,13 +26,20 @@ def compact(cache, table, starts, bases, keep, cu, dst_table=None):
     return lens
 
 
+def shared_end(refs, table, lens, new_lens, page_size):
+    """The rows that would grow from inside a page that others hold too."""
+    return np.asarray([new_lens[r] > lens[r] and lens[r] % page_size != 0 and refs[table[r, lens[r] // page_size]] > 1
+                       for r in range(len(lens))], bool)
+
+
 def resize(refs, table, lens, new_lens, page_size):
-    """False where pages ran out."""
+    """False where pages ran out. Rows of shared_end() stay as they are."""
+    held = shared_end(refs, table, lens, new_lens, page_size)
     free = iter(np.flatnonzero(refs == 0).tolist())
     left, ok = int((refs == 0).sum()), True
     refs0 = refs.copy()
     for r in range(len(lens)):
-        if new_lens[r] < 0:
+        if new_lens[r] < 0 or held[r]:
             continue
         have, need = _pages(lens[r], page_size), _pages(new_lens[r], page_size)
         if need > have:

@@ -316,3 +316,77 @@ def test_fork_lists_out_of_order_in_many_rows(tsel):
     O.fork(bytes_, *host, parents[good], children[good])
     _equal(dev, host)
     _same(cache, bytes_)
+
+
+def test_growth_behind_a_shared_page_is_refused(tsel):
+    """What is written behind a row's length must not land in a page that another row holds too."""
+    rng = np.random.default_rng(20)
+    page, rows, width, pages = 16, 6, 5, 24
+    host, dev, ws = _dev_state(tsel, rng, rows, width, pages, page, [40, 0, 0, 20, 0, 0])
+    cache, bytes_ = _cache(tsel, rng, pages, page, 2, 64)
+
+    def resize(new, bits=0):
+        tsel.tsel_cache_resize(*dev, i32(new), page, workspace=ws)
+        ok = O.resize(*host, new, page)
+        assert _status(tsel, ws) == bits and ok
+        _equal(dev, host)
+
+    def fork(parents, children):
+        tsel.tsel_cache_fork(cache, *dev, i32(parents), i32(children), workspace=ws)
+        O.fork(bytes_, *host, parents, children)
+        assert _status(tsel, ws) == 0
+        _equal(dev, host)
+        _same(cache, bytes_)
+    fork([0, 0], [1, 2])                                     # pages 0 and 1 of row 0 are held three times
+    resize([-1, 24, -1, -1, -1, -1])                         # row 1 rolls back into the second of them: read only
+    assert host[2].tolist() == [40, 24, 40, 20, 0, 0]
+    for then in (25, 32, 33, 80):                            # row 3 grows in the same calls
+        was = host[2][3]
+        resize([-1, then, -1, was + 9, -1, -1], tsel.TSEL_DEV_REQUESTS)
+        assert host[2][1] == 24 and host[2][3] == was + 9
+    resize([-1, 24, -1, -1, -1, -1])                         # the length that it has
+    resize([-1, 17, -1, -1, -1, -1])                         # further back
+    resize([20, -1, -1, -1, -1, -1])                         # the parent as well
+    resize([21, -1, -1, -1, -1, -1], tsel.TSEL_DEV_REQUESTS)
+    # a fork copies the rows in use: that row can grow and be written, no other sees it
+    fork([1], [4])
+    resize([-1, 0, -1, -1, 30, -1])
+    at = [int(host[1][4, p // page]) * page + p % page for p in range(17, 30)]
+    k = torch.from_numpy(rng.standard_normal((13, 2, 64))).to(torch.bfloat16).cuda()
+    before = [a[host[1][2, :3]].copy() for a in bytes_]
+    tsel.tsel_cache_write(k, k, i32(at), cache, workspace=ws)
+    for a, b in zip(cache, before):
+        assert np.array_equal(a.cpu().numpy()[host[1][2, :3]], b)
+    bytes_ = [a.cpu().numpy() for a in cache]
+    # at a whole page's end a row gets a page of its own
+    resize([16, -1, -1, -1, -1, -1])
+    resize([19, -1, -1, -1, -1, -1])
+    # counts when the call begins decide: row 2 gives back what row 5 holds too, row 5 grows one call later
+    fork([2], [5])
+    resize([-1, -1, -1, -1, -1, 18])
+    resize([-1, -1, 0, -1, -1, 19], tsel.TSEL_DEV_REQUESTS)
+    assert host[2][2] == 0 and host[2][5] == 18
+    resize([-1, -1, -1, -1, -1, 19])
+    resize([0] * rows)
+    assert not dev[0].any()
+
+
+def test_growth_behind_shared_pages_in_many_rows(tsel):
+    rng = np.random.default_rng(21)
+    page, rows, width, pages, parents = 16, 1500, 6, 20000, 40
+    host, dev, ws = _dev_state(tsel, rng, rows, width, pages, page, [int(n) for n in rng.integers(1, 80, parents)] + [0] * (rows - parents))
+    cache, bytes_ = _cache(tsel, rng, pages, page, 1, 64)
+    src, kids = rng.integers(0, parents, rows - parents).astype(np.int32), np.arange(parents, rows, dtype=np.int32)
+    tsel.tsel_cache_fork(cache, *dev, i32(src), i32(kids), workspace=ws)
+    O.fork(bytes_, *host, src, kids)
+    _equal(dev, host)
+    refused = []
+    for _ in range(6):
+        new = rng.integers(-1, width * page + 1, rows).astype(np.int32)
+        refused.append(O.shared_end(*host, new, page).sum())
+        tsel.tsel_cache_resize(*dev, i32(new), page, workspace=ws)
+        assert O.resize(*host, new, page) and _status(tsel, ws) == (tsel.TSEL_DEV_REQUESTS if refused[-1] else 0)
+        _equal(dev, host)
+    assert refused[0] == 0 and max(refused) > 10             # a fork's own last page can be written
+    tsel.tsel_cache_resize(*dev, i32([0] * rows), page, workspace=ws)
+    assert not dev[0].any()

@@ -261,3 +261,10 @@ def test_pages_oracle_lists_out_of_order():
     assert PO.good_forks([9, 6] + [0] * 6, [0, 0, 0], [5, 3, 5]) == [True, False, False]
     assert PO.good_forks([9, 6] + [0] * 6, [0, 0, 5], [5, 3, 6]) == [True, False, False]
     assert PO.good_forks([9, 6] + [0] * 6, [0, 3, 8, 1], [2, 3, 4, 5]) == [True, False, False, True]
+
+
+def test_pages_oracle_shared_ends():
+    refs, table, lens = np.asarray([2, 2, 1, 1, 0, 0]), np.asarray([[0, 1, 2], [0, 1, 3], [-1, -1, -1]]), np.asarray([9, 6, 0])
+    assert PO.shared_end(refs, table, lens, [12, 7, 4], 4).tolist() == [False, True, False]
+    assert PO.shared_end(refs, table, lens, [4, 6, -1], 4).tolist() == [False, False, False]
+    assert PO.resize(refs, table, lens, [-1, 12, 4], 4) and lens.tolist() == [9, 6, 4] and refs.tolist() == [2, 2, 1, 1, 1, 0]
