@@ -886,7 +886,8 @@ def tsel_cache_compact(cache: TselCache, page_table: torch.Tensor, keep_idx: tor
                        max_keep: int, *, starts: Optional[torch.Tensor] = None, bases: Optional[torch.Tensor] = None,
                        dst_table: Optional[torch.Tensor] = None, new_lens: Optional[torch.Tensor] = None,
                        workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """Moves the cached rows of kept tokens together; returns the new lengths int32 [R].
+    """Moves the cached rows of kept tokens together; returns the new lengths int32 [R],
+    -1 for a request that is refused.
 
     Token k of request r's kept ones goes from position starts[r] + keep_idx[cu_keep[r] + k]
     - bases[r] of its pages (page_table int32 [R, pages]) to position starts[r] + k of

@@ -57,7 +57,10 @@ __global__ void __launch_bounds__(kMoveThreads, IN_PLACE ? kMoveCtasInPlace : kM
   const bool lead = threadIdx.x == 0 && part == 0 && slice == 0 && first_chunk == 0;
   const int64_t room = int64_t(IN_PLACE ? p.width : p.dst_width) << p.page_shift;
   if (a < 0 || e < a || e > p.total || e - a > p.max_keep || (r == 0 && a != 0) || start < 0 || int64_t(start) + (e - a) > room) {
-    if (lead) set_status(p.status, TSEL_DEV_REQUESTS);
+    if (lead) {
+      set_status(p.status, TSEL_DEV_REQUESTS);
+      if (p.new_lens != nullptr) p.new_lens[r] = -1;
+    }
     return;
   }
   const int n = e - a;

@@ -570,7 +570,8 @@ TSEL_API tsel_status tsel_cache_read(const uint8_t* k_pages, const uint8_t* v_pa
  * cu_keep       int32 [num_req + 1] device: 0, monotone, at most max_keep each,
  *               the last at most total_keep. A request that breaks these, or whose
  *               kept tokens do not fit its destination's pages, sets
- *               TSEL_DEV_REQUESTS and is left as it is.
+ *               TSEL_DEV_REQUESTS and is left as it is; its new_lens is -1, with
+ *               which tsel_cache_resize leaves a row alone.
  * new_lens      int32 [num_req] device or NULL; not starts itself.
  * workspace     >= tsel_cache_workspace_size() bytes (status).
  * Pages outside the cache set TSEL_DEV_PAGES; their tokens are skipped. Rows that

@@ -390,3 +390,18 @@ def test_growth_behind_shared_pages_in_many_rows(tsel):
     assert refused[0] == 0 and max(refused) > 10             # a fork's own last page can be written
     tsel.tsel_cache_resize(*dev, i32([0] * rows), page, workspace=ws)
     assert not dev[0].any()
+
+
+def test_lengths_of_refused_requests(tsel):
+    """-1, which tsel_cache_resize takes as a row to leave alone, also in a length tensor of the call's own."""
+    rng = np.random.default_rng(24)
+    table = np.arange(12, dtype=np.int32).reshape(3, 4)
+    for to in (None, table + 12):
+        cache, host = _cache(tsel, rng, 24, 16, 2, 64)
+        for starts, keep, cu, most, want in (([9, -1, 5], [1, 2], [0, 1, 1, 2], 8, [10, -1, 6]), ([0, 0, 0], [1, 2, 3], [0, 1, 3, 3], 1, [1, -1, 0]),
+                                             ([64, 60, 0], [0, 0], [0, 0, 2, 1], 8, [64, 62, -1]), ([62, 0, 0], [0, 1, 2], [0, 3, 3, 9], 8, [-1, 0, -1])):
+            ws = _ws(tsel)
+            for given in (None, torch.full((3,), 77, dtype=torch.int32, device="cuda")):
+                new = tsel.tsel_cache_compact(cache, i32(table), i32(keep), i32(cu), most, starts=i32(starts), new_lens=given,
+                                              dst_table=None if to is None else i32(to), workspace=ws)
+                assert new.tolist() == want and _status(tsel, ws) & tsel.TSEL_DEV_REQUESTS
