@@ -104,6 +104,40 @@ tsel_status check_cache(const void* kp, const void* vp, const void* ke, const vo
   return TSEL_OK;
 }
 
+// Tables of int32 and vectors (one row): rows of `width` entries, `stride` apart.
+struct Ints {
+  const char* name;
+  const void* ptr;
+  int64_t rows, stride, width;
+  Ints(const char* what, const void* p, int64_t n) : name(what), ptr(p), rows(1), stride(n), width(n) {}
+  Ints(const char* what, const void* p, int64_t r, int64_t s, int64_t w) : name(what), ptr(p), rows(r), stride(s), width(w) {}
+  bool none() const { return ptr == nullptr || rows <= 0 || width <= 0; }
+  uintptr_t at(int64_t row) const { return reinterpret_cast<uintptr_t>(ptr) + uintptr_t(row) * uintptr_t(stride) * 4; }
+};
+
+// Whether row r of a, [begin, end), meets a row of b. Rows of b ascend without overlap,
+// so only the last one that begins before `end` can.
+bool meets(uintptr_t begin, uintptr_t end, const Ints& b) {
+  if (b.at(0) >= end) return false;
+  int64_t r = b.rows - 1;
+  if (b.rows > 1) {
+    const int64_t last = int64_t((end - 1 - b.at(0)) / (uintptr_t(b.stride) * 4));
+    if (last < r) r = last;
+  }
+  return b.at(r) + uintptr_t(b.width) * 4 > begin;
+}
+
+// What a call writes shares no memory with what it reads or writes besides.
+tsel_status check_apart(const Ints& a, const Ints& b) {
+  if (a.none() || b.none()) return TSEL_OK;
+  const Ints& few = a.rows <= b.rows ? a : b;
+  const Ints& many = a.rows <= b.rows ? b : a;
+  for (int64_t r = 0; r < few.rows; ++r)
+    if (meets(few.at(r), few.at(r) + uintptr_t(few.width) * 4, many))
+      return fail(TSEL_ERR_INVALID_VALUE, "%s and %s overlap", a.name, b.name);
+  return TSEL_OK;
+}
+
 #define TSEL_TRY(expr)                       \
   do {                                       \
     const tsel_status st_ = (expr);          \
@@ -612,6 +646,13 @@ tsel_status tsel_cache_compact(uint8_t* k_pages, uint8_t* v_pages, uint8_t* k_ex
   if (page_table_stride < pages_per_req || (dst_table != nullptr && dst_table_stride < dst_pages_per_req))
     return fail(TSEL_ERR_INVALID_VALUE, "table strides %lld, %lld", (long long)page_table_stride, (long long)dst_table_stride);
   if (!aligned(dst_table, 4)) return fail(TSEL_ERR_INVALID_VALUE, "dst_table");
+  const Ints lens("new_lens", new_lens, num_req);
+  TSEL_TRY(check_apart(lens, Ints("starts", starts, num_req)));
+  TSEL_TRY(check_apart(lens, Ints("bases", bases, num_req)));
+  TSEL_TRY(check_apart(lens, Ints("keep_idx", keep_idx, total_keep)));
+  TSEL_TRY(check_apart(lens, Ints("cu_keep", cu_keep, int64_t(num_req) + 1)));
+  TSEL_TRY(check_apart(lens, Ints("page_table", page_table, num_req, page_table_stride, pages_per_req)));
+  TSEL_TRY(check_apart(lens, Ints("dst_table", dst_table, num_req, dst_table_stride, dst_pages_per_req)));
   MoveParams p{};
   p.k_pages = k_pages;
   p.v_pages = v_pages;
@@ -686,6 +727,17 @@ static tsel_status pages_params(PagesParams* p, int32_t* refs, int num_pages, in
   return TSEL_OK;
 }
 
+// refs, page_table and lens are written: apart from one another and from `in`.
+static tsel_status pages_apart(const PagesParams& p, const Ints* in, int count) {
+  const Ints out[3] = {Ints("refs", p.refs, p.num_pages), Ints("page_table", p.table, p.rows, p.table_stride, p.width),
+                       Ints("lens", p.lens, p.rows)};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < i; ++j) TSEL_TRY(check_apart(out[j], out[i]));
+    for (int j = 0; j < count; ++j) TSEL_TRY(check_apart(out[i], in[j]));
+  }
+  return TSEL_OK;
+}
+
 tsel_status tsel_cache_resize(int32_t* refs, int num_pages, int page_size, int32_t* page_table,
                               int64_t page_table_stride, int num_rows, int pages_per_row, int32_t* lens,
                               const int32_t* new_lens, void* workspace, size_t workspace_bytes, void* stream_) {
@@ -695,6 +747,9 @@ tsel_status tsel_cache_resize(int32_t* refs, int num_pages, int page_size, int32
   if (num_rows == 0) return TSEL_OK;
   if (new_lens == nullptr || !aligned(new_lens, 4)) return fail(TSEL_ERR_INVALID_VALUE, "new_lens");
   p.new_lens = new_lens;
+  // lens themselves ask for what is there
+  const Ints in("new_lens", new_lens == lens ? nullptr : new_lens, num_rows);
+  TSEL_TRY(pages_apart(p, &in, 1));
   const cudaError_t e = launch_resize(p, static_cast<cudaStream_t>(stream_));
   return e == cudaSuccess ? TSEL_OK : cuda_fail(e, "cache resize launch");
 }
@@ -716,6 +771,8 @@ tsel_status tsel_cache_fork(uint8_t* k_pages, uint8_t* v_pages, uint8_t* k_exps,
   p.parents = parents;
   p.children = children;
   p.n = num_forks;
+  const Ints in[2] = {Ints("parents", parents, num_forks), Ints("children", children, num_forks)};
+  TSEL_TRY(pages_apart(p, in, 2));
   p.k_pages = k_pages;
   p.v_pages = v_pages;
   p.k_exps = k_exps;

@@ -572,7 +572,8 @@ TSEL_API tsel_status tsel_cache_read(const uint8_t* k_pages, const uint8_t* v_pa
  *               kept tokens do not fit its destination's pages, sets
  *               TSEL_DEV_REQUESTS and is left as it is; its new_lens is -1, with
  *               which tsel_cache_resize leaves a row alone.
- * new_lens      int32 [num_req] device or NULL; not starts itself.
+ * new_lens      int32 [num_req] device or NULL; shares no memory with the other
+ *               arguments (TSEL_ERR_INVALID_VALUE).
  * workspace     >= tsel_cache_workspace_size() bytes (status).
  * Pages outside the cache set TSEL_DEV_PAGES; their tokens are skipped. Rows that
  * are no destination keep what they hold.
@@ -608,7 +609,8 @@ TSEL_API size_t tsel_cache_resize_workspace_size(int num_rows, int pages_per_row
  * when the call began, sets TSEL_DEV_REQUESTS, and the row stays as it is. A fork
  * of it copies the rows in use; that row can grow.
  *
- * refs        int32 [num_pages] device.
+ * refs        int32 [num_pages] device. refs, page_table, lens and new_lens share no
+ *             memory (TSEL_ERR_INVALID_VALUE; new_lens may be lens itself).
  * page_table  int32 device, row r at page_table + r * page_table_stride,
  *             pages_per_row entries; num_rows * pages_per_row at most 2^31 - 1.
  * lens        int32 [num_rows] device, in and out; new_lens int32 [num_rows]
@@ -635,7 +637,8 @@ TSEL_API tsel_status tsel_cache_resize(int32_t* refs, int num_pages, int page_si
  *             ascending (each above all before it), of length 0, none of them a
  *             parent in the same call (else TSEL_DEV_REQUESTS, and that child is
  *             left as it is).
- *             num_forks at most num_rows.
+ *             num_forks at most num_rows. Neither shares memory with refs,
+ *             page_table or lens.
  * A child for which no page is free is left as it is (TSEL_DEV_PAGES); so is one
  * whose parent's last page is outside the cache. Other pages outside the cache are
  * noted in the child's row and flagged.

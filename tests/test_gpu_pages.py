@@ -405,3 +405,27 @@ def test_lengths_of_refused_requests(tsel):
                 new = tsel.tsel_cache_compact(cache, i32(table), i32(keep), i32(cu), most, starts=i32(starts), new_lens=given,
                                               dst_table=None if to is None else i32(to), workspace=ws)
                 assert new.tolist() == want and _status(tsel, ws) & tsel.TSEL_DEV_REQUESTS
+
+
+def test_overlapping_lengths(tsel):
+    """Results among the inputs are refused; lengths that stay, and tensors side by side, are taken."""
+    rng = np.random.default_rng(25)
+    cache, host = _cache(tsel, rng, 12, 16, 1, 64)
+    both = i32([3, 4, 5, 6])
+    table = i32(np.arange(12).reshape(3, 4))
+    for kw in (dict(starts=both[:3], new_lens=both[1:]), dict(bases=both[1:], new_lens=both[1:]), dict(bases=both[1:], new_lens=both[:3]),
+               dict(new_lens=table[1, :3])):
+        with pytest.raises(tsel.TselError, match="overlap"):
+            tsel.tsel_cache_compact(cache, table, i32([0, 1, 2]), i32([0, 1, 2, 3]), 1, **kw)
+    buf = i32([0] * 6)
+    new = tsel.tsel_cache_compact(cache, table, i32([0, 0, 0]), i32([0, 1, 2, 3]), 1, starts=buf[:3], new_lens=buf[3:])
+    assert new.tolist() == [1, 1, 1]
+    _same(cache, host)
+    # a table whose rows leave room for the lengths between them
+    state = torch.zeros(3, 8, dtype=torch.int32, device="cuda")
+    state[:, :4] = table
+    new = tsel.tsel_cache_compact(cache, state[:, :4], i32([0, 0, 0]), i32([0, 1, 2, 3]), 1, new_lens=state[1, 4:7])
+    assert new.tolist() == [1, 1, 1] and torch.equal(state[:, :4], table)
+    refs, lens = i32([1] * 12), i32([64, 64, 64])
+    tsel.tsel_cache_resize(refs, table, lens, lens, 16)      # every row keeps its length
+    assert lens.tolist() == [64] * 3 and refs.tolist() == [1] * 12

@@ -268,3 +268,22 @@ def test_pages_oracle_shared_ends():
     assert PO.shared_end(refs, table, lens, [12, 7, 4], 4).tolist() == [False, True, False]
     assert PO.shared_end(refs, table, lens, [4, 6, -1], 4).tolist() == [False, False, False]
     assert PO.resize(refs, table, lens, [-1, 12, 4], 4) and lens.tolist() == [9, 6, 4] and refs.tolist() == [2, 2, 1, 1, 1, 0]
+
+
+def test_overlapping_page_arguments(lib):
+    """What a call writes and what it reads or also writes must not share memory. Every call here is
+    refused before a launch."""
+    def refused(call, **over):
+        assert call(lib, **over) == 1 and b"overlap" in lib.tsel_last_error(), over
+    # [3 rows of 4] at 4096, vectors of 2 or 3 elsewhere
+    c = dict(t=4096, ki=8192, cu=12288, st=16384, ba=20480, dt=24576, ds=4, dw=4)
+    for at in (16384, 16384 + 4, 16384 - 4, 20480, 20480 + 4, 8192 + 12, 8192 - 4, 12288, 12288 + 8, 4096, 4096 + 28, 24576 + 16):
+        refused(_compact, **c, nl=at)
+    refused(_compact, **{**c, "ts": 16, "tw": 4}, nl=4096 + 64 + 12)          # the last entry of the second row
+    r = dict(refs=4096, t=8192, lens=12288, new=16384)
+    for over in (dict(new=12288 + 4), dict(new=12288 - 8), dict(new=4096 + 28), dict(new=8192 + 44), dict(lens=4096), dict(lens=8192 + 16),
+                 dict(t=4096 + 28)):
+        refused(_resize, **{**r, **over})
+    f = dict(refs=4096, t=8192, lens=12288, par=16384, kid=20480)
+    for over in (dict(par=12288 + 8), dict(kid=12288), dict(par=4096 - 4), dict(kid=8192 + 44), dict(lens=4096 + 28), dict(t=12288 + 8), dict(refs=8192 + 40)):
+        refused(_fork, **{**f, **over})
