@@ -265,8 +265,9 @@ def test_fork_refuses_and_runs_out(tsel):
 
 
 def _dev_state(tsel, rng, rows, width, pages, page, lens):
-    """Rows with pages of their own, here and on the device, and a workspace."""
-    host = list(_state(rng, rows, width, pages, page, lens))
+    """Rows with pages of their own (counts, table, lengths), here and on the device, and a workspace."""
+    table, refs, lens = _state(rng, rows, width, pages, page, lens)
+    host = [refs, table, lens]
     return host, [i32(x) for x in host], _ws(tsel, tsel.tsel_cache_resize_workspace_size(rows, width))
 
 
@@ -307,7 +308,7 @@ def test_fork_lists_out_of_order_in_many_rows(tsel):
     children = np.sort(rng.permutation(np.arange(50, rows))[:3500]).astype(np.int32)
     parents = rng.integers(0, 50, 3500).astype(np.int32)
     some = rng.permutation(3500)[:60]
-    children[some[:30]] = rng.integers(-3, rows + 1, 30)     # out of order, some of them rows that hold tokens
+    children[some[:30]] += rng.integers(-60, 60, 30).astype(np.int32)   # out of order; an early one may reach rows that hold tokens
     parents[some[30:]] = rng.integers(-1, rows + 1, 30)      # some of them children
     good = np.asarray(O.good_forks(host[2], parents, children))
     assert 30 < good.sum() < 3500
