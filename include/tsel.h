@@ -559,8 +559,10 @@ TSEL_API tsel_status tsel_cache_read(const uint8_t* k_pages, const uint8_t* v_pa
  * page_table    int32 device, row r at page_table + r * page_table_stride,
  *               pages_per_req pages in order. The pages of a request must differ.
  * dst_table     the same for the destinations, which must be no page that the
- *               call reads; NULL: in place, the pages of page_table. In place
- *               those pages must be the request's own (tsel_cache_fork shares them).
+ *               call reads; NULL: in place, the pages of page_table. In place the
+ *               pages that tokens move into must be the request's own. Pages that
+ *               others hold too (tsel_cache_fork) may hold tokens that stay where
+ *               they are or move out.
  * starts, bases int32 [num_req] device, NULL for zeros. E.g. starts = the length
  *               without the drafted tokens and keep_idx = the accepted nodes; or
  *               bases = req_tok_offsets with the outputs of tsel_select_topk.
