@@ -32,7 +32,8 @@ constexpr int kAttNarrowRows = 32;
 // Trees without a prefix take it up to more rows: 16 requests of up to 61 nodes
 // over up to 4,000 keys, 16 KV heads of 80, one query head each, take 95 us, in the
 // wide kernel 103. (Beside a prefix, which takes the wide kernel's launch, 32
-// requests of up to 64 rows take 236 us that way, in the wide kernel 219.)
+// requests of up to 64 rows take 236 us that way, in the wide kernel 219.) Between 33
+// and 64 rows only these shapes were timed.
 constexpr int kAttNarrowRowsTree = 64;
 constexpr int kAttNarrowRowsLong = 16;         // past
 constexpr int kAttNarrowKeys = 16384;          // this many keys of few requests

@@ -60,7 +60,9 @@ struct PromptPlan {
 };
 
 // Keys are cut into chunks only while the (segment, KV head, row block) units
-// leave SMs idle. `base` is a lower estimate of the units that have rows.
+// leave SMs idle. `base` estimates the units that have rows as if every segment had
+// some and total_q were used up, so a batch padded with many empty segments is cut
+// less than its lengths would allow.
 inline PromptPlan prompt_plan(int seg, int Tq, int max_q, int max_k, int H, int Hkv, int d) {
   PromptPlan a{};
   a.G = H / Hkv;

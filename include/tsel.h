@@ -619,7 +619,8 @@ TSEL_API size_t tsel_cache_resize_workspace_size(int num_rows, int pages_per_row
  *             device. Lengths past the row's pages set TSEL_DEV_REQUESTS; the row
  *             stays as it is.
  * workspace   >= tsel_cache_resize_workspace_size(num_rows, pages_per_row).
- * Deterministic; one CTA, for the pages that change hands between steps.
+ * Deterministic. Two launches: one CTA gives pages out, a CTA for each row takes
+ * them back; meant for the pages that change hands between steps.
  */
 TSEL_API tsel_status tsel_cache_resize(int32_t* refs, int num_pages, int page_size, int32_t* page_table,
                                        int64_t page_table_stride, int num_rows, int pages_per_row, int32_t* lens,
@@ -812,7 +813,8 @@ TSEL_API size_t tsel_prompt_attention_workspace_size(int num_seg, int total_q, i
  * Results are deterministic. Precision: products of the inputs as they are,
  * probabilities rounded to dtype (fp16: on a grid of 2^-30 below 2^-20 of a
  * reference that the row's largest may pass by 2^9), sums and statistics in
- * fp32.
+ * fp32. Sums hold V times probabilities of up to 2^15 of that reference before
+ * they are divided: finite V past 2^88 (bf16) may overflow them.
  */
 TSEL_API tsel_status tsel_prompt_attention(
     const void* q, int64_t q_row_stride, const void* k, int64_t k_row_stride, const void* v,
