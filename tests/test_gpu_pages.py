@@ -430,3 +430,72 @@ def test_overlapping_lengths(tsel):
     refs, lens = i32([1] * 12), i32([64, 64, 64])
     tsel.tsel_cache_resize(refs, table, lens, lens, 16)      # every row keeps its length
     assert lens.tolist() == [64] * 3 and refs.tolist() == [1] * 12
+
+
+def test_pools_past_32_bits_of_bytes(tsel):
+    """Pages whose bytes lie past 2^32: moved in place and elsewhere, copied by a fork, given out and back."""
+    rng = np.random.default_rng(26)
+    page, Hkv, d, pages = 128, 8, 128, 40000                 # 5.2 GB of codes in K and in V
+    free = torch.cuda.mem_get_info()[0]
+    if free < 14 << 30:
+        pytest.skip("needs 14 GB")
+    cache = tsel.TselCache(*[torch.zeros(pages, Hkv, page, *x, dtype=torch.uint8, device="cuda") for x in ([d], [d], [], [])])
+    rows, width, lens = 3, 4, [500, 300, 0]
+    order = (pages - 1 - rng.permutation(12)).astype(np.int32)
+    first = int(order.min())                                 # the last twelve pages, from `first` on
+    host = [rng.integers(0, 256, (12, Hkv, page, *x), dtype=np.uint8) for x in ([d], [d], [], [])]
+    for t, a in zip(cache, host):
+        t[first:] = torch.from_numpy(a).cuda()
+    table = np.full((rows, width), -1, np.int32)
+    table[0], table[1, :3] = order[:4], order[4:7]
+    refs = np.ones(pages, np.int32)                          # the free pages lie at the end
+    refs[order[7:]] = 0
+    state = [refs, table, np.asarray(lens, np.int32)]
+    dev = [i32(x) for x in state]
+    small = lambda: [refs[first:], np.where(table < 0, table, table - first), state[2]]   # noqa: E731
+    ws = _ws(tsel, tsel.tsel_cache_resize_workspace_size(rows, width))
+
+    def check():
+        assert _status(tsel, ws) == 0
+        _equal(dev, state)
+        for t, a in zip(cache, host):
+            assert np.array_equal(t[first:].cpu().numpy(), a)
+            assert not bool(t[:first:997].any())
+    # in place, and to two of the free pages
+    keep, cu = np.sort(rng.permutation(500)[:333]).astype(np.int32), [0, 333]
+    tsel.tsel_cache_compact(cache, dev[1][:1], i32(keep), i32(cu), 333, workspace=ws)
+    O.compact(host, small()[1][:1], [0], [0], keep, cu)
+    check()
+    keep, cu, to = np.sort(rng.permutation(300)[:200]).astype(np.int32), [0, 200], order[None, 8:10]
+    tsel.tsel_cache_compact(cache, dev[1][1:2], i32(keep), i32(cu), 200, dst_table=i32(to), workspace=ws)
+    O.compact(host, small()[1][1:2], [0], [0], keep, cu, to - first)
+    check()
+    tsel.tsel_cache_fork(cache, *dev, i32([0]), i32([2]), workspace=ws)
+    s = small()
+    O.fork(host, *s, [0], [2])
+    table[:] = np.where(s[1] < 0, s[1], s[1] + first)
+    check()
+    for new in ([-1, 0, 512], [0, -1, 0]):
+        tsel.tsel_cache_resize(*dev, i32(new), page, workspace=ws)
+        assert O.resize(*state, new, page)
+        check()
+
+
+@pytest.mark.parametrize("Hkv,d,page", [(4, 112, 32), (1, 112, 16), (8, 80, 128), (3, 96, 64)])
+def test_compact_long_and_short_requests_in_place(tsel, Hkv, d, page):
+    """Requests of many chunks beside ones that stop in their first, second or third."""
+    rng = np.random.default_rng(27)
+    counts = [4000, 3, 1700, 0, 130, 900, 2600, 64]
+    R, span = len(counts), 5000
+    starts = np.asarray([7 * r for r in range(R)], np.int32)
+    keep = np.concatenate([np.sort(rng.permutation(span if r % 2 == 0 else 2 * n + 1)[:n]) for r, n in enumerate(counts)]).astype(np.int32)
+    cu = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    width = -(-(span + 7 * R) // page)
+    table = rng.permutation(R * width).astype(np.int32).reshape(R, width)
+    cache, host = _cache(tsel, rng, R * width, page, Hkv, d)
+    ws = _ws(tsel)
+    for _ in range(2):                                       # the second call moves what the first one left behind
+        lens = tsel.tsel_cache_compact(cache, i32(table), i32(keep), i32(cu), max(counts), starts=i32(starts), workspace=ws)
+        assert tsel.tsel_read_device_status(ws) == 0
+        assert np.array_equal(lens.cpu().numpy(), O.compact(host, table, starts, [0] * R, keep, cu))
+        _same(cache, host)
