@@ -939,7 +939,9 @@ def tsel_cache_resize(refs: torch.Tensor, page_table: torch.Tensor, lens: torch.
     """Gives pages to the rows of page_table (int32 [rows, pages]) that grow from lens to
     new_lens (int32 [rows], negative: left alone) and takes them back from those that
     shrink. refs int32 [num_pages] counts the rows that hold a page; the lowest free
-    pages go to rows in order. page_table, refs and lens are written."""
+    pages go to rows in order. A row that ends inside a page which others hold too
+    (after tsel_cache_fork) does not grow from there; a fork of it does. page_table, refs
+    and lens are written."""
     index = refs.get_device()
     if index < 0:
         raise TypeError("refs must be a CUDA torch.int32 tensor")
