@@ -809,7 +809,7 @@ TSEL_API size_t tsel_prompt_attention_workspace_size(int num_seg, int total_q, i
  * unspecified; nothing out of range is touched. Keys that a row does not see
  * never reach it, infinities and NaN among them. An infinity or NaN in V makes
  * an infinity or NaN of its column in the rows that see the key, however small its
- * weight there (but not with a logit of -inf, which is no weight at all).
+ * weight there; at a logit of -inf, which is no weight at all, it may.
  * Results are deterministic. Precision: products of the inputs as they are,
  * probabilities rounded to dtype (fp16: on a grid of 2^-30 below 2^-20 of a
  * reference that the row's largest may pass by 2^9), sums and statistics in
